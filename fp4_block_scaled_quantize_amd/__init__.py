@@ -6,11 +6,13 @@ device memory and the current stream.  There is no fallback: if libfp4.so is
 missing or fails to load, every call raises.
 
 Names follow the C ABI: fp4_quantize, fp4_quantize_transposed, fp4_quantize_both, fp4_dequantize, fp4_gemm, fp4_wo_gemm,
-plus the amax state (per-tensor maximum refreshed every N calls,
+fp4_wo_gemm_lora, fp4_lora_apply, fp4_lora_backward, fp4_token_logprobs, fp4_token_logprobs_backward,
+fp4_residual_norm, fp4_residual_norm_backward, plus the amax state (per-tensor maximum refreshed every N calls,
 ue5m3-fp4-pretraining "Что сделали").
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -43,6 +45,19 @@ class Fp4TensorC(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("fmt", Fp4Format)]
 
 
+class Fp4LoraBankC(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("adapters", ctypes.c_int64), ("rank", ctypes.c_int64), ("k", ctypes.c_int64), ("n", ctypes.c_int64)]
+
+
+class Fp4NormC(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("res", ctypes.c_void_p), ("ld_res", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("w_pre", ctypes.c_void_p),
+                ("w_post", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("alpha", ctypes.c_float),
+                ("eps", ctypes.c_float), ("x_dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32)]
+
+
 class Fp4Error(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -61,7 +76,8 @@ def lib():
         raise RuntimeError(f"{LIB_PATH} is not built; run __graft_entry__.build() first")
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, u64, u32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_uint32
-    T = ctypes.POINTER(Fp4TensorC)
+    f32 = ctypes.c_float
+    T, LB, NA = ctypes.POINTER(Fp4TensorC), ctypes.POINTER(Fp4LoraBankC), ctypes.POINTER(Fp4NormC)
     sig = {
         "fp4_version": (i32, []),
         "fp4_status_string": (ctypes.c_char_p, [i32]),
@@ -79,6 +95,16 @@ def lib():
         "fp4_dequantize": (i32, [T, vp, i32, i64, vp]),
         "fp4_gemm": (i32, [T, T, vp, i64, vp]),
         "fp4_wo_gemm": (i32, [vp, i64, i64, T, vp, i64, vp]),
+        "fp4_lora_workspace": (i64, [i32, i64, i64, i64, i64, i64]),
+        "fp4_lora_apply": (i32, [vp, i64, i64, LB, vp, vp, i64, vp, i64, vp, vp, i64, vp]),
+        "fp4_lora_backward": (i32, [vp, i64, vp, i64, i64, vp, LB, vp, vp, i64, vp, i64, vp, vp, i32, vp, i64, vp]),
+        "fp4_wo_gemm_lora": (i32, [vp, i64, i64, T, LB, vp, vp, i64, vp, i64, vp]),
+        "fp4_token_logprobs_workspace": (i64, [i64, i64, i32]),
+        "fp4_token_logprobs": (i32, [vp, i32, i64, i64, i64, vp, f32, i32, vp, vp, vp, vp, vp, vp, i64, vp]),
+        "fp4_token_logprobs_backward": (i32, [vp, i32, i64, i64, i64, vp, f32, vp, vp, vp, vp, vp, i64, vp]),
+        "fp4_residual_norm": (i32, [NA, vp, i64, vp, i64, vp, vp]),
+        "fp4_residual_norm_workspace": (i64, [i64, i64, i32]),
+        "fp4_residual_norm_backward": (i32, [NA, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -422,6 +448,313 @@ def fp4_wo_gemm(x: torch.Tensor, w: QTensor, out: torch.Tensor | None = None, st
     return out
 
 
+# ---------------------------------------------------------------------------
+# Training and serving of low-rank adapters over quantized weights.  Outputs
+# and workspaces that these calls allocate belong to the call's stream, so
+# that memory freed here is not handed to another stream's work while the
+# call is still queued.
+# ---------------------------------------------------------------------------
+_LORA_APPLY, _LORA_BACKWARD, _LORA_WO_GEMM = range(3)
+
+
+def _allocating(stream, device: torch.device):
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device)
+    return torch.cuda.stream(stream)
+
+
+def _space(nbytes: int, device: torch.device, what: str) -> torch.Tensor | None:
+    """A workspace of `nbytes` (a negative number is a status)."""
+    if nbytes < 0:
+        _check(nbytes, what)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _is_rows(t, cols: int | None = None, rows: int | None = None) -> bool:
+    """A 2-D tensor whose rows are dense."""
+    return (t.dim() == 2 and (t.stride(1) == 1 or t.numel() == 0 or t.shape[1] == 1)
+            and (cols is None or t.shape[1] == cols) and (rows is None or t.shape[0] == rows))
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride; a single row's is its length, whatever torch keeps there."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _is_vector(t, n: int, dtype: torch.dtype) -> bool:
+    return t.dim() == 1 and t.shape[0] == n and t.dtype == dtype and (n < 2 or t.stride(0) == 1)
+
+
+@dataclass
+class LoraBank:
+    """Low-rank adapters of one projection: a [adapters, rank, K] and b
+    [adapters, N, rank] in bf16, scale [adapters] in fp32.  rank is a multiple
+    of 8 up to 128 (pad a smaller one with zeros)."""
+    a: torch.Tensor
+    b: torch.Tensor
+    scale: torch.Tensor
+
+    def c(self) -> Fp4LoraBankC:
+        a, b, s = self.a, self.b, self.scale
+        if a.dim() != 3 or b.dim() != 3 or s.dim() != 1 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2] \
+                or s.shape[0] != a.shape[0]:
+            raise ValueError("LoraBank: a is [adapters, rank, K], b is [adapters, N, rank], scale is [adapters]")
+        if a.dtype != torch.bfloat16 or b.dtype != torch.bfloat16 or s.dtype != torch.float32:
+            raise ValueError("LoraBank: a and b must be bfloat16, scale float32")
+        if not (a.is_contiguous() and b.is_contiguous() and s.is_contiguous()):
+            raise ValueError("LoraBank buffers must be contiguous")
+        return Fp4LoraBankC(a.data_ptr(), b.data_ptr(), s.data_ptr(), a.shape[0], a.shape[1], a.shape[2], b.shape[1])
+
+
+def _lora_rows(what: str, x: torch.Tensor, slots: torch.Tensor, k: int):
+    if x.dtype != torch.bfloat16 or not _is_rows(x, k):
+        raise ValueError(f"{what}: expected a bf16 [rows, {k}] tensor with unit column stride")
+    if not _is_vector(slots, x.shape[0], torch.int32):
+        raise ValueError(f"{what}: slots must be int32 [{x.shape[0]}], one adapter (or -1) for each row")
+
+
+def fp4_wo_gemm_lora(x: torch.Tensor, w: QTensor, bank: LoraBank, slots: torch.Tensor,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """fp4_wo_gemm plus each row's adapter: Y = X W^T + s_l (X A_l^T) B_l^T
+    with l = slots[row] (outside the bank: none), for at most 16 rows."""
+    _lora_rows("fp4_wo_gemm_lora", x, slots, w.cols)
+    dev = _on_device("fp4_wo_gemm_lora", x, w.q, w.scales, w.tensor_scale, bank.a, bank.b, bank.scale, slots,
+                     *(() if out is None else (out,)))
+    m, n, L = x.shape[0], w.rows, lib()
+    tw, tb = w.c(), bank.c()
+    with _allocating(stream, dev):
+        if out is None:
+            out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_dense_out(out, (m, n), (torch.bfloat16,), "fp4_wo_gemm_lora")
+        ws = _space(L.fp4_lora_workspace(_LORA_WO_GEMM, m, tb.n, tb.k, tb.rank, tb.adapters), dev, "fp4_wo_gemm_lora")
+        st = L.fp4_wo_gemm_lora(x.data_ptr(), _ld(x), m, ctypes.byref(tw), ctypes.byref(tb), slots.data_ptr(),
+                                out.data_ptr(), _ld(out), _ptr(ws), 0 if ws is None else ws.numel(),
+                                _stream(stream, dev))
+    _check(st, "fp4_wo_gemm_lora")
+    return out
+
+
+def fp4_lora_apply(x: torch.Tensor, bank: LoraBank, slots: torch.Tensor, base: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, stream=None) -> tuple:
+    """(y, t): y = base + s_l (x A_l^T) B_l^T for each row's adapter l =
+    slots[row], and t = x A_l^T (fp32 [rows, rank]), which fp4_lora_backward
+    takes.  base is the shared projection's output (None: zero); out may be
+    base."""
+    tb = bank.c()
+    _lora_rows("fp4_lora_apply", x, slots, tb.k)
+    m = x.shape[0]
+    dev = _on_device("fp4_lora_apply", x, bank.a, bank.b, bank.scale, slots,
+                     *(t for t in (base, out) if t is not None))
+    if base is not None:
+        _check_dense_out(base, (m, tb.n), (torch.bfloat16,), "fp4_lora_apply: base")
+    L = lib()
+    with _allocating(stream, dev):
+        if out is None:
+            out = torch.empty((m, tb.n), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_dense_out(out, (m, tb.n), (torch.bfloat16,), "fp4_lora_apply")
+        t = torch.empty((m, tb.rank), dtype=torch.float32, device=dev)
+        ws = _space(L.fp4_lora_workspace(_LORA_APPLY, m, tb.n, tb.k, tb.rank, tb.adapters), dev, "fp4_lora_apply")
+        st = L.fp4_lora_apply(x.data_ptr(), _ld(x), m, ctypes.byref(tb), slots.data_ptr(), _ptr(base),
+                              0 if base is None else _ld(base), out.data_ptr(), _ld(out), t.data_ptr(), _ptr(ws),
+                              0 if ws is None else ws.numel(), _stream(stream, dev))
+    _check(st, "fp4_lora_apply")
+    return out, t
+
+
+def fp4_lora_backward(dy: torch.Tensor, x: torch.Tensor, t: torch.Tensor, bank: LoraBank, slots: torch.Tensor,
+                      dx_base: torch.Tensor | None = None, grad_dtype=torch.float32, dx: torch.Tensor | None = None,
+                      stream=None) -> tuple:
+    """(dx, da, db) of fp4_lora_apply for the gradient dy [rows, N] of its y.
+    t is fp4_lora_apply's; dx_base the gradient that reaches x through the
+    shared projection (None: zero; dx may be dx_base); da and db have the
+    bank's shapes in grad_dtype."""
+    tb = bank.c()
+    _lora_rows("fp4_lora_backward", x, slots, tb.k)
+    m = x.shape[0]
+    if dy.dtype != torch.bfloat16 or not _is_rows(dy, tb.n, m):
+        raise ValueError(f"fp4_lora_backward: dy must be bf16 [{m}, {tb.n}] with unit column stride")
+    if t.dtype != torch.float32 or tuple(t.shape) != (m, tb.rank) or not t.is_contiguous():
+        raise ValueError(f"fp4_lora_backward: t must be the dense fp32 [{m}, {tb.rank}] of fp4_lora_apply")
+    if grad_dtype not in DTYPE:
+        raise ValueError("fp4_lora_backward: grad_dtype must be float32 or bfloat16")
+    dev = _on_device("fp4_lora_backward", dy, x, t, bank.a, bank.b, bank.scale, slots,
+                     *(v for v in (dx_base, dx) if v is not None))
+    if dx_base is not None:
+        _check_dense_out(dx_base, (m, tb.k), (torch.bfloat16,), "fp4_lora_backward: dx_base")
+    L = lib()
+    with _allocating(stream, dev):
+        if dx is None:
+            dx = torch.empty((m, tb.k), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_dense_out(dx, (m, tb.k), (torch.bfloat16,), "fp4_lora_backward")
+        da = torch.empty(bank.a.shape, dtype=grad_dtype, device=dev)
+        db = torch.empty(bank.b.shape, dtype=grad_dtype, device=dev)
+        ws = _space(L.fp4_lora_workspace(_LORA_BACKWARD, m, tb.n, tb.k, tb.rank, tb.adapters), dev, "fp4_lora_backward")
+        st = L.fp4_lora_backward(dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), m, t.data_ptr(), ctypes.byref(tb),
+                                 slots.data_ptr(), _ptr(dx_base), 0 if dx_base is None else _ld(dx_base),
+                                 dx.data_ptr(), _ld(dx), da.data_ptr(), db.data_ptr(), DTYPE[grad_dtype], _ptr(ws),
+                                 0 if ws is None else ws.numel(), _stream(stream, dev))
+    _check(st, "fp4_lora_backward")
+    return dx, da, db
+
+
+@dataclass
+class TokenLogprobs:
+    """logprob (None without tokens) and entropy [rows]; top_ids (int32) and
+    top_logprobs [rows, top], largest first (None for top = 0); stats [rows,
+    2] for the backward call."""
+    logprob: torch.Tensor | None
+    entropy: torch.Tensor
+    stats: torch.Tensor
+    top_ids: torch.Tensor | None
+    top_logprobs: torch.Tensor | None
+
+
+def _logits(what: str, logits: torch.Tensor, tokens: torch.Tensor | None):
+    if logits.dtype not in DTYPE or not _is_rows(logits) or logits.shape[1] < 1:
+        raise ValueError(f"{what}: logits must be a float32 or bfloat16 [rows, vocab] tensor with unit column stride")
+    if tokens is not None and not _is_vector(tokens, logits.shape[0], torch.int64):
+        raise ValueError(f"{what}: tokens must be int64 [{logits.shape[0]}]")
+
+
+def fp4_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, temperature: float = 1.0,
+                       top: int = 0, stream=None) -> TokenLogprobs:
+    """Log probability of each row's token under softmax(logits /
+    temperature) (0 for a token outside the vocabulary, such as -100), the
+    entropy, and the `top` (up to 32) most probable tokens."""
+    _logits("fp4_token_logprobs", logits, tokens)
+    dev = _on_device("fp4_token_logprobs", logits, *(() if tokens is None else (tokens,)))
+    n, v = logits.shape
+    L = lib()
+    with _allocating(stream, dev):
+        ws = _space(L.fp4_token_logprobs_workspace(n, v, top), dev, "fp4_token_logprobs")
+        logprob = torch.empty(n, dtype=torch.float32, device=dev) if tokens is not None else None
+        entropy = torch.empty(n, dtype=torch.float32, device=dev)
+        stats = torch.empty((n, 2), dtype=torch.float32, device=dev)
+        ids = torch.empty((n, top), dtype=torch.int32, device=dev) if top else None
+        best = torch.empty((n, top), dtype=torch.float32, device=dev) if top else None
+        st = L.fp4_token_logprobs(logits.data_ptr(), DTYPE[logits.dtype], _ld(logits), n, v, _ptr(tokens), temperature,
+                                  top, _ptr(logprob), entropy.data_ptr(), stats.data_ptr(), _ptr(ids), _ptr(best),
+                                  _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream, dev))
+    _check(st, "fp4_token_logprobs")
+    return TokenLogprobs(logprob, entropy, stats, ids, best)
+
+
+def fp4_token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor | None, saved: TokenLogprobs,
+                                grad_logprob: torch.Tensor | None = None, grad_entropy: torch.Tensor | None = None,
+                                temperature: float = 1.0, out: torch.Tensor | None = None,
+                                stream=None) -> torch.Tensor:
+    """The gradient of the logits for the gradients of logprob and entropy
+    (fp32 [rows]; None: zero).  logits, tokens and temperature are the forward
+    call's, saved its result; out may be the logits."""
+    what = "fp4_token_logprobs_backward"
+    _logits(what, logits, tokens)
+    n, v = logits.shape
+    for g in (grad_logprob, grad_entropy):
+        if g is not None and not _is_vector(g, n, torch.float32):
+            raise ValueError(f"{what}: gradients must be float32 [{n}]")
+    if grad_logprob is not None and tokens is None:
+        raise ValueError(f"{what}: grad_logprob needs the tokens")
+    if not _is_vector(saved.entropy, n, torch.float32) or tuple(saved.stats.shape) != (n, 2) \
+            or saved.stats.dtype != torch.float32 or not saved.stats.is_contiguous():
+        raise ValueError(f"{what}: saved is not the result of a forward call on these logits")
+    dev = _on_device(what, logits, saved.entropy, saved.stats,
+                     *(t for t in (tokens, grad_logprob, grad_entropy, out) if t is not None))
+    with _allocating(stream, dev):
+        if out is None:
+            out = torch.empty((n, v), dtype=logits.dtype, device=dev)
+        elif out.dtype != logits.dtype or not _is_rows(out, v, n):
+            raise ValueError(f"{what}: out must be [{n}, {v}] of the logits' dtype with unit column stride")
+        st = lib().fp4_token_logprobs_backward(logits.data_ptr(), DTYPE[logits.dtype], _ld(logits), n, v, _ptr(tokens),
+                                               temperature, saved.entropy.data_ptr(), saved.stats.data_ptr(),
+                                               _ptr(grad_logprob), _ptr(grad_entropy), out.data_ptr(), _ld(out),
+                                               _stream(stream, dev))
+    _check(st, what)
+    return out
+
+
+def _norm_args(what: str, x, res, w_pre, w_post, gate, alpha, eps) -> Fp4NormC:
+    if x.dtype not in DTYPE or not _is_rows(x) or res.dtype not in DTYPE or not _is_rows(res, x.shape[1], x.shape[0]):
+        raise ValueError(f"{what}: x and res must be float32 or bfloat16 [rows, cols] tensors with unit column stride")
+    m, c = x.shape
+    if w_pre.dtype not in DTYPE or not _is_vector(w_pre, c, w_pre.dtype) or \
+            (w_post is not None and not _is_vector(w_post, c, w_pre.dtype)):
+        raise ValueError(f"{what}: weights must be dense [{c}] vectors of one dtype, float32 or bfloat16")
+    if gate is not None and not _is_vector(gate, m, torch.float32):
+        raise ValueError(f"{what}: gate must be float32 [{m}]")
+    return Fp4NormC(x.data_ptr(), _ld(x), res.data_ptr(), _ld(res), m, c, w_pre.data_ptr(), _ptr(w_post), _ptr(gate),
+                    alpha, eps, DTYPE[x.dtype], DTYPE[res.dtype], DTYPE[w_pre.dtype])
+
+
+def fp4_residual_norm(x: torch.Tensor, res: torch.Tensor, w_pre: torch.Tensor, w_post: torch.Tensor | None = None,
+                      gate: torch.Tensor | None = None, alpha: float = 1.0, eps: float = 1e-6, stream=None) -> tuple:
+    """(h, n, stats): h = alpha res + gate RMSNorm(x) w_post (x itself without
+    w_post; gate fp32 [rows], 1 without) in res' dtype and n = RMSNorm(h)
+    w_pre in x's; stats goes to fp4_residual_norm_backward."""
+    args = _norm_args("fp4_residual_norm", x, res, w_pre, w_post, gate, alpha, eps)
+    dev = _on_device("fp4_residual_norm", x, res, w_pre, *(t for t in (w_post, gate) if t is not None))
+    m, c = x.shape
+    with _allocating(stream, dev):
+        h = torch.empty((m, c), dtype=res.dtype, device=dev)
+        n = torch.empty((m, c), dtype=x.dtype, device=dev)
+        stats = torch.empty((m, 2), dtype=torch.float32, device=dev)
+        st = lib().fp4_residual_norm(ctypes.byref(args), h.data_ptr(), c, n.data_ptr(), c, stats.data_ptr(),
+                                     _stream(stream, dev))
+    _check(st, "fp4_residual_norm")
+    return h, n, stats
+
+
+@dataclass
+class ResidualNormGrads:
+    """dx and dres in the dtypes of x and res; dw_pre, dw_post [cols] and
+    dgate [rows] in fp32 (None where the call had no w_post, gate)."""
+    dx: torch.Tensor
+    dres: torch.Tensor
+    dw_pre: torch.Tensor
+    dw_post: torch.Tensor | None
+    dgate: torch.Tensor | None
+
+
+def fp4_residual_norm_backward(dn: torch.Tensor | None, dh: torch.Tensor | None, x: torch.Tensor, res: torch.Tensor,
+                               w_pre: torch.Tensor, stats: torch.Tensor, w_post: torch.Tensor | None = None,
+                               gate: torch.Tensor | None = None, alpha: float = 1.0, stream=None) -> ResidualNormGrads:
+    """Gradients of fp4_residual_norm for the gradients dn of n and dh of h
+    (None: zero); the other arguments are the forward call's."""
+    what = "fp4_residual_norm_backward"
+    args = _norm_args(what, x, res, w_pre, w_post, gate, alpha, 0.0)
+    m, c = x.shape
+    for g, like, name in ((dn, x, "dn"), (dh, res, "dh")):
+        if g is not None and (g.dtype != like.dtype or not _is_rows(g, c, m)):
+            raise ValueError(f"{what}: {name} must be {like.dtype} [{m}, {c}] with unit column stride")
+    if tuple(stats.shape) != (m, 2) or stats.dtype != torch.float32 or not stats.is_contiguous():
+        raise ValueError(f"{what}: stats must be the forward call's")
+    dev = _on_device(what, x, res, w_pre, stats, *(t for t in (dn, dh, w_post, gate) if t is not None))
+    L = lib()
+    with _allocating(stream, dev):
+        dx = torch.empty((m, c), dtype=x.dtype, device=dev)
+        dres = torch.empty((m, c), dtype=res.dtype, device=dev)
+        dw_pre = torch.empty(c, dtype=torch.float32, device=dev)
+        dw_post = torch.empty(c, dtype=torch.float32, device=dev) if w_post is not None else None
+        dgate = torch.empty(m, dtype=torch.float32, device=dev) if gate is not None else None
+        ws = _space(L.fp4_residual_norm_workspace(m, c, w_post is not None), dev, what)
+        st = L.fp4_residual_norm_backward(ctypes.byref(args), stats.data_ptr(), _ptr(dn), 0 if dn is None else _ld(dn),
+                                          _ptr(dh), 0 if dh is None else _ld(dh), dx.data_ptr(), c, dres.data_ptr(), c,
+                                          dw_pre.data_ptr(), _ptr(dw_post), _ptr(dgate), _ptr(ws),
+                                          0 if ws is None else ws.numel(), _stream(stream, dev))
+    _check(st, what)
+    return ResidualNormGrads(dx, dres, dw_pre, dw_post, dgate)
+
+
 __all__ = ["fp4_quantize", "fp4_quantize_transposed", "fp4_quantize_both", "fp4_dequantize", "fp4_gemm",
            "fp4_wo_gemm", "AmaxState", "QTensor", "Fp4Error", "SCALE_FORMATS", "lib", "status_string", "LIB_PATH",
-           "set_exchange_wait", "set_gemm_small_outputs", "fp4_quantize_noalloc"]
+           "set_exchange_wait", "set_gemm_small_outputs", "fp4_quantize_noalloc", "LoraBank", "fp4_wo_gemm_lora",
+           "fp4_lora_apply", "fp4_lora_backward", "TokenLogprobs", "fp4_token_logprobs",
+           "fp4_token_logprobs_backward", "fp4_residual_norm", "ResidualNormGrads", "fp4_residual_norm_backward"]

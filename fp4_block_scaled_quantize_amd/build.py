@@ -29,7 +29,7 @@ PER_FILE = {
     "quant.hip": ["-ffp-contract=off", "-mllvm", "-amdgpu-atomic-optimizer-strategy=None"],
     "api.cpp": ["-ffp-contract=off"],
 }
-SOURCES = ["quant.hip", "gemm.hip", "api.cpp"]
+SOURCES = ["quant.hip", "gemm.hip", "lora.hip", "logprobs.hip", "norm.hip", "api.cpp", "api_train.cpp"]
 
 
 def hipcc() -> str:

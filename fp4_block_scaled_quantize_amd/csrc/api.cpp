@@ -11,6 +11,7 @@
 #include <atomic>
 #include <new>
 
+#include "api_checks.h"
 #include "fp4_internal.h"
 
 namespace fp4 {
@@ -61,7 +62,7 @@ struct fp4_amax_state {
 
 extern "C" {
 
-int32_t fp4_version(void) { return 107; }
+int32_t fp4_version(void) { return 108; }
 
 const char* fp4_status_string(fp4_status st)
 {
@@ -147,37 +148,6 @@ fp4_status fp4_amax_state_set(fp4_amax_state* st, uint64_t calls, float amax)
     st->calls = calls;
     return FP4_OK;
 }
-
-static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-static bool elem_is_8bit(int32_t e) { return e == FP4_ELEM_FP8_E4M3 || e == FP4_ELEM_INT8; }
-static bool elem_is_6bit(int32_t e) { return e >= FP4_ELEM_FP6_E2M3 && e <= FP4_ELEM_INT6; }
-// the 8- and 6-bit grids: no two-orientation call and no weight-only GEMM
-static bool elem_is_wide(int32_t e) { return elem_is_8bit(e) || elem_is_6bit(e); }
-
-static fp4_status check_tensor(const fp4_tensor* t, ScaleFmtHost* f)
-{
-    if (!t || !t->tensor_scale) return FP4_ERR_INVALID_ARG;
-    const bool empty = t->rows == 0 || t->cols == 0;
-    if (!empty && (!t->q || !t->scales)) return FP4_ERR_INVALID_ARG;
-    if (t->fmt.block != 16 && t->fmt.block != 32) return FP4_ERR_INVALID_ARG;
-    if (t->fmt.rounding != FP4_ROUND_NEAREST_EVEN && t->fmt.rounding != FP4_ROUND_STOCHASTIC)
-        return FP4_ERR_INVALID_ARG;
-    if (t->fmt.amax != FP4_AMAX_NONE && t->fmt.amax != FP4_AMAX_CURRENT && t->fmt.amax != FP4_AMAX_DELAYED)
-        return FP4_ERR_INVALID_ARG;
-    if (!scale_fmt_params(t->fmt.scale, f)) return FP4_ERR_INVALID_ARG;
-    if (t->fmt.transform != FP4_TRANSFORM_NONE && t->fmt.transform != FP4_TRANSFORM_RHT) return FP4_ERR_INVALID_ARG;
-    if (t->fmt.element < FP4_ELEM_E2M1 || t->fmt.element > FP4_ELEM_INT6) return FP4_ERR_INVALID_ARG;
-    if (t->rows < 0 || t->cols < 0) return FP4_ERR_SHAPE;
-    if (t->cols % t->fmt.block) return FP4_ERR_SHAPE;
-    // codes leave as 4-byte pieces (4-bit grids), 8-byte pieces (8-bit
-    // grids) or 2-byte pieces at 6-byte steps (6-bit grids; 8-byte alignment
-    // asked for as for 8 bits)
-    if (((uintptr_t)t->q & (elem_is_wide(t->fmt.element) ? 7u : 3u)) != 0) return FP4_ERR_ALIGN;
-    if ((t->rows * (t->cols / 8)) >= (int64_t(1) << 31)) return FP4_ERR_SHAPE;
-    return FP4_OK;
-}
-
-static fp4_status hip_status(hipError_t e) { return e == hipSuccess ? FP4_OK : FP4_ERR_HIP; }
 
 // Checks of fp4_quantize's arguments other than the amax state.
 static fp4_status check_quantize_args(const void* x, int32_t x_dtype, int64_t ld_x, fp4_tensor* out,
@@ -474,31 +444,12 @@ fp4_status fp4_gemm(const fp4_tensor* a, const fp4_tensor* b, uint16_t* c, int64
 fp4_status fp4_wo_gemm(const uint16_t* x, int64_t ldx, int64_t m, const fp4_tensor* w, uint16_t* y, int64_t ldy,
                        void* stream)
 {
-    ScaleFmtHost fw;
-    fp4_status st = check_tensor(w, &fw);
+    WoGemmLaunch p;
+    const fp4_status st = check_wo_gemm(x, ldx, m, w, y, ldy, &p);
     if (st != FP4_OK) return st;
-    if (!y || (!x && w->cols != 0)) return FP4_ERR_INVALID_ARG;
-    if (m < 1 || m > 16) return FP4_ERR_UNSUPPORTED;
-    if (w->fmt.transform != FP4_TRANSFORM_NONE) return FP4_ERR_UNSUPPORTED;   // x would need the same transform
-    if (w->cols % 256) return FP4_ERR_SHAPE;
-    if (ldx < w->cols || ldy < w->rows) return FP4_ERR_SHAPE;
     if (w->rows == 0) return FP4_OK;
     // an empty K: Y is the empty sum, zero; neither x nor W is read
     if (w->cols == 0) return hip_status(launch_fill_zero_bf16(y, ldy, m, w->rows, (hipStream_t)stream));
-    // the kernel addresses W and x with 32-bit byte/element offsets
-    const int64_t wbits = elem_is_8bit(w->fmt.element) ? 8 : elem_is_6bit(w->fmt.element) ? 6 : 4;
-    if (w->rows * (w->cols * wbits / 8) >= (int64_t(1) << 32) || ldx * m >= (int64_t(1) << 31))
-        return FP4_ERR_UNSUPPORTED;
-    if (!aligned16(x) || ldx % 8) return FP4_ERR_ALIGN;
-    if (!aligned16(w->q) || ((uintptr_t)w->scales & 3u)) return FP4_ERR_ALIGN;
-    WoGemmLaunch p;
-    p.x = x; p.ldx = ldx; p.m = m;
-    p.qw = w->q; p.sw = w->scales; p.gw = w->tensor_scale;
-    p.n = w->rows; p.k = w->cols;
-    p.elem = w->fmt.element;
-    p.block = w->fmt.block;
-    p.fw = fw;
-    p.y = y; p.ldy = ldy;
     return hip_status(launch_wo_gemm(p, (hipStream_t)stream));
 }
 

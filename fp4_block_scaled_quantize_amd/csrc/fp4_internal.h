@@ -122,6 +122,13 @@ extern int64_t g_gemm_small_outputs;
 bool gemm_small_supported(const GemmLaunch& p);
 hipError_t launch_gemm_small(const GemmLaunch& p, hipStream_t s);
 
+// T = x A^T of the rows' adapters as `splits` partial sums [M, rank], and the
+// up projections B [adapters, N, rank].
+struct WoAdapters {
+    const float* t; int32_t splits; int32_t rank;
+    const uint16_t* b; const float* scale; const int32_t* slots; int64_t adapters;
+};
+
 struct WoGemmLaunch {
     const uint16_t* x; int64_t ldx; int64_t m;
     const uint8_t* qw; const uint8_t* sw; const float* gw;
@@ -130,10 +137,116 @@ struct WoGemmLaunch {
     ScaleFmtHost fw;
     uint16_t* y; int64_t ldy;
     int32_t elem;              // element grid of the weights (fp4_element)
+    WoAdapters ad{};           // low-rank adapters added in the epilogue (none: t null)
 };
 
 hipError_t launch_wo_gemm(const WoGemmLaunch& p, hipStream_t s);
 // C[rows, cols] (bf16, row stride ld) = 0: the product over an empty K.
 hipError_t launch_fill_zero_bf16(uint16_t* c, int64_t ld, int64_t rows, int64_t cols, hipStream_t s);
+
+
+// ---------------------------------------------------------------------------
+// low-rank adapters (lora.hip)
+// ---------------------------------------------------------------------------
+struct LoraDown {
+    const uint16_t* x; int64_t ldx; int64_t m, k;
+    const uint16_t* a; int64_t adapters; int32_t rank;    // [adapters, rank, k]
+    const int32_t* slots;
+    const float* scale;        // null: 1
+    float* t;                  // [splits, m, rank]
+    int64_t kstep;
+};
+// Row tiles of 16 mi rows, K ranges of kstep, z adapters of a tile at once.
+struct LoraDownShape { int mi; int64_t splits, kstep, z; };
+LoraDownShape lora_down_shape(int64_t m, int64_t k, int rank, int64_t adapters);
+hipError_t launch_lora_down(const LoraDown& p, const LoraDownShape& sh, hipStream_t s);
+
+struct LoraUp {
+    const float* t; int32_t splits; int64_t m, n;
+    const uint16_t* b; int64_t adapters; int32_t rank;    // [adapters, n, rank]
+    const int32_t* slots;
+    const float* scale;        // null: 1
+    const uint16_t* base; int64_t ldbase;                 // null: zero
+    uint16_t* y; int64_t ldy;
+    float* t_out;              // the joined T [m, rank], if not null
+};
+hipError_t launch_lora_up(const LoraUp& p, hipStream_t s);
+
+struct LoraTranspose {
+    const uint16_t* src[2]; uint16_t* dst[2];
+    int64_t rows[2], cols[2], blocks[2];
+};
+hipError_t launch_lora_transpose(const uint16_t* a, uint16_t* at, const uint16_t* b, uint16_t* bt, int64_t adapters,
+                                 int64_t rank, int64_t k, int64_t n, hipStream_t s);
+
+struct LoraOuterJob {
+    const uint16_t* d; int64_t ldd; int64_t c;            // [m, c]
+    const float* p; const float* scale;                   // [m, rank]; scale null: 1
+    void* out; int32_t by_col;                            // [adapters, rank, c], or by_col [adapters, c, rank]
+    float* part;               // [splits] of out in binary32
+};
+struct LoraOuter {
+    LoraOuterJob job[2];
+    int32_t tiles[2];
+    int64_t m, mstep;
+    int32_t rank; int64_t adapters;
+    const int32_t* slots;
+    int32_t out_bf16;
+    uint32_t* flags;           // [splits, adapters]: the partial sum exists
+};
+int64_t lora_outer_splits(int64_t m, int64_t n, int64_t k, int rank, int64_t adapters);
+hipError_t launch_lora_outer(const LoraOuter& p, int64_t splits, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// token log probabilities (logprobs.hip)
+// ---------------------------------------------------------------------------
+constexpr int kLpMaxPieces = 32;
+struct LogprobLaunch {
+    const void* logits; int32_t bf16; int64_t ld, rows, vocab;
+    const int64_t* tokens;     // null: no token given
+    float inv_temperature; int32_t top;
+    float* logprob; float* entropy; float* stats;         // stats [rows, 2] = {maximum, log of the sum}
+    int32_t* top_ids; float* top_logprobs;                // [rows, top]
+    uint64_t* part_keys;       // [rows, pieces, top]
+    float* part_sums;          // [rows, pieces, 4]
+    int64_t piece;
+};
+int64_t logprob_pieces(int64_t rows, int64_t vocab);
+hipError_t launch_logprobs(const LogprobLaunch& p, int64_t pieces, hipStream_t s);
+
+struct LogprobGradLaunch {
+    const void* logits; int32_t bf16; int64_t ld, rows, vocab;
+    const int64_t* tokens;
+    float inv_temperature;
+    const float* entropy; const float* stats;
+    const float* g_logprob; const float* g_entropy;       // null: zero
+    void* dlogits; int64_t ldd;
+    int64_t piece;
+};
+hipError_t launch_logprobs_backward(const LogprobGradLaunch& p, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// residual norms (norm.hip)
+// ---------------------------------------------------------------------------
+struct NormLaunch {
+    const void* x; int64_t ldx; const void* res; int64_t ldres;
+    int32_t x_bf16, res_bf16, w_bf16;
+    int64_t rows, cols;
+    const void* w_pre; const void* w_post;                // w_post null: no post norm
+    const float* gate;                                    // [rows], null: 1
+    float alpha, eps;
+    void* h; int64_t ldh; void* n; int64_t ldn;
+    float* stats;                                         // [rows, 2] = {rho(x), rho(h)}
+};
+struct NormGradLaunch {
+    NormLaunch f;
+    const void* dn; int64_t lddn; const void* dh; int64_t lddh;   // null: zero
+    void* dx; int64_t lddx; void* dres; int64_t lddres;
+    float* dw_pre; float* dw_post; float* dgate;
+    float* part; int64_t part_rows, groups;               // [groups, part_rows, cols]
+};
+int64_t norm_groups(int64_t rows);
+hipError_t launch_norm(const NormLaunch& p, bool vec, hipStream_t s);
+hipError_t launch_norm_backward(const NormGradLaunch& p, bool vec, hipStream_t s);
 
 }  // namespace fp4

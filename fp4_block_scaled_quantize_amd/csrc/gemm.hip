@@ -2260,6 +2260,16 @@ __global__ __launch_bounds__(64 * NW) void k_wo_gemm(WoGemmLaunch p)
     for (int g = 0; g < RG; ++g)
 #pragma unroll
         for (int r = 0; r < 4; ++r) red[wave][g][lane * 4 + r] = acc[g][r];
+    // T [M, rank] of the rows' adapters, joined from its partial sums
+    float* const ts = reinterpret_cast<float*>(wo_ring) + NW * RG * 256;
+    if (p.ad.t) {
+        const int mr_ = (int)M * p.ad.rank;
+        for (int e = tid; e < mr_; e += 64 * NW) {
+            float v = 0.0f;
+            for (int s = 0; s < p.ad.splits; ++s) v += p.ad.t[(int64_t)s * mr_ + e];
+            ts[e] = v;
+        }
+    }
     __syncthreads();
     for (int e = tid; e < 256 * RG; e += 64 * NW) {
         const int g = e >> 8, t = e & 255;
@@ -2268,7 +2278,25 @@ __global__ __launch_bounds__(64 * NW) void k_wo_gemm(WoGemmLaunch p)
         for (int w = 0; w < NW; ++w) sum += red[w][g][t];
         const int l = t >> 2, r = t & 3;
         const int64_t m = 4 * (l >> 4) + r, nn = n0 + 16 * g + (l & 15);
-        if (m < M && nn < N) p.y[m * p.ldy + nn] = (uint16_t)f32_to_bf16_rne(sum * gres);
+        if (m < M && nn < N) {
+            float v = sum * gres;
+            if (p.ad.t) {
+                const int sl = p.ad.slots[m];
+                if (sl >= 0 && sl < p.ad.adapters) {
+                    const uint16_t* const b = p.ad.b + ((int64_t)sl * N + nn) * p.ad.rank;
+                    const float* const t = ts + m * p.ad.rank;
+                    float dot = 0.0f;
+                    for (int r = 0; r < p.ad.rank; r += 8) {
+                        const v4i w = *reinterpret_cast<const v4i*>(b + r);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            dot += t[r + 2 * q] * bf16_lo((uint32_t)w[q]) + t[r + 2 * q + 1] * bf16_hi((uint32_t)w[q]);
+                    }
+                    v += p.ad.scale[sl] * dot;
+                }
+            }
+            p.y[m * p.ldy + nn] = (uint16_t)f32_to_bf16_rne(v);
+        }
     }
 }
 
@@ -2280,12 +2308,14 @@ using WoSlotOf = WoSlot<RG, XQ, WoRow<ELEM, SUB>::WP, SUB, 128 * SUB / BLOCK>;
 template <int NW, int D, int RG, int XQ, int BLOCK, bool SPLIT, bool POW2, int ELEM, int SUB>
 static hipError_t launch_wo_k(const WoGemmLaunch& p, hipStream_t s)
 {
-    constexpr size_t sh = (size_t)NW * D * WoSlotOf<RG, XQ, ELEM, SUB, BLOCK>::Bytes;   // the ring, later the partial tiles
+    // the ring, later the partial tiles and the adapters' T (16 rows of up to 128)
+    constexpr size_t ring = (size_t)NW * D * WoSlotOf<RG, XQ, ELEM, SUB, BLOCK>::Bytes;
+    constexpr size_t tail = sizeof(float) * (NW * RG * 256 + 16 * 128);
+    constexpr size_t sh = ring > tail ? ring : tail;
     if constexpr (sh + sizeof(float) * 256 > 160 * 1024) {
         static_assert(NW != 4 || D != 2, "the smallest ring fits");
         return launch_wo_k<4, 2, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB>(p, s);
     }
-    static_assert(sh >= sizeof(float) * NW * RG * 256, "partial tiles fit the ring");
     if (sh > 64 * 1024) {
         const hipError_t e = allow_lds(k_wo_gemm<NW, D, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB>, sh);
         if (e != hipSuccess) return e;

@@ -1,0 +1,578 @@
+// lora.hip -- low-rank adapters of many requests beside a shared projection
+// (quant_prune_distill/574 "Метод": a trained low-rank adapter runs in
+// parallel with the FP4 weight).
+//
+// Row i of a batch uses adapter l = slots[i] (none when l is outside the
+// bank).  With A [L, R, K], B [L, N, R] in bf16 and a scale s_l:
+//   forward   T = x A_l^T,  y = base + s_l T B_l^T
+//   backward  dT = s_l dy B_l,  dx = base + dT A_l,
+//             dA_l = sum_i dT_i^T x_i,  dB_l = s_l sum_i dy_i^T T_i
+// T and dT stay in binary32.  Where one enters a bf16 matrix instruction it
+// goes in as a sum of bf16 terms, t = hi + lo (16 significant bits; plus a
+// third term, 24 bits, for gradients returned in binary32), so the results
+// are rounded once, at the end.
+#include "fp4_device.hpp"
+#include "fp4_internal.h"
+
+namespace fp4 {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ v4f mfma16(v4i a, v4i b, v4f c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
+}
+
+// The adapter of a row: slots[row] when it names one of the bank, else -1.
+__device__ __forceinline__ int row_slot(const int32_t* slots, int64_t row, int64_t m, int64_t adapters)
+{
+    if (row >= m) return -1;
+    const int s = slots[row];
+    return s >= 0 && s < adapters ? s : -1;
+}
+
+// t as NT bf16 terms (each the rounding of what the ones before leave; an
+// infinite term leaves nothing).
+template <int NT>
+__device__ __forceinline__ void bf16_terms(float t, uint32_t (&out)[NT])
+{
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        out[i] = f32_to_bf16_rne(t);
+        const float h = bits_f(out[i] << 16);
+        t = __builtin_isinf(h) ? 0.0f : t - h;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// T = x A_l^T: one workgroup per 16 MI rows and K range, its four waves on
+// quarters of the range, joined through LDS in a fixed order.  Both operands
+// run along K, so each lane's 16 bytes are a matrix-instruction fragment as
+// they come from memory; nothing is staged.  A tile whose rows use several
+// adapters runs its K range once for each (gridDim.z of them side by side)
+// and keeps each row's own.  With gridDim.y > 1 the K ranges' partial sums
+// are left for the reader of T to join.
+// ---------------------------------------------------------------------------
+template <int MI, int RT>
+__global__ __launch_bounds__(256) void k_lora_down(LoraDown p)
+{
+    __shared__ v4f red[4][MI * RT * 64];
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, grp = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t m0 = (int64_t)blockIdx.x * (16 * MI);
+    const int64_t M = p.m, K = p.k;
+    const int R = p.rank;
+    float* const t = p.t + (int64_t)blockIdx.y * M * R;
+    const int slot = lane < 16 * MI ? row_slot(p.slots, m0 + lane, M, p.adapters) : -1;
+
+    if (blockIdx.z == 0) {                    // rows without an adapter
+        for (int i = wave; i < 16 * MI; i += 4)
+            if (__builtin_amdgcn_readlane(slot, i) < 0 && m0 + i < M)
+                for (int r = lane; r < R; r += 64) t[(m0 + i) * R + r] = 0.0f;
+    }
+
+    const int64_t kb = (int64_t)blockIdx.y * p.kstep, ke = kb + p.kstep < K ? kb + p.kstep : K;
+    const int64_t kw = p.kstep / 4;                                      // a multiple of 32
+    const int64_t k0 = kb + wave * kw, k1 = k0 + kw < ke ? k0 + kw : ke;
+    const uint16_t* xr[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int64_t m = m0 + 16 * i + r16;
+        xr[i] = p.x + (m < M ? m : M - 1) * p.ldx + 8 * grp;
+    }
+    int64_t ar[RT];
+#pragma unroll
+    for (int j = 0; j < RT; ++j) ar[j] = (int64_t)(16 * j + r16 < R ? 16 * j + r16 : R - 1) * K + 8 * grp;
+
+    uint64_t todo = __builtin_amdgcn_ballot_w64(slot >= 0);
+    for (unsigned nth = 0; todo; ++nth) {
+        const int cur = __builtin_amdgcn_readlane(slot, __builtin_ctzll(todo));
+        const uint64_t match = __builtin_amdgcn_ballot_w64(slot == cur);
+        todo &= ~match;
+        if (nth % gridDim.z != blockIdx.z) continue;
+        const uint16_t* const a = p.a + (int64_t)cur * R * K;
+        v4f acc[MI][RT];
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < RT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+        int64_t k = k0;
+        for (; k + 128 <= k1; k += 128) {
+            v4i xf[4][MI], af[4][RT];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                for (int i = 0; i < MI; ++i) xf[u][i] = *reinterpret_cast<const v4i*>(xr[i] + k + 32 * u);
+#pragma unroll
+                for (int j = 0; j < RT; ++j) af[u][j] = *reinterpret_cast<const v4i*>(a + ar[j] + k + 32 * u);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+#pragma unroll
+                    for (int j = 0; j < RT; ++j) acc[i][j] = mfma16(af[u][j], xf[u][i], acc[i][j]);
+        }
+        for (; k < k1; k += 32) {
+            const bool in = k + 8 * grp < k1;          // 8 elements, all in or all out
+            const v4i zero{0, 0, 0, 0};
+            v4i xf[MI], af[RT];
+#pragma unroll
+            for (int i = 0; i < MI; ++i) xf[i] = in ? *reinterpret_cast<const v4i*>(xr[i] + k) : zero;
+#pragma unroll
+            for (int j = 0; j < RT; ++j) af[j] = in ? *reinterpret_cast<const v4i*>(a + ar[j] + k) : zero;
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < RT; ++j) acc[i][j] = mfma16(af[j], xf[i], acc[i][j]);
+        }
+        // acc[i][j][e] = T[m = 16 i + r16][r = 16 j + 4 grp + e]
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < RT; ++j) red[wave][(i * RT + j) * 64 + lane] = acc[i][j];
+        __syncthreads();
+        const float s = p.scale ? p.scale[cur] : 1.0f;
+        for (int e = tid; e < MI * RT * 64; e += 256) {
+            const int tile = e >> 6, l = e & 63, i = tile / RT, j = tile % RT;
+            const int m = 16 * i + (l & 15), r = 16 * j + 4 * (l >> 4);
+            if (((match >> m) & 1) && r < R) {
+                const v4f v = ((red[0][e] + red[1][e]) + (red[2][e] + red[3][e])) * s;
+                *reinterpret_cast<v4f*>(t + (m0 + m) * R + r) = v;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// y = base + s_l T B_l^T: one workgroup per 16 MI rows x 256 columns, 64
+// columns a wave.  The columns of a matrix-instruction pair are dealt so that
+// a lane's eight results are eight consecutive columns of one row: base is
+// read and y written 16 bytes a lane.  T comes from LDS as hi and lo terms;
+// rows of another adapter than the one whose B is multiplied drop the result
+// (a select, so that nothing of one adapter reaches another's rows).
+// ---------------------------------------------------------------------------
+template <int MI, int RC>
+__global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
+{
+    constexpr int RP = 32 * RC + 4;                     // LDS row pitch (floats)
+    __shared__ __align__(16) float ts[16 * MI][RP];
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, grp = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t M = p.m, N = p.n;
+    const int R = p.rank;
+    const int64_t m0 = (int64_t)blockIdx.y * (16 * MI);
+    const int64_t n0 = (int64_t)blockIdx.x * 256 + 64 * wave + 8 * grp;
+    const int slot = lane < 16 * MI ? row_slot(p.slots, m0 + lane, M, p.adapters) : -1;
+
+    v4i old[MI][2];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int64_t m = m0 + 16 * i + r16, n = n0 + 32 * u;
+            old[i][u] = p.base && m < M && n < N ? *reinterpret_cast<const v4i*>(p.base + m * p.ldbase + n)
+                                                 : v4i{0, 0, 0, 0};
+        }
+    for (int e = tid; e < 16 * MI * 8 * RC; e += 256) {
+        const int m = e / (8 * RC), r = 4 * (e % (8 * RC));
+        v4f v{0.f, 0.f, 0.f, 0.f};
+        if (m0 + m < M && r < R) {
+            for (int s = 0; s < p.splits; ++s)
+                v += *reinterpret_cast<const v4f*>(p.t + ((int64_t)s * M + m0 + m) * R + r);
+            if (p.t_out && blockIdx.x == 0) *reinterpret_cast<v4f*>(p.t_out + (m0 + m) * R + r) = v;
+        }
+        *reinterpret_cast<v4f*>(&ts[m][r]) = v;
+    }
+    __syncthreads();
+    v4i th[MI][RC], tl[MI][RC];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int c = 0; c < RC; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t x0[2], x1[2];
+                bf16_terms<2>(ts[16 * i + r16][32 * c + 8 * grp + 2 * q], x0);
+                bf16_terms<2>(ts[16 * i + r16][32 * c + 8 * grp + 2 * q + 1], x1);
+                th[i][c][q] = (int)(x0[0] | (x1[0] << 16));
+                tl[i][c][q] = (int)(x0[1] | (x1[1] << 16));
+            }
+    int mine[MI];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) mine[i] = __shfl(slot, 16 * i + r16);
+
+    float o[MI][2][8];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[i][u][e] = 0.0f;
+    uint64_t todo = __builtin_amdgcn_ballot_w64(slot >= 0);
+    while (todo) {
+        const int cur = __builtin_amdgcn_readlane(slot, __builtin_ctzll(todo));
+        todo &= ~__builtin_amdgcn_ballot_w64(slot == cur);
+        const uint16_t* const b = p.b + (int64_t)cur * N * R;
+        const float s = p.scale ? p.scale[cur] : 1.0f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t n = (int64_t)blockIdx.x * 256 + 64 * wave + 32 * u + 8 * (r16 >> 2) + 4 * h + (r16 & 3);
+                const uint16_t* const row = b + (n < N ? n : N - 1) * R + 8 * grp;
+                v4i bf[RC];
+#pragma unroll
+                for (int c = 0; c < RC; ++c)
+                    bf[c] = 32 * c + 8 * grp < R ? *reinterpret_cast<const v4i*>(row + 32 * c) : v4i{0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    v4f acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < RC; ++c) {
+                        acc = mfma16(bf[c], tl[i][c], acc);
+                        acc = mfma16(bf[c], th[i][c], acc);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][u][4 * h + e] = mine[i] == cur ? acc[e] * s : o[i][u][4 * h + e];
+                }
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int64_t m = m0 + 16 * i + r16;
+        // a row without an adapter keeps its bits (and is left alone in place)
+        if (m >= M || (mine[i] < 0 && p.base == p.y)) continue;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int64_t n = n0 + 32 * u;
+            if (n >= N) continue;
+            v4i v = old[i][u];
+            if (mine[i] >= 0) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t w = (uint32_t)old[i][u][q];
+                    const uint32_t lo = f32_to_bf16_rne(bf16_lo(w) + o[i][u][2 * q]);
+                    const uint32_t hi = f32_to_bf16_rne(bf16_hi(w) + o[i][u][2 * q + 1]);
+                    v[q] = (int)(lo | (hi << 16));
+                }
+            }
+            *reinterpret_cast<v4i*>(p.y + m * p.ldy + n) = v;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// A_l [R, K] -> [K, R] and B_l [N, R] -> [R, N], 64 x 64 tiles through LDS:
+// the backward products contract over the other index of each.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void k_lora_transpose(LoraTranspose p)
+{
+    __shared__ uint16_t tile[64][66];
+    int64_t b = blockIdx.x;
+    const int which = b >= p.blocks[0];
+    if (which) b -= p.blocks[0];
+    const int64_t rows = p.rows[which], cols = p.cols[which];
+    const int64_t tr = (rows + 63) / 64, tc = (cols + 63) / 64;
+    const int64_t l = b / (tr * tc), in = b % (tr * tc);
+    const int64_t r0 = in / tc * 64, c0 = in % tc * 64;
+    const uint16_t* const src = p.src[which] + l * rows * cols;
+    uint16_t* const dst = p.dst[which] + l * rows * cols;
+    for (int e = threadIdx.x; e < 64 * 8; e += 256) {
+        const int r = e >> 3, c = 8 * (e & 7);
+        if (r0 + r < rows && c0 + c < cols) {          // cols % 8 == 0
+            const v4i v = *reinterpret_cast<const v4i*>(src + (r0 + r) * cols + c0 + c);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                tile[r][c + 2 * q] = (uint16_t)v[q];
+                tile[r][c + 2 * q + 1] = (uint16_t)((uint32_t)v[q] >> 16);
+            }
+        }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 64 * 8; e += 256) {
+        const int c = e >> 3, r = 8 * (e & 7);
+        if (c0 + c < cols && r0 + r < rows) {          // rows % 8 == 0
+            v4i v;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = (int)(tile[r + 2 * q][c] | ((uint32_t)tile[r + 2 * q + 1][c] << 16));
+            *reinterpret_cast<v4i*>(dst + (c0 + c) * rows + r0 + r) = v;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// G_l[c, r] = sum over the rows of adapter l of D[row, c] P[row, r]: dA (D =
+// x, P = dT) and dB (D = dy, P = s_l T) in one launch.  The sum runs down the
+// rows, so a fragment is a column's 8 values: each lane reads 16 bytes of 8
+// rows and transposes its own 8 x 8 block with byte permutes; matrix
+// instruction ci then covers columns {8 i + ci}, and a lane ends with 32
+// consecutive columns of one r.  Each wave takes every fourth chunk of 32
+// rows, skips the chunks without a row of l and zeroes other adapters' rows
+// in both operands (an infinity there must not meet a zero).  Row ranges
+// (gridDim.z) leave partial sums, joined in a fixed order by k_lora_join.
+// ---------------------------------------------------------------------------
+template <int RT, int NT>
+__global__ __launch_bounds__(256) void k_lora_outer(LoraOuter p)
+{
+    __shared__ v4f red[8 * RT * 64];
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, grp = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int which = (int)blockIdx.x >= p.tiles[0];
+    const LoraOuterJob& job = p.job[which];
+    const int R = p.rank, rgroups = (R + 16 * RT - 1) / (16 * RT);
+    const int l = (int)blockIdx.y / rgroups, rg = (int)blockIdx.y % rgroups;
+    const int64_t M = p.m, C = job.c;
+    const int64_t c0 = (int64_t)(blockIdx.x - (which ? p.tiles[0] : 0)) * 128;
+    const int64_t cl = c0 + 8 * r16 < C ? c0 + 8 * r16 : C - 8;       // this lane's 8 columns (C % 8 == 0)
+    const int64_t mb = (int64_t)blockIdx.z * p.mstep, me = mb + p.mstep < M ? mb + p.mstep : M;
+
+    v4f acc[8][RT];
+#pragma unroll
+    for (int ci = 0; ci < 8; ++ci)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[ci][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    int any = 0;
+    for (int64_t mc = mb + 32 * wave; mc < me; mc += 128) {
+        const int s = lane < 32 ? row_slot(p.slots, mc + lane, me, p.adapters) : -1;
+        const uint32_t rows = (uint32_t)__builtin_amdgcn_ballot_w64(s == l);
+        if (rows == 0) continue;
+        any = 1;
+        const uint32_t keep = (rows >> (8 * grp)) & 0xFFu;
+        v4i d[8];
+        float pv[RT][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t m = mc + 8 * grp + j < M ? mc + 8 * grp + j : M - 1;
+            d[j] = *reinterpret_cast<const v4i*>(job.d + m * job.ldd + cl);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const int r = 16 * (rg * RT + t) + r16;
+                pv[t][j] = job.p[m * R + (r < R ? r : R - 1)];
+            }
+        }
+        if (rows != 0xFFFFFFFFu) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bool in = (keep >> j) & 1;
+                d[j] = in ? d[j] : v4i{0, 0, 0, 0};
+#pragma unroll
+                for (int t = 0; t < RT; ++t) pv[t][j] = in ? pv[t][j] : 0.0f;
+            }
+        }
+        v4i pf[RT][NT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t x0[NT], x1[NT];
+                bf16_terms<NT>(pv[t][2 * q], x0);
+                bf16_terms<NT>(pv[t][2 * q + 1], x1);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) pf[t][i][q] = (int)(x0[i] | (x1[i] << 16));
+            }
+#pragma unroll
+        for (int ci = 0; ci < 8; ++ci) {
+            v4i f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                f[q] = (int)__builtin_amdgcn_perm((uint32_t)d[2 * q + 1][ci >> 1], (uint32_t)d[2 * q][ci >> 1],
+                                                  (ci & 1) ? 0x07060302u : 0x05040100u);
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int i = NT - 1; i >= 0; --i) acc[ci][t] = mfma16(f, pf[t][i], acc[ci][t]);
+        }
+    }
+    any = __syncthreads_or(any);
+    if (gridDim.z > 1) {
+        if (blockIdx.x == 0 && rg == 0 && tid == 0) p.flags[(int64_t)blockIdx.z * p.adapters + l] = (uint32_t)any;
+        if (!any) return;
+    }
+    // waves 1, 2, 3 onto wave 0, in that order
+    for (int w = 1; w < 4; ++w) {
+        if (wave == w) {
+#pragma unroll
+            for (int ci = 0; ci < 8; ++ci)
+#pragma unroll
+                for (int t = 0; t < RT; ++t) red[(ci * RT + t) * 64 + lane] = acc[ci][t];
+        }
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int ci = 0; ci < 8; ++ci)
+#pragma unroll
+                for (int t = 0; t < RT; ++t) acc[ci][t] += red[(ci * RT + t) * 64 + lane];
+        }
+        __syncthreads();
+    }
+    if (wave) return;
+    // acc[ci][t][e] = G[c = c0 + 32 grp + 8 e + ci][r = 16 (rg RT + t) + r16]
+    const float s = job.scale ? job.scale[l] : 1.0f;
+    float* const part = gridDim.z > 1 ? job.part + (int64_t)blockIdx.z * p.adapters * R * C : nullptr;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int r = 16 * (rg * RT + t) + r16;
+        if (r >= R) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t c = c0 + 32 * grp + 8 * e;
+            if (c >= C) continue;
+            float v[8];
+#pragma unroll
+            for (int ci = 0; ci < 8; ++ci) v[ci] = acc[ci][t][e] * s;
+            // dA [R, C]: 8 consecutive elements; dB [C, R]: one element each of 8 rows, 16 lanes side by side
+            const int64_t at = (int64_t)l * R * C + (job.by_col ? c * R + r : (int64_t)r * C + c);
+            const int64_t step = job.by_col ? R : 1;
+            if (part) {
+#pragma unroll
+                for (int ci = 0; ci < 8; ++ci) part[at + ci * step] = v[ci];
+            } else if (p.out_bf16) {
+#pragma unroll
+                for (int ci = 0; ci < 8; ++ci)
+                    reinterpret_cast<uint16_t*>(job.out)[at + ci * step] = (uint16_t)f32_to_bf16_rne(v[ci]);
+            } else {
+#pragma unroll
+                for (int ci = 0; ci < 8; ++ci) reinterpret_cast<float*>(job.out)[at + ci * step] = v[ci];
+            }
+        }
+    }
+}
+
+// Sum of the row ranges' partial gradients that hold anything, in order.
+__global__ __launch_bounds__(256) void k_lora_join(LoraOuter p, int splits)
+{
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const LoraOuterJob& job = p.job[which];
+        const int64_t per = (int64_t)p.rank * job.c, total = per * p.adapters;
+        for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; e < total; e += (int64_t)gridDim.x * 1024) {
+            const int64_t l = e / per;
+            v4f v{0.f, 0.f, 0.f, 0.f};
+            for (int s = 0; s < splits; ++s)
+                if (p.flags[(int64_t)s * p.adapters + l]) v += *reinterpret_cast<const v4f*>(job.part + s * total + e);
+            if (p.out_bf16) {
+                uint2 w;
+                w.x = f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16);
+                w.y = f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16);
+                *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(job.out) + e) = w;
+            } else {
+                *reinterpret_cast<v4f*>(reinterpret_cast<float*>(job.out) + e) = v;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// launch shapes
+// ---------------------------------------------------------------------------
+static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+static int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// Row tiles: 64 rows where that leaves registers for the rank's accumulators
+// (MI * RT <= 8), 16 for a batch of at most 16 rows.
+static int down_mi(int64_t m, int rank) { return m <= 16 || rank > 64 ? 1 : rank > 32 ? 2 : 4; }
+
+// K ranges: enough workgroups for every CU, none below 256 elements (64 a
+// wave), at most 32 partial sums for the reader to join.
+LoraDownShape lora_down_shape(int64_t m, int64_t k, int rank, int64_t adapters)
+{
+    LoraDownShape s;
+    s.mi = down_mi(m, rank);
+    const int64_t tiles = cdiv(m, 16 * s.mi);
+    s.splits = clamp64(256 / tiles, 1, clamp64(k / 256, 1, 32));
+    s.kstep = cdiv(cdiv(k, s.splits), 128) * 128;
+    s.splits = cdiv(k, s.kstep);
+    int64_t most = m < 16 * s.mi ? m : 16 * s.mi;
+    if (adapters < most) most = adapters;
+    s.z = clamp64(1024 / (tiles * s.splits), 1, most);
+    return s;
+}
+
+// The row ranges of the gradient sums: enough workgroups to fill the device
+// when the rows of the adapters are about even, at least 256 rows each (two
+// chunks a wave).  Many adapters fill it by themselves, and a range costs a
+// partial sum of every adapter's gradient.
+int64_t lora_outer_splits(int64_t m, int64_t n, int64_t k, int rank, int64_t adapters)
+{
+    const int64_t groups = (cdiv(n, 128) + cdiv(k, 128)) * adapters * cdiv(rank, 64);
+    return clamp64(2048 / groups, 1, clamp64(m / 256, 1, 16));
+}
+
+template <int MI, int RT>
+static hipError_t run_down(const LoraDown& p, const LoraDownShape& sh, hipStream_t s)
+{
+    const dim3 grid((unsigned)cdiv(p.m, 16 * MI), (unsigned)sh.splits, (unsigned)sh.z);
+    hipLaunchKernelGGL((k_lora_down<MI, RT>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_lora_down(const LoraDown& in, const LoraDownShape& sh, hipStream_t s)
+{
+    LoraDown p = in;
+    p.kstep = sh.kstep;
+    const int rt = p.rank <= 16 ? 1 : p.rank <= 32 ? 2 : p.rank <= 64 ? 4 : 8;
+    if (sh.mi == 4) return rt == 1 ? run_down<4, 1>(p, sh, s) : run_down<4, 2>(p, sh, s);
+    if (sh.mi == 2) return run_down<2, 4>(p, sh, s);
+    switch (rt) {
+    case 1: return run_down<1, 1>(p, sh, s);
+    case 2: return run_down<1, 2>(p, sh, s);
+    case 4: return run_down<1, 4>(p, sh, s);
+    default: return run_down<1, 8>(p, sh, s);
+    }
+}
+
+template <int MI, int RC>
+static hipError_t run_up(const LoraUp& p, hipStream_t s)
+{
+    const dim3 grid((unsigned)cdiv(p.n, 256), (unsigned)cdiv(p.m, 16 * MI));
+    hipLaunchKernelGGL((k_lora_up<MI, RC>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_lora_up(const LoraUp& p, hipStream_t s)
+{
+    const int rc = p.rank <= 32 ? 1 : p.rank <= 64 ? 2 : 4;
+    if (p.m <= 16) return rc == 1 ? run_up<1, 1>(p, s) : rc == 2 ? run_up<1, 2>(p, s) : run_up<1, 4>(p, s);
+    return rc == 1 ? run_up<4, 1>(p, s) : rc == 2 ? run_up<4, 2>(p, s) : run_up<2, 4>(p, s);
+}
+
+hipError_t launch_lora_transpose(const uint16_t* a, uint16_t* at, const uint16_t* b, uint16_t* bt, int64_t adapters,
+                                 int64_t rank, int64_t k, int64_t n, hipStream_t s)
+{
+    LoraTranspose p;
+    p.src[0] = a; p.dst[0] = at; p.rows[0] = rank; p.cols[0] = k;
+    p.src[1] = b; p.dst[1] = bt; p.rows[1] = n; p.cols[1] = rank;
+    for (int i = 0; i < 2; ++i) p.blocks[i] = adapters * cdiv(p.rows[i], 64) * cdiv(p.cols[i], 64);
+    hipLaunchKernelGGL(k_lora_transpose, dim3((unsigned)(p.blocks[0] + p.blocks[1])), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+template <int RT, int NT>
+static hipError_t run_outer(const LoraOuter& p, int64_t splits, hipStream_t s)
+{
+    const dim3 grid((unsigned)(p.tiles[0] + p.tiles[1]), (unsigned)(p.adapters * cdiv(p.rank, 16 * RT)), (unsigned)splits);
+    hipLaunchKernelGGL((k_lora_outer<RT, NT>), grid, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_lora_outer(const LoraOuter& in, int64_t splits, hipStream_t s)
+{
+    LoraOuter p = in;
+    p.tiles[0] = (int32_t)cdiv(p.job[0].c, 128);
+    p.tiles[1] = (int32_t)cdiv(p.job[1].c, 128);
+    p.mstep = cdiv(cdiv(p.m, splits), 128) * 128;
+    hipError_t e;
+    if (p.rank <= 16) e = p.out_bf16 ? run_outer<1, 2>(p, splits, s) : run_outer<1, 3>(p, splits, s);
+    else if (p.rank <= 32) e = p.out_bf16 ? run_outer<2, 2>(p, splits, s) : run_outer<2, 3>(p, splits, s);
+    else e = p.out_bf16 ? run_outer<4, 2>(p, splits, s) : run_outer<4, 3>(p, splits, s);
+    if (e != hipSuccess || splits == 1) return e;
+    const int64_t most = p.adapters * p.rank * (p.job[0].c > p.job[1].c ? p.job[0].c : p.job[1].c);
+    hipLaunchKernelGGL(k_lora_join, dim3((unsigned)clamp64(cdiv(most, 1024), 1, 2048)), dim3(256), 0, s, p, (int)splits);
+    return hipGetLastError();
+}
+
+}  // namespace fp4

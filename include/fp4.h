@@ -387,6 +387,159 @@ FP4_API fp4_status fp4_set_gemm_small_outputs(int64_t outputs, int64_t* previous
 FP4_API fp4_status fp4_wo_gemm(const uint16_t* x, int64_t ldx, int64_t m, const fp4_tensor* w, uint16_t* y,
                        int64_t ldy, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection
+ * (quant_prune_distill/574 "Метод": a trained low-rank adapter in parallel
+ * with the NVFP4 weight; the page gives no formula).  Row i of a batch uses
+ * adapter l = slots[i]; a value outside 0 .. adapters - 1 (-1 by convention)
+ * gives the row none.  Reading:
+ *   T = x A_l^T,  y = base + s_l T B_l^T
+ * with T, and every sum, in binary32.  Rows of one adapter need not be
+ * adjacent; a batch that keeps each request's rows together is read fewest
+ * times.  Nothing of one adapter or row reaches another row's results
+ * (infinities and NaN included).  Rows without an adapter keep base.
+ *
+ * A bank: a [adapters, rank, k] and b [adapters, n, rank] in bf16, dense and
+ * 16-byte aligned; scale [adapters] in binary32.  rank % 8 == 0 and at most
+ * 128 (a smaller rank is padded with zeros), k % 8 == 0, n % 8 == 0 (any n
+ * for fp4_wo_gemm_lora), at most 16384 adapters.
+ *
+ * `workspace`: device memory, 16-byte aligned, of at least
+ * fp4_lora_workspace bytes (it may be null when that is 0), in use until the
+ * call's work on the stream has finished.  At most 2^20 rows a call. */
+typedef struct fp4_lora_bank {
+    const uint16_t* a;
+    const uint16_t* b;
+    const float* scale;
+    int64_t adapters, rank, k, n;
+} fp4_lora_bank;
+
+typedef enum fp4_lora_call {
+    FP4_LORA_APPLY = 0,
+    FP4_LORA_BACKWARD = 1,
+    FP4_LORA_WO_GEMM = 2
+} fp4_lora_call;
+
+/* Bytes of workspace that a call on m rows needs (negative: a status). */
+FP4_API int64_t fp4_lora_workspace(int32_t call, int64_t m, int64_t n, int64_t k, int64_t rank, int64_t adapters);
+
+/*
+ * fp4_lora_apply -- y[m, n] (bf16) = bf16_RNE(base + s_l T B_l^T) and T
+ * [m, rank] (binary32, zero for rows without an adapter), which the backward
+ * call reads.  base: bf16 [m, n], the shared projection's output; null for
+ * zero; it may be y itself (same row stride).  x: bf16 [m, k].  Rows 16-byte
+ * aligned (row strides % 8 == 0).
+ */
+FP4_API fp4_status fp4_lora_apply(const uint16_t* x, int64_t ldx, int64_t m, const fp4_lora_bank* bank,
+                                  const int32_t* slots, const uint16_t* base, int64_t ld_base, uint16_t* y, int64_t ldy,
+                                  float* t, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * fp4_lora_backward -- the gradients of fp4_lora_apply for dy [m, n]:
+ *   dT = s_l dy B_l,  dx = bf16_RNE(dx_base + dT A_l),
+ *   da[l] = sum_i dT_i^T x_i,  db[l] = s_l sum_i dy_i^T T_i
+ * over the rows i of adapter l (zero for an adapter without rows).  t is
+ * fp4_lora_apply's T; dx_base is the gradient that arrives at x through the
+ * shared projection (null for zero; it may be dx).  da, db have the bank's
+ * shapes in grad_dtype, are written whole and 16-byte aligned.  The sums are
+ * taken in a fixed order: the same inputs give the same bits.
+ */
+FP4_API fp4_status fp4_lora_backward(const uint16_t* dy, int64_t ld_dy, const uint16_t* x, int64_t ldx, int64_t m,
+                                     const float* t, const fp4_lora_bank* bank, const int32_t* slots,
+                                     const uint16_t* dx_base, int64_t ld_dx_base, uint16_t* dx, int64_t ld_dx, void* da,
+                                     void* db, int32_t grad_dtype, void* workspace, int64_t workspace_bytes,
+                                     void* stream);
+
+/*
+ * fp4_wo_gemm_lora -- fp4_wo_gemm with the rows' adapters in its epilogue:
+ * Y = bf16_RNE(gw sum_k x (e(w) s_w) + s_l T B_l^T), rounded once.
+ * Requirements and errors as fp4_wo_gemm (neither N nor K may be 0 here),
+ * bank->k = K and bank->n = N.
+ */
+FP4_API fp4_status fp4_wo_gemm_lora(const uint16_t* x, int64_t ldx, int64_t m, const fp4_tensor* w,
+                                    const fp4_lora_bank* bank, const int32_t* slots, uint16_t* y, int64_t ldy,
+                                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * fp4_token_logprobs -- for every row z of logits [rows, vocab] (f32 or bf16,
+ * any row stride ld >= vocab, element aligned), with p = softmax(z /
+ * temperature) (quant_prune_distill/574: the rollouts' policy loss reads the
+ * chosen tokens' log probabilities and the policy's entropy):
+ *   logprob[row] = log p[tokens[row]] (0 when the token is outside 0 ..
+ *     vocab - 1, by convention -100: no token); tokens may be null
+ *   entropy[row] = -sum p log p
+ *   top_ids / top_logprobs [rows, top]: the `top` (0 .. 32) largest, largest
+ *     first, equal logits by the lower index; NaN sorts above everything
+ *   stats [rows, 2]: {largest logit, log sum exp((z - largest) / temperature)},
+ *     which the backward call reads
+ * A logit of -inf has probability 0 and adds nothing.  A row of only -inf
+ * has no probability: entropy 0, log probabilities -inf.  A NaN or +inf
+ * makes its own row's results NaN.  Sums in binary32.
+ * workspace: as above, fp4_token_logprobs_workspace bytes.
+ */
+FP4_API int64_t fp4_token_logprobs_workspace(int64_t rows, int64_t vocab, int32_t top);
+FP4_API fp4_status fp4_token_logprobs(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
+                                      const int64_t* tokens, float temperature, int32_t top, float* logprob,
+                                      float* entropy, float* stats, int32_t* top_ids, float* top_logprobs,
+                                      void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * fp4_token_logprobs_backward -- dlogits [rows, vocab] (the logits' type, row
+ * stride ld_d; it may be the logits themselves) for the gradients
+ * grad_logprob and grad_entropy [rows] (either null for zero):
+ *   dz_v = (grad_logprob ([v = token] - p_v)
+ *           - grad_entropy p_v (log p_v + entropy)) / temperature
+ * entropy and stats are the forward call's.  A row whose two gradients are
+ * zero, or whose token is none and whose grad_entropy is zero, gets zeros
+ * whatever its logits hold; so does a row of only -inf.  The top
+ * alternatives carry no gradient.
+ */
+FP4_API fp4_status fp4_token_logprobs_backward(const void* logits, int32_t dtype, int64_t ld, int64_t rows,
+                                               int64_t vocab, const int64_t* tokens, float temperature,
+                                               const float* entropy, const float* stats, const float* grad_logprob,
+                                               const float* grad_entropy, void* dlogits, int64_t ld_d, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * fp4_residual_norm -- the norms after and before a block, fused with its
+ * gate and residual scale (quant_prune_distill/574 "Метод": the RMSNorms
+ * around the FP4 products; reading):
+ *   u = RMSNorm(x) w_post  (u = x when w_post is null)
+ *   h = alpha res + gate u  (gate [rows], binary32; null for 1)
+ *   n = RMSNorm(h) w_pre,  RMSNorm(v) = v / sqrt(mean v^2 + eps)
+ * x and n in x_dtype, res and h in res_dtype, the weights in weight_dtype
+ * (each f32 or bf16); n comes from the unrounded h.  cols at most 32768, any
+ * value and alignment of elements (rows of whole 16-byte vectors, cols % 8
+ * == 0, are read as vectors).  stats [rows, 2] = {1 / sqrt(mean x^2 + eps)
+ * (1 without w_post), 1 / sqrt(mean h^2 + eps)} for the backward call.  h may
+ * be res and n may be x (same row strides). */
+typedef struct fp4_norm {
+    const void* x; int64_t ld_x;
+    const void* res; int64_t ld_res;
+    int64_t rows, cols;
+    const void* w_pre;
+    const void* w_post;
+    const float* gate;
+    float alpha, eps;
+    int32_t x_dtype, res_dtype, weight_dtype;
+} fp4_norm;
+
+FP4_API fp4_status fp4_residual_norm(const fp4_norm* args, void* h, int64_t ld_h, void* n, int64_t ld_n, float* stats,
+                                     void* stream);
+
+/*
+ * fp4_residual_norm_backward -- gradients for dn (of n, x_dtype) and dh (of
+ * h, res_dtype; either null for zero): dx, dres in the types of x and res,
+ * dw_pre and dw_post [cols] and dgate [rows] in binary32 (dw_post, dgate only
+ * where the forward call had w_post, gate).  dx may be x or dn, dres may be
+ * res or dh.  The weights' sums over the rows are taken in a fixed order.
+ * workspace: as above, fp4_residual_norm_workspace bytes (post: w_post given).
+ */
+FP4_API int64_t fp4_residual_norm_workspace(int64_t rows, int64_t cols, int32_t post);
+FP4_API fp4_status fp4_residual_norm_backward(const fp4_norm* args, const float* stats, const void* dn, int64_t ld_dn,
+                                              const void* dh, int64_t ld_dh, void* dx, int64_t ld_dx, void* dres,
+                                              int64_t ld_dres, float* dw_pre, float* dw_post, float* dgate,
+                                              void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 FP4_API const char* fp4_status_string(fp4_status status);
 
