@@ -365,7 +365,7 @@ int64_t fp4_residual_norm_workspace(int64_t rows, int64_t cols, int32_t post)
 {
     if (rows < 0 || cols < 1) return FP4_ERR_SHAPE;
     if (cols > kMaxNormCols || rows >= (int64_t(1) << 31)) return FP4_ERR_UNSUPPORTED;
-    return up16(4 * norm_groups(rows) * (post ? 2 : 1) * cols);
+    return up16(4 * norm_groups(rows, cols) * (post ? 2 : 1) * cols);
 }
 
 fp4_status fp4_residual_norm_backward(const fp4_norm* args, const float* stats, const void* dn, int64_t ld_dn,
@@ -398,7 +398,7 @@ fp4_status fp4_residual_norm_backward(const fp4_norm* args, const float* stats, 
     p.dgate = args->gate ? dgate : nullptr;
     p.part = (float*)workspace;
     p.part_rows = args->w_post ? 2 : 1;
-    p.groups = norm_groups(rows);
+    p.groups = norm_groups(rows, cols);
     // partial rows of odd widths start off the vectors' boundary
     return hip_status(launch_norm_backward(p, vec, (hipStream_t)stream));
 }

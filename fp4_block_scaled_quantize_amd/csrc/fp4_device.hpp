@@ -31,6 +31,15 @@ __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f)
     return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
+// Two fp32 -> packed bf16, nearest even (NaN stays NaN), in the one
+// conversion instruction gfx950 has for it.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    typedef float v2f_ __attribute__((ext_vector_type(2)));
+    typedef __bf16 v2bf_ __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f_{lo, hi}, v2bf_));
+}
+
 // ---------------------------------------------------------------------------
 // block-scale formats
 // ---------------------------------------------------------------------------

@@ -244,8 +244,9 @@ struct NormGradLaunch {
     void* dx; int64_t lddx; void* dres; int64_t lddres;
     float* dw_pre; float* dw_post; float* dgate;
     float* part; int64_t part_rows, groups;               // [groups, part_rows, cols]
+    int32_t sums;              // 1: w_pre's sums and every other output, 2: w_post's sums, 3: all
 };
-int64_t norm_groups(int64_t rows);
+int64_t norm_groups(int64_t rows, int64_t cols);
 hipError_t launch_norm(const NormLaunch& p, bool vec, hipStream_t s);
 hipError_t launch_norm_backward(const NormGradLaunch& p, bool vec, hipStream_t s);
 
