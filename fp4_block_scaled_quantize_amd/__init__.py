@@ -125,7 +125,7 @@ def _check(status: int, what: str):
 
 def _stream(stream, device: torch.device | None = None) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device.index)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -136,11 +136,11 @@ def _on_device(what: str, *tensors: torch.Tensor) -> torch.device:
     one device (the kernels dereference these pointers on that device)."""
     dev = None
     for t in tensors:
-        if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{what}: every tensor must be a CUDA tensor")
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
+            dev, index = t.device, t.get_device()
+        elif t.get_device() != index:
             raise ValueError(f"{what}: tensors on different devices ({dev} and {t.device})")
     return dev
 
@@ -457,9 +457,12 @@ def fp4_wo_gemm(x: torch.Tensor, w: QTensor, out: torch.Tensor | None = None, st
 _LORA_APPLY, _LORA_BACKWARD, _LORA_WO_GEMM = range(3)
 
 
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
 def _allocating(stream, device: torch.device):
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE_AND_NOW
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device)
     return torch.cuda.stream(stream)

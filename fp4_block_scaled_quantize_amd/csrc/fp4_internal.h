@@ -156,8 +156,8 @@ struct LoraDown {
     float* t;                  // [splits, m, rank]
     int64_t kstep;
 };
-// Row tiles of 16 mi rows, K ranges of kstep, z adapters of a tile at once.
-struct LoraDownShape { int mi; int64_t splits, kstep, z; };
+// At most 16 rows or tiles of more, K ranges of kstep, z adapters of a tile at once.
+struct LoraDownShape { bool few; int64_t splits, kstep, z; };
 LoraDownShape lora_down_shape(int64_t m, int64_t k, int rank, int64_t adapters);
 hipError_t launch_lora_down(const LoraDown& p, const LoraDownShape& sh, hipStream_t s);
 
@@ -169,6 +169,7 @@ struct LoraUp {
     const uint16_t* base; int64_t ldbase;                 // null: zero
     uint16_t* y; int64_t ldy;
     float* t_out;              // the joined T [m, rank], if not null
+    int64_t ncols;             // columns of a workgroup
 };
 hipError_t launch_lora_up(const LoraUp& p, hipStream_t s);
 
@@ -200,7 +201,7 @@ hipError_t launch_lora_outer(const LoraOuter& p, int64_t splits, hipStream_t s);
 // ---------------------------------------------------------------------------
 // token log probabilities (logprobs.hip)
 // ---------------------------------------------------------------------------
-constexpr int kLpMaxPieces = 32;
+constexpr int kLpMaxPieces = 32;      // at most a lane of the join for each
 struct LogprobLaunch {
     const void* logits; int32_t bf16; int64_t ld, rows, vocab;
     const int64_t* tokens;     // null: no token given

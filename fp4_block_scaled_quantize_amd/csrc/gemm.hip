@@ -2266,7 +2266,8 @@ __global__ __launch_bounds__(64 * NW) void k_wo_gemm(WoGemmLaunch p)
         const int mr_ = (int)M * p.ad.rank;
         for (int e = tid; e < mr_; e += 64 * NW) {
             float v = 0.0f;
-            for (int s = 0; s < p.ad.splits; ++s) v += p.ad.t[(int64_t)s * mr_ + e];
+#pragma unroll 8
+            for (int s = 0; s < p.ad.splits; ++s) v += p.ad.t[s * mr_ + e];
             ts[e] = v;
         }
     }

@@ -11,6 +11,8 @@
 // binary32: a larger maximum m' = m + D rescales s by f = exp(-c D) and w to
 // f (w - c D s).  The kernels work in powers of two (k = c log2 e), where w
 // carries log2 units.
+#include <type_traits>
+
 #include "fp4_device.hpp"
 #include "fp4_internal.h"
 
@@ -48,22 +50,47 @@ struct Logit<false> {
     }
 };
 
-// Running sums in log2 units.  m is a value of the row (or -inf).
+// Running sums in log2 units, about the maximum m (or -inf).
 struct Sums { float m, s, w; };
 
-// (z - m) k, where a maximum of -inf (nothing finite so far) counts as 0.
-__device__ __forceinline__ float shift2(float z, float m, float k)
-{
-    return (z - (m == -INFINITY ? 0.0f : m)) * k;
-}
-__device__ __forceinline__ void sums_add(Sums& a, float z, float k)
-{
-    const float d = shift2(z, a.m, k);
-    const float e = __builtin_amdgcn_exp2f(d);        // NaN stays NaN
-    a.s += e;
-    a.w = __builtin_fmaf(e, fmaxf(d, -1000.0f), a.w);   // 0 * -inf must not meet the sum
-}
-// raise the maximum to m
+constexpr float kLpFar = 1e30f;        // beyond it m k may leave binary32
+
+// A thread's sums while it reads: about h = RN(m k) instead of m k, so that
+// an element costs one fused product and no subtraction (h only has to be
+// near the maximum); a maximum beyond kLpFar is subtracted first instead.
+struct Running {
+    float m, h, s, w;
+    __device__ __forceinline__ bool far() const { return fabsf(m) > kLpFar && m != -INFINITY; }
+    // raise the maximum to `to`
+    __device__ __forceinline__ void raise(float to, float k)
+    {
+        if (!(to > m)) return;
+        const bool was = far(), first = m == -INFINITY;
+        const float m1 = m, h1 = h;
+        m = to;
+        h = far() ? 0.0f : to * k;
+        if (first) return;                             // nothing but zeros (or NaN) summed yet
+        const float d = fmaxf(was || far() ? (m1 - to) * k : h1 - h, -1000.0f), f = __builtin_amdgcn_exp2f(d);
+        w = f * __builtin_fmaf(d, s, w);
+        s *= f;
+    }
+    template <bool FAR>
+    __device__ __forceinline__ void add(float z, float k)
+    {
+        const float d = FAR ? (z - (m == -INFINITY ? 0.0f : m)) * k : __builtin_fmaf(z, k, -h);
+        const float e = __builtin_amdgcn_exp2f(d);     // NaN stays NaN
+        s += e;
+        w = __builtin_fmaf(e, fmaxf(d, -1000.0f), w);  // 0 * -inf must not meet the sum
+    }
+    // the sums about m k itself
+    __device__ __forceinline__ Sums about_max(float k) const
+    {
+        if (far() || m == -INFINITY) return Sums{m, s, w};
+        const float d = __builtin_fmaf(m, k, -h), f = __builtin_amdgcn_exp2f(-d);
+        return Sums{m, s * f, f * __builtin_fmaf(-d, s, w)};
+    }
+};
+
 __device__ __forceinline__ void sums_raise(Sums& a, float m, float k)
 {
     if (!(m > a.m)) return;
@@ -119,34 +146,53 @@ __device__ __forceinline__ void wave_sync()
 struct TopList {
     uint64_t* buf;
     uint64_t thr;              // keys above it are candidates
+    float value;               // its logit: a smaller one cannot be a candidate
     int cnt, top;
 
+    __device__ __forceinline__ void raise(uint64_t key)
+    {
+        if (key <= thr) return;
+        thr = key;
+        value = key_value(key);
+    }
+    // rank the lane's N keys against the whole buffer and keep the best, sorted
+    template <int N>
+    __device__ __forceinline__ void rank(int lane)
+    {
+        uint64_t mine[N];
+        int at[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) { mine[i] = 64 * i + lane < cnt ? buf[64 * i + lane] : 0; at[i] = 0; }
+        for (int j = 0; j < cnt; j += 8) {             // eight reads in flight
+            uint64_t o[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) o[u] = buf[j + u];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int i = 0; i < N; ++i) at[i] += o[u] > mine[i];
+        }
+        wave_sync();
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (64 * i + lane < cnt && at[i] < top) buf[at[i]] = mine[i];
+    }
     __device__ __forceinline__ void reduce(int lane)
     {
-        uint64_t mine[kLpBuf / 64];
-        int rank[kLpBuf / 64];
+        if (lane < 8 && cnt + lane < kLpBuf) buf[cnt + lane] = 0;       // whole groups of eight
         wave_sync();
-#pragma unroll
-        for (int i = 0; i < kLpBuf / 64; ++i) { mine[i] = 64 * i + lane < cnt ? buf[64 * i + lane] : 0; rank[i] = 0; }
-        for (int j = 0; j < cnt; ++j) {
-            const uint64_t o = buf[j];
-#pragma unroll
-            for (int i = 0; i < kLpBuf / 64; ++i) rank[i] += o > mine[i];
-        }
-        wave_sync();
-#pragma unroll
-        for (int i = 0; i < kLpBuf / 64; ++i)
-            if (64 * i + lane < cnt && rank[i] < top) buf[rank[i]] = mine[i];
+        if (cnt <= 64) rank<1>(lane);
+        else rank<kLpBuf / 64>(lane);
         wave_sync();
         if (cnt > top) cnt = top;
-        if (cnt == top) {
-            const uint64_t last = buf[top - 1];
-            if (last > thr) thr = last;
-        }
+        if (cnt == top) raise(buf[top - 1]);
     }
-    // every lane offers one key
-    __device__ __forceinline__ void offer(uint64_t key, int lane)
+    // every lane offers one element (`in`: it has one)
+    __device__ __forceinline__ void offer(bool in, float z, uint32_t idx, int lane)
     {
+        in = in && !(z < value);                       // NaN passes
+        if (!__builtin_amdgcn_ballot_w64(in)) return;
+        const uint64_t key = in ? sort_key(z, idx) : 0;
         uint64_t want = __builtin_amdgcn_ballot_w64(key > thr);
         if (!want) return;
         if (cnt + __builtin_popcountll(want) > kLpBuf) {
@@ -157,64 +203,115 @@ struct TopList {
         if (key > thr) buf[cnt + __builtin_popcountll(want & ((1ull << lane) - 1))] = key;
         cnt += __builtin_popcountll(want);
     }
-    // a first threshold from one key a lane (0: none)
-    __device__ __forceinline__ void start(uint64_t key)
+    // a first threshold from the lanes' largest logits: below the smallest of
+    // those that fewer than `top` lanes exceed
+    __device__ __forceinline__ void start(bool in, float z)
     {
-        int rank = 0;
-#pragma unroll 8
-        for (int j = 0; j < 64; ++j) {
-            const uint64_t o = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), j) << 32) |
-                               (uint32_t)__builtin_amdgcn_readlane((int)key, j);
-            rank += o > key;
-        }
-        const uint64_t at = __builtin_amdgcn_ballot_w64(key != 0 && rank == top - 1);
-        if (at) {
-            const int j = __builtin_ctzll(at);
-            thr = (((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), j) << 32) |
-                   (uint32_t)__builtin_amdgcn_readlane((int)key, j)) - 1;
-        }
+        const uint32_t v = in ? (uint32_t)(sort_key(z, 0) >> 32) : 0;
+        int at = 0;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) at += (uint32_t)__builtin_amdgcn_readlane((int)v, j) > v;
+        const uint64_t best = __builtin_amdgcn_ballot_w64(v != 0 && at < top);
+        if (__builtin_popcountll(best) < top) return;
+        // the last of them: the lane with the largest count
+        uint32_t low = (best >> (threadIdx.x & 63)) & 1 ? v : 0xFFFFFFFFu;
+#pragma unroll
+        for (int o = 32; o; o >>= 1) { const uint32_t x = __shfl_xor((int)low, o); low = x < low ? x : low; }
+        thr = (uint64_t)low << 32;                     // an index never makes all ones: every key of that value is above
+        value = key_value(thr);
     }
 };
 
-// The best `top` of `n` distinct keys in LDS, sorted, by counting larger ones.
-template <typename F>
-__device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, int top, int tid, int threads, F put)
+__device__ __forceinline__ uint64_t readlane64(uint64_t v, int j)
 {
+    return ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), j) << 32) |
+           (uint32_t)__builtin_amdgcn_readlane((int)v, j);
+}
+__device__ __forceinline__ uint64_t shfl_xor64(uint64_t v, int o)
+{
+    return ((uint64_t)(uint32_t)__shfl_xor((int)(v >> 32), o) << 32) | (uint32_t)__shfl_xor((int)v, o);
+}
+
+// The best `top` keys, sorted, of `lists` sorted lists of at most `top` keys
+// each (at most 64) side by side (zeros, which are no keys, fill a short one).  The last
+// key of a whole list bounds the result from below; the few above the largest
+// such bound are ranked by counting the larger ones.  `few` holds at most
+// lists * top + 8 keys; all `threads` of the workgroup call.
+template <typename F>
+__device__ __forceinline__ void best_of_lists(const uint64_t* keys, int lists, int top, uint64_t* few, int* count, int tid,
+                                              int threads, F put)
+{
+    uint64_t low = 0;
+    const int lane = tid & 63;
+    if (lane < lists) low = keys[(lane + 1) * top - 1];
+#pragma unroll
+    for (int o = 32; o; o >>= 1) { const uint64_t x = shfl_xor64(low, o); low = x > low ? x : low; }
+    if (lists >= top) {                                // many short lists: the top-th of their first keys bounds it closer
+        const uint64_t mine = lane < lists ? keys[lane * top] : 0;
+        int at = 0;
+#pragma unroll 8
+        for (int j = 0; j < 64; ++j) at += readlane64(mine, j) > mine;
+        const uint64_t last = __builtin_amdgcn_ballot_w64(mine != 0 && at == top - 1);
+        if (last) {
+            const uint64_t x = readlane64(mine, __builtin_ctzll(last));
+            low = x > low ? x : low;
+        }
+    }
+    if (tid == 0) *count = 0;
+    __syncthreads();
+    for (int i = tid; i < lists * top; i += threads) {
+        const uint64_t o = keys[i];
+        if (o != 0 && o >= low) few[atomicAdd(count, 1)] = o;      // their order does not matter
+    }
+    __syncthreads();
+    const int n = *count;
+    if (tid < 8) few[n + tid] = 0;
+    __syncthreads();
     for (int i = tid; i < n; i += threads) {
-        const uint64_t mine = keys[i];
-        if (mine == 0) continue;
+        const uint64_t mine = few[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += keys[j] > mine;
+        for (int j = 0; j < n; j += 8) {               // eight reads in flight
+            uint64_t o[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) o[u] = few[j + u];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) rank += o[u] > mine;
+        }
         if (rank < top) put(rank, mine);
     }
 }
 
-// Results of a row from its sums; the token's logit is read again (one
-// element).  A row with no finite logit and no NaN holds no probability:
+// Results of a row from its sums.  A row with no finite logit and no NaN holds no probability:
 // its entropy is 0 and every log probability -inf.
+// The row's token and its logit, fetched ahead of the sums by one thread.
+struct Given { bool is; float z; };
+
 template <bool BF16>
-__device__ __forceinline__ void finish_row(const LogprobLaunch& p, int64_t row, const Sums& r, const uint64_t* keys,
-                                           int nkeys, int tid, int threads)
+__device__ __forceinline__ Given given_token(const LogprobLaunch& p, int64_t row)
 {
     using T = typename Logit<BF16>::Raw;
+    const int64_t t = p.tokens ? p.tokens[row] : -1;
+    const bool is = t >= 0 && t < p.vocab;
+    return Given{is, is ? Logit<BF16>::one((const T*)p.logits + row * p.ld + t) : 0.0f};
+}
+
+__device__ __forceinline__ void finish_row(const LogprobLaunch& p, int64_t row, const Sums& r, const Given& g)
+{
     const float c = p.inv_temperature;
     const bool empty = r.m == -INFINITY && r.s == 0.0f;
     const float m0 = r.m == -INFINITY ? 0.0f : r.m, logs = empty ? 0.0f : logf(r.s);
-    if (tid == 0) {
-        const int64_t t = p.tokens ? p.tokens[row] : -1;
-        float lp = 0.0f;
-        if (t >= 0 && t < p.vocab)
-            lp = empty ? -INFINITY : (Logit<BF16>::one((const T*)p.logits + row * p.ld + t) - m0) * c - logs;
-        if (p.logprob) p.logprob[row] = lp;
-        p.entropy[row] = empty ? 0.0f : logs - r.w * kLn2 / r.s;
-        p.stats[2 * row] = r.m;
-        p.stats[2 * row + 1] = empty ? -INFINITY : logs;
-    }
-    if (p.top > 0)
-        rank_keys(keys, nkeys, p.top, tid, threads, [&](int rank, uint64_t key) {
-            p.top_ids[row * p.top + rank] = (int32_t)key_index(key);
-            p.top_logprobs[row * p.top + rank] = empty ? -INFINITY : (key_value(key) - m0) * c - logs;
-        });
+    if (p.logprob) p.logprob[row] = !g.is ? 0.0f : empty ? -INFINITY : (g.z - m0) * c - logs;
+    p.entropy[row] = empty ? 0.0f : logs - r.w * kLn2 / r.s;
+    p.stats[2 * row] = r.m;
+    p.stats[2 * row + 1] = empty ? -INFINITY : logs;
+}
+
+__device__ __forceinline__ void put_top(const LogprobLaunch& p, int64_t row, const Sums& r, int rank, uint64_t key)
+{
+    const bool empty = r.m == -INFINITY && r.s == 0.0f;
+    const float m0 = r.m == -INFINITY ? 0.0f : r.m;
+    p.top_ids[row * p.top + rank] = (int32_t)key_index(key);
+    p.top_logprobs[row * p.top + rank] = empty ? -INFINITY : (key_value(key) - m0) * p.inv_temperature - logf(r.s);
 }
 
 // ---------------------------------------------------------------------------
@@ -229,115 +326,118 @@ __global__ __launch_bounds__(THREADS) void k_lp_rows(LogprobLaunch p)
     using L = Logit<BF16>;
     using T = typename L::Raw;
     constexpr int NW = THREADS / 64, VN = L::N;
+    constexpr int64_t kRound = (int64_t)THREADS * kLpVec;
     __shared__ uint64_t cand[TOP ? NW * kLpBuf : 1];
+    __shared__ uint64_t lists[TOP ? NW * kLpMaxTop : 1];
+    __shared__ int count;
     __shared__ float sm[NW][3];
-    __shared__ int counts[NW];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t row = blockIdx.x;
     const T* const z = (const T*)p.logits + row * p.ld;
     const int64_t b = (int64_t)blockIdx.y * p.piece, e = b + p.piece < p.vocab ? b + p.piece : p.vocab;
     const float k = p.inv_temperature * kLog2e;
 
-    Sums a{-INFINITY, 0.0f, 0.0f};
-    TopList list{cand + (TOP ? wave * kLpBuf : 0), 0, 0, p.top};
+    Given given{false, 0.0f};
+    if (tid == 0 && gridDim.y == 1) given = given_token<BF16>(p, row);
+    Running a{-INFINITY, 0.0f, 0.0f, 0.0f};
+    TopList list{cand + (TOP ? wave * kLpBuf : 0), 0, -INFINITY, 0, p.top};
     // elements before the first boundary, and after the last whole vector
     const int64_t head = (int64_t)((16 - ((uintptr_t)(z + b) & 15)) & 15) / (int64_t)sizeof(T);
     const int64_t vb = b + head < e ? b + head : e;
     const int64_t nvec = (e - vb) / VN;
     const int64_t ve = vb + nvec * VN;
     const v4i* const zv = reinterpret_cast<const v4i*>(z + vb);
-    bool first = true;
-    for (int64_t r0 = 0; r0 < nvec; r0 += (int64_t)THREADS * kLpVec) {
-        v4i raw[kLpVec];
-        bool in[kLpVec];
+    // the next round's vectors are on their way while this one's are summed
+    v4i next[kLpVec];
+    auto fetch = [&](int64_t r0) {
 #pragma unroll
         for (int u = 0; u < kLpVec; ++u) {
             const int64_t i = r0 + (int64_t)u * THREADS + tid;
-            in[u] = i < nvec;
-            if (in[u]) raw[u] = zv[i];
+            if (i < nvec) next[u] = zv[i];
         }
+    };
+    fetch(0);
+    bool first = true;
+    auto round = [&](int64_t r0, auto whole) {             // whole: every thread has all of its vectors
+        bool in[kLpVec];
         float f[kLpVec][VN], best = -INFINITY;
 #pragma unroll
         for (int u = 0; u < kLpVec; ++u) {
-            if (in[u]) {
-                L::unpack(raw[u], f[u]);
-            } else {
+            in[u] = whole || r0 + (int64_t)u * THREADS + tid < nvec;
+            L::unpack(next[u], f[u]);
+            if (!in[u]) {
 #pragma unroll
                 for (int j = 0; j < VN; ++j) f[u][j] = -INFINITY;
             }
-#pragma unroll
-            for (int j = 0; j < VN; ++j) best = fmaxf(best, f[u][j]);
         }
-        sums_raise(a, best, k);
+        fetch(r0 + kRound);
 #pragma unroll
         for (int u = 0; u < kLpVec; ++u)
 #pragma unroll
-            for (int j = 0; j < VN; ++j) sums_add(a, f[u][j], k);
+            for (int j = 0; j < VN; ++j) best = fmaxf(best, f[u][j]);
+        a.raise(best, k);
+        if (__builtin_amdgcn_ballot_w64(a.far())) {
+#pragma unroll
+            for (int u = 0; u < kLpVec; ++u)
+#pragma unroll
+                for (int j = 0; j < VN; ++j) {
+                    if (a.far()) a.template add<true>(f[u][j], k);
+                    else a.template add<false>(f[u][j], k);
+                }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kLpVec; ++u)
+#pragma unroll
+                for (int j = 0; j < VN; ++j) a.template add<false>(f[u][j], k);
+        }
         if (TOP) {
+            if (first) list.start(in[0], best);
+            first = false;
             // a NaN is above everything and `best` drops it: look at the sum
-            const bool odd = a.s != a.s;
-            if (first) {
-                uint64_t mk = 0;
+            if (__builtin_amdgcn_ballot_w64(!(best < list.value) || a.s != a.s)) {
 #pragma unroll
                 for (int u = 0; u < kLpVec; ++u)
 #pragma unroll
                     for (int j = 0; j < VN; ++j)
-                        if (in[u]) {
-                            const uint64_t key = sort_key(f[u][j], (uint32_t)(vb + (r0 + (int64_t)u * THREADS + tid) * VN + j));
-                            mk = key > mk ? key : mk;
-                        }
-                list.start(mk);
-                first = false;
-            }
-            const uint64_t bk = sort_key(best, 0u);
-            if (__builtin_amdgcn_ballot_w64(bk > list.thr || odd)) {
-#pragma unroll
-                for (int u = 0; u < kLpVec; ++u)
-#pragma unroll
-                    for (int j = 0; j < VN; ++j)
-                        list.offer(in[u] ? sort_key(f[u][j], (uint32_t)(vb + (r0 + (int64_t)u * THREADS + tid) * VN + j)) : 0,
-                                   lane);
+                        list.offer(in[u], f[u][j], (uint32_t)(vb + (r0 + (int64_t)u * THREADS + tid) * VN + j), lane);
             }
         }
-    }
+    };
+    int64_t r0 = 0;
+    for (; r0 + kRound <= nvec; r0 += kRound) round(r0, std::true_type{});
+    if (r0 < nvec) round(r0, std::false_type{});
     // at most VN - 1 elements on either side
-    {
+    if (wave == 0) {
         const int64_t nh = vb - b, nt = e - ve;
         const int64_t i = tid < nh ? b + tid : ve + (tid - nh);
         const bool in = tid < nh + nt;
         const float v = in ? L::one(z + i) : -INFINITY;
-        sums_raise(a, v, k);
-        sums_add(a, v, k);
-        if (TOP && wave == 0) list.offer(in ? sort_key(v, (uint32_t)i) : 0, lane);
-    }
-    if (TOP) {
-        list.reduce(lane);
-        if (lane == 0) counts[wave] = list.cnt;
+        a.raise(v, k);
+        if (a.far()) a.template add<true>(v, k);
+        else a.template add<false>(v, k);
+        if (TOP) list.offer(in, v, (uint32_t)i, lane);
     }
     // threads of the wave, then the waves
+    Sums r = a.about_max(k);
 #pragma unroll
     for (int o = 32; o; o >>= 1) {
-        const float m = __shfl_xor(a.m, o), s = __shfl_xor(a.s, o), w = __shfl_xor(a.w, o);
-        sums_merge(a, m, s, w, k);
+        const float m = __shfl_xor(r.m, o), s = __shfl_xor(r.s, o), w = __shfl_xor(r.w, o);
+        sums_merge(r, m, s, w, k);
     }
-    if (lane == 0) { sm[wave][0] = a.m; sm[wave][1] = a.s; sm[wave][2] = a.w; }
+    if (lane == 0) { sm[wave][0] = r.m; sm[wave][1] = r.s; sm[wave][2] = r.w; }
+    if (TOP) {
+        list.reduce(lane);
+        if (lane < p.top) lists[wave * p.top + lane] = lane < list.cnt ? list.buf[lane] : 0;
+    }
     __syncthreads();
-    Sums r{-INFINITY, 0.0f, 0.0f};
+    r = Sums{-INFINITY, 0.0f, 0.0f};
 #pragma unroll
     for (int w = 0; w < NW; ++w) sums_merge(r, sm[w][0], sm[w][1], sm[w][2], k);
-    int n = 0;
-    if (TOP) {                                        // the waves' lists side by side
-        uint64_t mine = 0;
-        int at = 0;
-        for (int w = 0; w < wave; ++w) at += counts[w];
-        for (int w = 0; w < NW; ++w) n += counts[w];
-        if (lane < counts[wave]) mine = list.buf[lane];
-        __syncthreads();
-        if (lane < counts[wave]) cand[at + lane] = mine;
-        __syncthreads();
-    }
     if (gridDim.y == 1) {
-        finish_row<BF16>(p, row, r, cand, n, tid, THREADS);
+        if (tid == 0) finish_row(p, row, r, given);
+        if (TOP)
+            best_of_lists(lists, NW, p.top, cand, &count, tid, THREADS,
+                          [&](int rank, uint64_t key) { put_top(p, row, r, rank, key); });
         return;
     }
     const int64_t part = row * gridDim.y + blockIdx.y;
@@ -347,28 +447,46 @@ __global__ __launch_bounds__(THREADS) void k_lp_rows(LogprobLaunch p)
     }
     if (TOP) {
         uint64_t* const o = p.part_keys + part * p.top;
-        for (int i = n + tid; i < p.top; i += THREADS) o[i] = 0;      // fewer elements than the list is long
-        rank_keys(cand, n, p.top, tid, THREADS, [&](int rank, uint64_t key) { o[rank] = key; });
+        if (e - b < p.top)                                 // fewer elements than the list is long
+            for (int i = tid; i < p.top; i += THREADS)
+                if (i >= e - b) o[i] = 0;
+        best_of_lists(lists, NW, p.top, cand, &count, tid, THREADS, [&](int rank, uint64_t key) { o[rank] = key; });
     }
 }
 
+constexpr int kLpJoin = 256;           // threads
+
 template <bool BF16, bool TOP>
-__global__ __launch_bounds__(256) void k_lp_join(LogprobLaunch p, int pieces)
+__global__ __launch_bounds__(kLpJoin) void k_lp_join(LogprobLaunch p, int pieces)
 {
     __shared__ uint64_t cand[TOP ? kLpMaxTop * kLpMaxPieces : 1];
+    __shared__ uint64_t few[TOP ? kLpMaxTop * kLpMaxPieces + 8 : 1];
+    __shared__ int count;
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     const float k = p.inv_temperature * kLog2e;
     Sums r{-INFINITY, 0.0f, 0.0f};
-    for (int i = 0; i < pieces; ++i) {
-        const float* const o = p.part_sums + 4 * (row * pieces + i);
-        sums_merge(r, o[0], o[1], o[2], k);
+    Given given{false, 0.0f};
+    if (tid == 0) given = given_token<BF16>(p, row);
+    if (TOP)
+#pragma unroll 4
+        for (int i = tid; i < pieces * p.top; i += kLpJoin) cand[i] = p.part_keys[row * pieces * p.top + i];
+    // a piece for each lane of every wave, joined as the lanes of k_lp_rows are
+    if ((tid & 63) < pieces) {
+        const float* const o = p.part_sums + 4 * (row * pieces + (tid & 63));
+        r = Sums{o[0], o[1], o[2]};
     }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) {
+        const float m = __shfl_xor(r.m, o), s = __shfl_xor(r.s, o), w = __shfl_xor(r.w, o);
+        sums_merge(r, m, s, w, k);
+    }
+    if (tid == 0) finish_row(p, row, r, given);
     if (TOP) {
-        for (int i = tid; i < pieces * p.top; i += 256) cand[i] = p.part_keys[row * pieces * p.top + i];
         __syncthreads();
+        best_of_lists(cand, pieces, p.top, few, &count, tid, kLpJoin,
+                      [&](int rank, uint64_t key) { put_top(p, row, r, rank, key); });
     }
-    finish_row<BF16>(p, row, r, cand, pieces * p.top, tid, 256);
 }
 
 // ---------------------------------------------------------------------------
@@ -434,11 +552,11 @@ __global__ __launch_bounds__(256) void k_lp_backward(LogprobGradLaunch p)
                 for (int j = 0; j < VN; ++j) f[j] = grad(f[j]) + (at == j ? c * gl : 0.0f);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    if constexpr (BF16) out[q] = (int)(f32_to_bf16_rne(f[2 * q]) | (f32_to_bf16_rne(f[2 * q + 1]) << 16));
+                    if constexpr (BF16) out[q] = (int)pack_bf16(f[2 * q], f[2 * q + 1]);
                     else out[q] = (int)f_bits(f[q]);
                 }
             }
-            dv[i] = out;
+            __builtin_nontemporal_store(out, dv + i);     // read next long after it has left the caches
         }
     }
     for (int64_t i = b + tid; i < vb; i += 256) put(i);
@@ -451,12 +569,13 @@ __global__ __launch_bounds__(256) void k_lp_backward(LogprobGradLaunch p)
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // A row stays whole when the rows alone fill the device; else it is cut so
-// that about 512 workgroups run, none with less than one round of its
-// threads (8192 elements).
+// that about 512 workgroups run, none with less than 4096 elements (two bf16
+// vectors a thread: a wave offers its elements to its top list one after the
+// other, which is what a lone row waits for).
 int64_t logprob_pieces(int64_t rows, int64_t vocab)
 {
     if (rows < 1 || rows >= 512) return 1;
-    int64_t n = cdiv(512, rows), most = cdiv(vocab, 8192);
+    int64_t n = cdiv(512, rows), most = cdiv(vocab, 4096);
     n = n < most ? n : most;
     n = n < kLpMaxPieces ? n : kLpMaxPieces;
     return n < 1 ? 1 : n;
@@ -471,7 +590,7 @@ static hipError_t run_logprobs(LogprobLaunch p, int64_t pieces, hipStream_t s)
     hipLaunchKernelGGL((k_lp_rows<BF16, TOP, 256>), grid, dim3(256), 0, s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || pieces == 1) return e;
-    hipLaunchKernelGGL((k_lp_join<BF16, TOP>), dim3((unsigned)p.rows), dim3(256), 0, s, p, (int)pieces);
+    hipLaunchKernelGGL((k_lp_join<BF16, TOP>), dim3((unsigned)p.rows), dim3(TOP ? kLpJoin : 64), 0, s, p, (int)pieces);
     return hipGetLastError();
 }
 

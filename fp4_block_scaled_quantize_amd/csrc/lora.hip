@@ -47,44 +47,153 @@ __device__ __forceinline__ void bf16_terms(float t, uint32_t (&out)[NT])
 }
 
 // ---------------------------------------------------------------------------
-// T = x A_l^T: one workgroup per 16 MI rows and K range, its four waves on
-// quarters of the range, joined through LDS in a fixed order.  Both operands
-// run along K, so each lane's 16 bytes are a matrix-instruction fragment as
-// they come from memory; nothing is staged.  A tile whose rows use several
-// adapters runs its K range once for each (gridDim.z of them side by side)
-// and keeps each row's own.  With gridDim.y > 1 the K ranges' partial sums
-// are left for the reader of T to join.
+// T = x A_l^T for at most 16 rows: one workgroup per K range, its eight waves
+// on every eighth batch of 128 elements, joined through LDS in a fixed order.
+// Both operands run along K, so each lane's 16 bytes are a matrix-instruction
+// fragment as they come from memory; nothing is staged, and a batch's loads
+// leave together: latency is what such a call waits for.  Rows of several
+// adapters run the K range once for each (gridDim.z of them side by side) and
+// keep each row's own.  With gridDim.y > 1 the K ranges' partial sums are left
+// for the reader of T to join.
 // ---------------------------------------------------------------------------
-template <int MI, int RT>
-__global__ __launch_bounds__(256) void k_lora_down(LoraDown p)
+constexpr int kFewWaves = 8;
+
+template <int RT>
+__global__ __launch_bounds__(64 * kFewWaves) void k_lora_down_few(LoraDown p)
 {
-    __shared__ v4f red[4][MI * RT * 64];
+    constexpr int NW = kFewWaves;
+    __shared__ v4f red[NW][RT * 64];
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t m0 = (int64_t)blockIdx.x * (16 * MI);
     const int64_t M = p.m, K = p.k;
     const int R = p.rank;
     float* const t = p.t + (int64_t)blockIdx.y * M * R;
-    const int slot = lane < 16 * MI ? row_slot(p.slots, m0 + lane, M, p.adapters) : -1;
+    const int slot = lane < 16 ? row_slot(p.slots, lane, M, p.adapters) : -1;
 
     if (blockIdx.z == 0) {                    // rows without an adapter
-        for (int i = wave; i < 16 * MI; i += 4)
+        for (int i = wave; i < (int)M; i += NW)
+            if (__builtin_amdgcn_readlane(slot, i) < 0)
+                for (int r = lane; r < R; r += 64) t[i * R + r] = 0.0f;
+    }
+
+    const int64_t kb = (int64_t)blockIdx.y * p.kstep, ke = kb + p.kstep < K ? kb + p.kstep : K;
+    const uint16_t* const xr = p.x + (r16 < M ? r16 : M - 1) * p.ldx + 8 * grp;
+    int64_t ar[RT];
+#pragma unroll
+    for (int j = 0; j < RT; ++j) ar[j] = (int64_t)(16 * j + r16 < R ? 16 * j + r16 : R - 1) * K + 8 * grp;
+
+    uint64_t todo = __builtin_amdgcn_ballot_w64(slot >= 0);
+    for (unsigned nth = 0; todo; ++nth) {
+        const int cur = __builtin_amdgcn_readlane(slot, __builtin_ctzll(todo));
+        const uint64_t match = __builtin_amdgcn_ballot_w64(slot == cur);
+        todo &= ~match;
+        if (nth % gridDim.z != blockIdx.z) continue;
+        const uint16_t* const a = p.a + (int64_t)cur * R * K;
+        v4f acc[RT];
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int64_t k = kb + 128 * wave; k < ke; k += 128 * NW) {
+            const v4i zero{0, 0, 0, 0};
+            v4i xf[4], af[4][RT];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool in = k + 32 * u + 8 * grp < ke;     // 8 elements, all in or all out
+                xf[u] = in ? *reinterpret_cast<const v4i*>(xr + k + 32 * u) : zero;
+#pragma unroll
+                for (int j = 0; j < RT; ++j) af[u][j] = in ? *reinterpret_cast<const v4i*>(a + ar[j] + k + 32 * u) : zero;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < RT; ++j) acc[j] = mfma16(af[u][j], xf[u], acc[j]);
+        }
+        // acc[j][e] = T[m = r16][r = 16 j + 4 grp + e]
+#pragma unroll
+        for (int j = 0; j < RT; ++j) red[wave][j * 64 + lane] = acc[j];
+        __syncthreads();
+        const float s = p.scale ? p.scale[cur] : 1.0f;
+        for (int e = tid; e < RT * 64; e += 64 * NW) {
+            const int l = e & 63, m = l & 15, r = 16 * (e >> 6) + 4 * (l >> 4);
+            if (((match >> m) & 1) && r < R) {
+                v4f v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int w = 0; w < NW; ++w) v += red[w][e];
+                *reinterpret_cast<v4f*>(t + m * R + r) = v * s;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// T = x A_l^T for more rows: one workgroup per 32 rows and K range, its four
+// waves on every fourth chunk of 128 elements.  Bound by reading x, which
+// wants whole lines: fragments taken straight from memory touch 64 bytes of
+// 16 rows at a time (8192 rows of 11008: 71 us that way).  So a wave brings
+// its next chunk (32 rows x 256 bytes) into LDS with direct loads of four rows
+// each while it multiplies the one before; A's fragments, shared by all row
+// tiles, come from the cache.  A 16-byte piece c of row r lies at c ^ (r % 16),
+// so that the 16 rows of a fragment read fall on distinct banks (the lanes
+// pick their global pieces accordingly).  Adapters and K ranges as above.
+// ---------------------------------------------------------------------------
+constexpr int kDownWaves = 4, kDownRows = 32;
+constexpr int kDownSlot = kDownRows * 256;              // bytes of a chunk
+
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+// At most N of the wave's loads still in flight.  The builtin, not inline
+// assembly: the compiler then knows that older loads into registers have
+// landed and adds no wait for everything before their use.
+template <int N>
+__device__ __forceinline__ void wait_loads()
+{
+    static_assert(N < 16, "the low bits of the counter's field");
+    __builtin_amdgcn_s_waitcnt(N | 0x0F70);
+    asm volatile("" ::: "memory");
+}
+
+template <int RT>
+__global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraDown p)
+{
+    constexpr int NW = kDownWaves, MI = kDownRows / 16, ND = kDownSlot / 1024;
+    // two chunks a wave, later the waves' partial tiles
+    __shared__ __align__(16) uint8_t lds[NW * 2 * kDownSlot];
+    static_assert(NW * MI * RT * 1024 <= NW * 2 * kDownSlot, "partial tiles fit");
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, grp = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t m0 = (int64_t)blockIdx.x * kDownRows;
+    const int64_t M = p.m, K = p.k;
+    const int R = p.rank;
+    float* const t = p.t + (int64_t)blockIdx.y * M * R;
+    const int slot = lane < kDownRows ? row_slot(p.slots, m0 + lane, M, p.adapters) : -1;
+
+    if (blockIdx.z == 0) {                    // rows without an adapter
+        for (int i = wave; i < kDownRows; i += NW)
             if (__builtin_amdgcn_readlane(slot, i) < 0 && m0 + i < M)
                 for (int r = lane; r < R; r += 64) t[(m0 + i) * R + r] = 0.0f;
     }
 
     const int64_t kb = (int64_t)blockIdx.y * p.kstep, ke = kb + p.kstep < K ? kb + p.kstep : K;
-    const int64_t kw = p.kstep / 4;                                      // a multiple of 32
-    const int64_t k0 = kb + wave * kw, k1 = k0 + kw < ke ? k0 + kw : ke;
-    const uint16_t* xr[MI];
+    uint8_t* const ring = lds + wave * 2 * kDownSlot;
+    // direct load q of a chunk: lane l brings piece (l % 16) ^ (row % 16) of row 4 q + l / 16
+    const uint16_t* xr[ND];
+    int xp[ND];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int64_t m = m0 + 16 * i + r16;
-        xr[i] = p.x + (m < M ? m : M - 1) * p.ldx + 8 * grp;
+    for (int q = 0; q < ND; ++q) {
+        const int r = 4 * q + (lane >> 4);
+        xr[q] = p.x + (m0 + r < M ? m0 + r : M - 1) * p.ldx;
+        xp[q] = 8 * ((lane & 15) ^ (r & 15));
     }
+    auto bring = [&](int64_t k, int s) {
+#pragma unroll
+        for (int q = 0; q < ND; ++q) {
+            const int64_t at = k + xp[q] < ke ? k + xp[q] : ke - 8;       // past the end: any element, zeroed below
+            __builtin_amdgcn_global_load_lds(xr[q] + at, (lds_ptr_t)(ring + s * kDownSlot + 1024 * q), 16, 0, 0);
+        }
+    };
     int64_t ar[RT];
 #pragma unroll
-    for (int j = 0; j < RT; ++j) ar[j] = (int64_t)(16 * j + r16 < R ? 16 * j + r16 : R - 1) * K + 8 * grp;
+    for (int j = 0; j < RT; ++j) ar[j] = (int64_t)(16 * j + r16 < R ? 16 * j + r16 : R - 1) * K;
 
     uint64_t todo = __builtin_amdgcn_ballot_w64(slot >= 0);
     for (unsigned nth = 0; todo; ++nth) {
@@ -98,49 +207,60 @@ __global__ __launch_bounds__(256) void k_lora_down(LoraDown p)
         for (int i = 0; i < MI; ++i)
 #pragma unroll
             for (int j = 0; j < RT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-        int64_t k = k0;
-        for (; k + 128 <= k1; k += 128) {
-            v4i xf[4][MI], af[4][RT];
+        const int64_t k0 = kb + 128 * wave;
+        if (k0 < ke) bring(k0, 0);
+        int s = 0;
+        for (int64_t k = k0; k < ke; k += 128 * NW, s ^= 1) {
+            const v4i zero{0, 0, 0, 0};
+            v4i af[4][RT];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
+                const int64_t c = k + 32 * u + 8 * grp < ke ? k + 32 * u + 8 * grp : ke - 8;
 #pragma unroll
-                for (int i = 0; i < MI; ++i) xf[u][i] = *reinterpret_cast<const v4i*>(xr[i] + k + 32 * u);
-#pragma unroll
-                for (int j = 0; j < RT; ++j) af[u][j] = *reinterpret_cast<const v4i*>(a + ar[j] + k + 32 * u);
+                for (int j = 0; j < RT; ++j) af[u][j] = *reinterpret_cast<const v4i*>(a + ar[j] + c);
             }
+            // Every load is issued unconditionally (the last chunk is brought
+            // again instead of one past the end), so that the number in flight
+            // is known: this chunk, and A's fragments, are older than the ND
+            // loads of the next one.
+            bring(k + 128 * NW < ke ? k + 128 * NW : k, s ^ 1);
+            wait_loads<ND>();
+            const uint8_t* const at = ring + s * kDownSlot;
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < 4; ++u) {
+                const bool in = k + 32 * u + 8 * grp < ke;     // 8 elements, all in or all out
+                v4i xf[MI];
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    xf[i] = *reinterpret_cast<const v4i*>(at + 256 * (16 * i + r16) + 16 * ((4 * u + grp) ^ r16));
+                    xf[i] = in ? xf[i] : zero;
+                }
+#pragma unroll
+                for (int j = 0; j < RT; ++j) af[u][j] = in ? af[u][j] : zero;
 #pragma unroll
                 for (int i = 0; i < MI; ++i)
 #pragma unroll
-                    for (int j = 0; j < RT; ++j) acc[i][j] = mfma16(af[u][j], xf[u][i], acc[i][j]);
+                    for (int j = 0; j < RT; ++j) acc[i][j] = mfma16(af[u][j], xf[i], acc[i][j]);
+            }
+            // every read of this chunk has returned before its place is filled again
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         }
-        for (; k < k1; k += 32) {
-            const bool in = k + 8 * grp < k1;          // 8 elements, all in or all out
-            const v4i zero{0, 0, 0, 0};
-            v4i xf[MI], af[RT];
-#pragma unroll
-            for (int i = 0; i < MI; ++i) xf[i] = in ? *reinterpret_cast<const v4i*>(xr[i] + k) : zero;
-#pragma unroll
-            for (int j = 0; j < RT; ++j) af[j] = in ? *reinterpret_cast<const v4i*>(a + ar[j] + k) : zero;
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int j = 0; j < RT; ++j) acc[i][j] = mfma16(af[j], xf[i], acc[i][j]);
-        }
+        wait_loads<0>();
+        __syncthreads();
         // acc[i][j][e] = T[m = 16 i + r16][r = 16 j + 4 grp + e]
+        v4f* const red = reinterpret_cast<v4f*>(lds);
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < RT; ++j) red[wave][(i * RT + j) * 64 + lane] = acc[i][j];
+            for (int j = 0; j < RT; ++j) red[((wave * MI + i) * RT + j) * 64 + lane] = acc[i][j];
         __syncthreads();
-        const float s = p.scale ? p.scale[cur] : 1.0f;
-        for (int e = tid; e < MI * RT * 64; e += 256) {
+        const float sc = p.scale ? p.scale[cur] : 1.0f;
+        for (int e = tid; e < MI * RT * 64; e += 64 * NW) {
             const int tile = e >> 6, l = e & 63, i = tile / RT, j = tile % RT;
             const int m = 16 * i + (l & 15), r = 16 * j + 4 * (l >> 4);
             if (((match >> m) & 1) && r < R) {
-                const v4f v = ((red[0][e] + red[1][e]) + (red[2][e] + red[3][e])) * s;
-                *reinterpret_cast<v4f*>(t + (m0 + m) * R + r) = v;
+                const v4f v = (red[e] + red[MI * RT * 64 + e]) + (red[2 * MI * RT * 64 + e] + red[3 * MI * RT * 64 + e]);
+                *reinterpret_cast<v4f*>(t + (m0 + m) * R + r) = v * sc;
             }
         }
         __syncthreads();
@@ -148,116 +268,118 @@ __global__ __launch_bounds__(256) void k_lora_down(LoraDown p)
 }
 
 // ---------------------------------------------------------------------------
-// y = base + s_l T B_l^T: one workgroup per 16 MI rows x 256 columns, 64
-// columns a wave.  The columns of a matrix-instruction pair are dealt so that
-// a lane's eight results are eight consecutive columns of one row: base is
-// read and y written 16 bytes a lane.  T comes from LDS as hi and lo terms;
-// rows of another adapter than the one whose B is multiplied drop the result
-// (a select, so that nothing of one adapter reaches another's rows).
+// y = base + s_l T B_l^T: a wave owns 16 rows, holds their T as hi and lo
+// fragments and walks the columns 64 at a time.  The columns of a
+// matrix-instruction pair are dealt so that a lane's eight results are eight
+// consecutive columns of one row: base is read and y written 16 bytes a lane,
+// 128 bytes a row.  Bound by memory, so the wave is kept small (many in
+// flight) and nothing passes through LDS; the WM waves of a workgroup on
+// neighbouring rows read the same part of B, which the first brings into the
+// cache.  Rows of another adapter than the one whose B is multiplied drop the
+// result (a select, so that nothing of one adapter reaches another's rows).
 // ---------------------------------------------------------------------------
-template <int MI, int RC>
+template <int WM, int RC>
 __global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
 {
-    constexpr int RP = 32 * RC + 4;                     // LDS row pitch (floats)
-    __shared__ __align__(16) float ts[16 * MI][RP];
-    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, grp = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int WN = 4 / WM;                          // waves side by side along the columns
+    const int lane = threadIdx.x & 63, r16 = lane & 15, grp = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t M = p.m, N = p.n;
     const int R = p.rank;
-    const int64_t m0 = (int64_t)blockIdx.y * (16 * MI);
-    const int64_t n0 = (int64_t)blockIdx.x * 256 + 64 * wave + 8 * grp;
-    const int slot = lane < 16 * MI ? row_slot(p.slots, m0 + lane, M, p.adapters) : -1;
+    const int64_t m = ((int64_t)blockIdx.y * WM + wave % WM) * 16 + r16;
+    if (m - r16 >= M) return;
+    const int64_t nb = (int64_t)blockIdx.x * p.ncols, ne = nb + p.ncols < N ? nb + p.ncols : N;
+    const int slot = row_slot(p.slots, m, M, p.adapters);   // the same in the four lanes of a row
+    const bool live = m < M && (slot >= 0 || p.base != p.y);
 
-    v4i old[MI][2];
+    v4i th[RC], tl[RC];
+    {
+        v4f v[RC][2];
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+        for (int c = 0; c < RC; ++c) v[c][0] = v[c][1] = v4f{0.f, 0.f, 0.f, 0.f};
+        if (m < M) {
+            const float* t = p.t + m * R + 8 * grp;
+#pragma unroll 4
+            for (int s = 0; s < p.splits; ++s, t += M * R) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int64_t m = m0 + 16 * i + r16, n = n0 + 32 * u;
-            old[i][u] = p.base && m < M && n < N ? *reinterpret_cast<const v4i*>(p.base + m * p.ldbase + n)
-                                                 : v4i{0, 0, 0, 0};
+                for (int c = 0; c < RC; ++c)
+                    if (32 * c + 8 * grp < R) {
+                        v[c][0] += *reinterpret_cast<const v4f*>(t + 32 * c);
+                        v[c][1] += *reinterpret_cast<const v4f*>(t + 32 * c + 4);
+                    }
+            }
         }
-    for (int e = tid; e < 16 * MI * 8 * RC; e += 256) {
-        const int m = e / (8 * RC), r = 4 * (e % (8 * RC));
-        v4f v{0.f, 0.f, 0.f, 0.f};
-        if (m0 + m < M && r < R) {
-            for (int s = 0; s < p.splits; ++s)
-                v += *reinterpret_cast<const v4f*>(p.t + ((int64_t)s * M + m0 + m) * R + r);
-            if (p.t_out && blockIdx.x == 0) *reinterpret_cast<v4f*>(p.t_out + (m0 + m) * R + r) = v;
-        }
-        *reinterpret_cast<v4f*>(&ts[m][r]) = v;
-    }
-    __syncthreads();
-    v4i th[MI][RC], tl[MI][RC];
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int c = 0; c < RC; ++c)
+        for (int c = 0; c < RC; ++c) {
+            if (p.t_out && blockIdx.x == 0 && wave / WM == 0 && m < M && 32 * c + 8 * grp < R) {
+                *reinterpret_cast<v4f*>(p.t_out + m * R + 32 * c + 8 * grp) = v[c][0];
+                *reinterpret_cast<v4f*>(p.t_out + m * R + 32 * c + 8 * grp + 4) = v[c][1];
+            }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint32_t x0[2], x1[2];
-                bf16_terms<2>(ts[16 * i + r16][32 * c + 8 * grp + 2 * q], x0);
-                bf16_terms<2>(ts[16 * i + r16][32 * c + 8 * grp + 2 * q + 1], x1);
-                th[i][c][q] = (int)(x0[0] | (x1[0] << 16));
-                tl[i][c][q] = (int)(x0[1] | (x1[1] << 16));
+                bf16_terms<2>(v[c][q >> 1][2 * (q & 1)], x0);
+                bf16_terms<2>(v[c][q >> 1][2 * (q & 1) + 1], x1);
+                th[c][q] = (int)(x0[0] | (x1[0] << 16));
+                tl[c][q] = (int)(x0[1] | (x1[1] << 16));
             }
-    int mine[MI];
+        }
+    }
+    const uint64_t used = __builtin_amdgcn_ballot_w64(slot >= 0);
+    const int ncol = 8 * (r16 >> 2) + (r16 & 3);        // this lane's column of B within 32 (+ 4 for the pair's second)
+    for (int64_t n0 = nb + 64 * (wave / WM); n0 < ne; n0 += 64 * WN) {
+        v4i old[2];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) mine[i] = __shfl(slot, 16 * i + r16);
-
-    float o[MI][2][8];
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[i][u][e] = 0.0f;
-    uint64_t todo = __builtin_amdgcn_ballot_w64(slot >= 0);
-    while (todo) {
-        const int cur = __builtin_amdgcn_readlane(slot, __builtin_ctzll(todo));
-        todo &= ~__builtin_amdgcn_ballot_w64(slot == cur);
-        const uint16_t* const b = p.b + (int64_t)cur * N * R;
-        const float s = p.scale ? p.scale[cur] : 1.0f;
+        for (int u = 0; u < 2; ++u) {
+            const int64_t n = n0 + 32 * u + 8 * grp;
+            old[u] = p.base && live && n < ne ? *reinterpret_cast<const v4i*>(p.base + m * p.ldbase + n) : v4i{0, 0, 0, 0};
+        }
+        float o[2][8];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t n = (int64_t)blockIdx.x * 256 + 64 * wave + 32 * u + 8 * (r16 >> 2) + 4 * h + (r16 & 3);
-                const uint16_t* const row = b + (n < N ? n : N - 1) * R + 8 * grp;
-                v4i bf[RC];
+            for (int e = 0; e < 8; ++e) o[u][e] = 0.0f;
+        for (uint64_t todo = used; todo;) {
+            const int cur = __builtin_amdgcn_readlane(slot, __builtin_ctzll(todo));
+            todo &= ~__builtin_amdgcn_ballot_w64(slot == cur);
+            const uint16_t* const b = p.b + (int64_t)cur * N * R + 8 * grp;
+            const float s = p.scale ? p.scale[cur] : 1.0f;
+            v4i bf[2][2][RC];
 #pragma unroll
-                for (int c = 0; c < RC; ++c)
-                    bf[c] = 32 * c + 8 * grp < R ? *reinterpret_cast<const v4i*>(row + 32 * c) : v4i{0, 0, 0, 0};
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < MI; ++i) {
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t n = n0 + 32 * u + 4 * h + ncol;
+                    const uint16_t* const row = b + (n < N ? n : N - 1) * R;
+#pragma unroll
+                    for (int c = 0; c < RC; ++c)
+                        bf[u][h][c] = 32 * c + 8 * grp < R ? *reinterpret_cast<const v4i*>(row + 32 * c) : v4i{0, 0, 0, 0};
+                }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
                     v4f acc{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int c = 0; c < RC; ++c) {
-                        acc = mfma16(bf[c], tl[i][c], acc);
-                        acc = mfma16(bf[c], th[i][c], acc);
+                        acc = mfma16(bf[u][h][c], tl[c], acc);
+                        acc = mfma16(bf[u][h][c], th[c], acc);
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[i][u][4 * h + e] = mine[i] == cur ? acc[e] * s : o[i][u][4 * h + e];
+                    for (int e = 0; e < 4; ++e) o[u][4 * h + e] = slot == cur ? acc[e] * s : o[u][4 * h + e];
                 }
-            }
-    }
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int64_t m = m0 + 16 * i + r16;
+        }
         // a row without an adapter keeps its bits (and is left alone in place)
-        if (m >= M || (mine[i] < 0 && p.base == p.y)) continue;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int64_t n = n0 + 32 * u;
-            if (n >= N) continue;
-            v4i v = old[i][u];
-            if (mine[i] >= 0) {
+            const int64_t n = n0 + 32 * u + 8 * grp;
+            if (!live || n >= ne) continue;
+            v4i v = old[u];
+            if (slot >= 0) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const uint32_t w = (uint32_t)old[i][u][q];
-                    const uint32_t lo = f32_to_bf16_rne(bf16_lo(w) + o[i][u][2 * q]);
-                    const uint32_t hi = f32_to_bf16_rne(bf16_hi(w) + o[i][u][2 * q + 1]);
-                    v[q] = (int)(lo | (hi << 16));
+                    const uint32_t w = (uint32_t)old[u][q];
+                    v[q] = (int)pack_bf16(bf16_lo(w) + o[u][2 * q], bf16_hi(w) + o[u][2 * q + 1]);
                 }
             }
             *reinterpret_cast<v4i*>(p.y + m * p.ldy + n) = v;
@@ -472,21 +594,20 @@ __global__ __launch_bounds__(256) void k_lora_join(LoraOuter p, int splits)
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 static int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-// Row tiles: 64 rows where that leaves registers for the rank's accumulators
-// (MI * RT <= 8), 16 for a batch of at most 16 rows.
-static int down_mi(int64_t m, int rank) { return m <= 16 || rank > 64 ? 1 : rank > 32 ? 2 : 4; }
-
-// K ranges: enough workgroups for every CU, none below 256 elements (64 a
-// wave), at most 32 partial sums for the reader to join.
+// K ranges: enough workgroups for the device (two of four waves on a CU, or
+// many small ones for a few rows), none with less than one chunk a wave, at
+// most 32 partial sums for the reader to join; then the adapters of a tile
+// side by side while that leaves the device unfilled.
 LoraDownShape lora_down_shape(int64_t m, int64_t k, int rank, int64_t adapters)
 {
     LoraDownShape s;
-    s.mi = down_mi(m, rank);
-    const int64_t tiles = cdiv(m, 16 * s.mi);
-    s.splits = clamp64(256 / tiles, 1, clamp64(k / 256, 1, 32));
+    s.few = m <= 16;
+    const int64_t rows = s.few ? 16 : kDownRows, waves = s.few ? kFewWaves : kDownWaves;
+    const int64_t tiles = cdiv(m, rows);
+    s.splits = clamp64(512 / tiles, 1, clamp64(cdiv(k, 128 * waves), 1, 32));
     s.kstep = cdiv(cdiv(k, s.splits), 128) * 128;
     s.splits = cdiv(k, s.kstep);
-    int64_t most = m < 16 * s.mi ? m : 16 * s.mi;
+    int64_t most = m < rows ? m : rows;
     if (adapters < most) most = adapters;
     s.z = clamp64(1024 / (tiles * s.splits), 1, most);
     return s;
@@ -502,11 +623,12 @@ int64_t lora_outer_splits(int64_t m, int64_t n, int64_t k, int rank, int64_t ada
     return clamp64(2048 / groups, 1, clamp64(m / 256, 1, 16));
 }
 
-template <int MI, int RT>
+template <int RT>
 static hipError_t run_down(const LoraDown& p, const LoraDownShape& sh, hipStream_t s)
 {
-    const dim3 grid((unsigned)cdiv(p.m, 16 * MI), (unsigned)sh.splits, (unsigned)sh.z);
-    hipLaunchKernelGGL((k_lora_down<MI, RT>), grid, dim3(256), 0, s, p);
+    const dim3 grid((unsigned)(sh.few ? 1 : cdiv(p.m, kDownRows)), (unsigned)sh.splits, (unsigned)sh.z);
+    if (sh.few) hipLaunchKernelGGL((k_lora_down_few<RT>), grid, dim3(64 * kFewWaves), 0, s, p);
+    else hipLaunchKernelGGL((k_lora_down<RT>), grid, dim3(64 * kDownWaves), 0, s, p);
     return hipGetLastError();
 }
 
@@ -514,22 +636,25 @@ hipError_t launch_lora_down(const LoraDown& in, const LoraDownShape& sh, hipStre
 {
     LoraDown p = in;
     p.kstep = sh.kstep;
-    const int rt = p.rank <= 16 ? 1 : p.rank <= 32 ? 2 : p.rank <= 64 ? 4 : 8;
-    if (sh.mi == 4) return rt == 1 ? run_down<4, 1>(p, sh, s) : run_down<4, 2>(p, sh, s);
-    if (sh.mi == 2) return run_down<2, 4>(p, sh, s);
-    switch (rt) {
-    case 1: return run_down<1, 1>(p, sh, s);
-    case 2: return run_down<1, 2>(p, sh, s);
-    case 4: return run_down<1, 4>(p, sh, s);
-    default: return run_down<1, 8>(p, sh, s);
-    }
+    if (p.rank <= 16) return run_down<1>(p, sh, s);
+    if (p.rank <= 32) return run_down<2>(p, sh, s);
+    if (p.rank <= 64) return run_down<4>(p, sh, s);
+    return run_down<8>(p, sh, s);
 }
 
-template <int MI, int RC>
-static hipError_t run_up(const LoraUp& p, hipStream_t s)
+// Columns of a workgroup: 512 when the row tiles alone fill the device (the
+// rows' T is then read once for eight steps of a wave), fewer where they do
+// not, but at least four for every element of a row of T.
+template <int WM, int RC>
+static hipError_t run_up(const LoraUp& in, hipStream_t s)
 {
-    const dim3 grid((unsigned)cdiv(p.n, 256), (unsigned)cdiv(p.m, 16 * MI));
-    hipLaunchKernelGGL((k_lora_up<MI, RC>), grid, dim3(256), 0, s, p);
+    LoraUp p = in;
+    const int64_t step = 64 * (4 / WM), rows = cdiv(p.m, 16 * WM);
+    const int64_t least = step > 4 * p.rank ? step : 4 * p.rank;
+    const int64_t blocks = clamp64(2048 / rows, cdiv(p.n, 512), cdiv(p.n, least));
+    p.ncols = cdiv(cdiv(p.n, blocks), step) * step;
+    const dim3 grid((unsigned)cdiv(p.n, p.ncols), (unsigned)rows);
+    hipLaunchKernelGGL((k_lora_up<WM, RC>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
@@ -537,7 +662,7 @@ hipError_t launch_lora_up(const LoraUp& p, hipStream_t s)
 {
     const int rc = p.rank <= 32 ? 1 : p.rank <= 64 ? 2 : 4;
     if (p.m <= 16) return rc == 1 ? run_up<1, 1>(p, s) : rc == 2 ? run_up<1, 2>(p, s) : run_up<1, 4>(p, s);
-    return rc == 1 ? run_up<4, 1>(p, s) : rc == 2 ? run_up<4, 2>(p, s) : run_up<2, 4>(p, s);
+    return rc == 1 ? run_up<4, 1>(p, s) : rc == 2 ? run_up<4, 2>(p, s) : run_up<4, 4>(p, s);
 }
 
 hipError_t launch_lora_transpose(const uint16_t* a, uint16_t* at, const uint16_t* b, uint16_t* bt, int64_t adapters,

@@ -33,9 +33,10 @@ def _apply(bank=None, x=FAKE, ldx=256, m=32, slots=FAKE, base=None, ldb=64, y=FA
     (dict(t=None), -1), (dict(t=FAKE + 4), -4), (dict(ws=None), -1), (dict(room=15), -1), (dict(ws=FAKE + 8), -4),
 ])
 def test_apply_rejects_before_launch(kw, want):
-    # 512 K-elements in two ranges need a workspace, so that its checks are reached
+    # a long K is taken in ranges, which need a workspace, so that its checks are reached
     if "bank" not in kw:
-        kw = dict(kw, bank=_bank(k=512), ldx=kw.get("ldx", 512) if kw.get("ldx") not in (248, 260) else kw["ldx"] + 256)
+        k = 65536
+        kw = dict(kw, bank=_bank(k=k), ldx=kw.get("ldx", k) if kw.get("ldx") not in (248, 260) else kw["ldx"] + k - 256)
     assert _apply(**kw) == want
 
 
@@ -109,8 +110,8 @@ def test_logprobs_workspace():
     ws = fq.lib().fp4_token_logprobs_workspace
     assert ws(-1, 5, 0) == -3 and ws(1, 0, 0) == -3 and ws(1, 5, 33) == -2
     assert ws(0, 128000, 5) == 0 and ws(1, 1000, 5) == 0 and ws(512, 128000, 5) == 0
-    assert ws(1, 128000, 20) == 16 * (16 + 160)
-    assert 0 < ws(300, 128000, 32) <= 300 * 32 * (16 + 256)
+    assert 0 < ws(1, 128000, 20) <= 64 * (16 + 160)
+    assert 0 < ws(300, 128000, 32) <= 300 * 64 * (16 + 256)
 
 
 def test_logprobs_backward_rejects_before_launch():
