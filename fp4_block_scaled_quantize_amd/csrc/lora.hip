@@ -33,16 +33,20 @@ __device__ __forceinline__ int row_slot(const int32_t* slots, int64_t row, int64
     return s >= 0 && s < adapters ? s : -1;
 }
 
-// t as NT bf16 terms (each the rounding of what the ones before leave; an
-// infinite term leaves nothing).
+// Two values as NT bf16 terms each, packed (a in the low half): each term the
+// rounding of what the ones before leave.  A value that rounds to infinity
+// leaves nothing, so that it stays one.
 template <int NT>
-__device__ __forceinline__ void bf16_terms(float t, uint32_t (&out)[NT])
+__device__ __forceinline__ void bf16_terms(float a, float b, uint32_t (&out)[NT])
 {
+    constexpr float kTop = 3.3961775e38f;               // the midpoint above the largest bf16
+    const bool fa = !(fabsf(a) >= kTop), fb = !(fabsf(b) >= kTop);
+    out[0] = pack_bf16(a, b);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        out[i] = f32_to_bf16_rne(t);
-        const float h = bits_f(out[i] << 16);
-        t = __builtin_isinf(h) ? 0.0f : t - h;
+    for (int i = 1; i < NT; ++i) {
+        a = fa ? a - bf16_lo(out[i - 1]) : 0.0f;
+        b = fb ? b - bf16_hi(out[i - 1]) : 0.0f;
+        out[i] = pack_bf16(a, b);
     }
 }
 
@@ -129,7 +133,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_lora_down_few(LoraDown p)
 // T = x A_l^T for more rows: one workgroup per 32 rows and K range, its four
 // waves on every fourth chunk of 128 elements.  Bound by reading x, which
 // wants whole lines: fragments taken straight from memory touch 64 bytes of
-// 16 rows at a time (8192 rows of 11008: 71 us that way).  So a wave brings
+// 16 rows at a time (8192 rows of 11008, rank 16: 71 us that way, 42 so, 4.3
+// TB/s).  So a wave brings
 // its next chunk (32 rows x 256 bytes) into LDS with direct loads of four rows
 // each while it multiplies the one before; A's fragments, shared by all row
 // tiles, come from the cache.  A 16-byte piece c of row r lies at c ^ (r % 16),
@@ -269,28 +274,32 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraDown p)
 
 // ---------------------------------------------------------------------------
 // y = base + s_l T B_l^T: a wave owns 16 rows, holds their T as hi and lo
-// fragments and walks the columns 64 at a time.  The columns of a
-// matrix-instruction pair are dealt so that a lane's eight results are eight
-// consecutive columns of one row: base is read and y written 16 bytes a lane,
-// 128 bytes a row.  Bound by memory, so the wave is kept small (many in
-// flight) and nothing passes through LDS; the WM waves of a workgroup on
-// neighbouring rows read the same part of B, which the first brings into the
-// cache.  Rows of another adapter than the one whose B is multiplied drop the
-// result (a select, so that nothing of one adapter reaches another's rows).
+// fragments and walks the columns 64 at a time.  Bound by memory, so the wave
+// is kept small (many in flight) and base and y move in whole 128-byte lines:
+// the products, which leave the matrix instructions as 4 columns of a row a
+// lane, pass through the wave's own 4 KB of LDS and come back as 8 columns a
+// lane, 8 lanes a row.  8192 x 4096, rank 16, 134 MB: 29 us, 4.6 TB/s; the same
+// loads and stores without the products take 28.8.
+// The WM waves of a workgroup on neighbouring rows read the same part of B,
+// which the first brings into the cache.  Rows of another adapter than the
+// one whose B is multiplied drop the result (a select, so that nothing of one
+// adapter reaches another's rows).
 // ---------------------------------------------------------------------------
 template <int WM, int RC>
 __global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
 {
     constexpr int WN = 4 / WM;                          // waves side by side along the columns
+    constexpr int Pitch = 68;                           // floats: 17 times 16 bytes
+    __shared__ __align__(16) float tile[4][16 * Pitch];
     const int lane = threadIdx.x & 63, r16 = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t M = p.m, N = p.n;
     const int R = p.rank;
-    const int64_t m = ((int64_t)blockIdx.y * WM + wave % WM) * 16 + r16;
-    if (m - r16 >= M) return;
+    const int64_t m0 = ((int64_t)blockIdx.y * WM + wave % WM) * 16, m = m0 + r16;
+    if (m0 >= M) return;                                // no barrier below: waves are on their own
     const int64_t nb = (int64_t)blockIdx.x * p.ncols, ne = nb + p.ncols < N ? nb + p.ncols : N;
     const int slot = row_slot(p.slots, m, M, p.adapters);   // the same in the four lanes of a row
-    const bool live = m < M && (slot >= 0 || p.base != p.y);
+    float* const out = tile[wave];
 
     v4i th[RC], tl[RC];
     {
@@ -317,74 +326,125 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                uint32_t x0[2], x1[2];
-                bf16_terms<2>(v[c][q >> 1][2 * (q & 1)], x0);
-                bf16_terms<2>(v[c][q >> 1][2 * (q & 1) + 1], x1);
-                th[c][q] = (int)(x0[0] | (x1[0] << 16));
-                tl[c][q] = (int)(x0[1] | (x1[1] << 16));
+                uint32_t x[2];
+                bf16_terms<2>(v[c][q >> 1][2 * (q & 1)], v[c][q >> 1][2 * (q & 1) + 1], x);
+                th[c][q] = (int)x[0];
+                tl[c][q] = (int)x[1];
             }
         }
     }
     const uint64_t used = __builtin_amdgcn_ballot_w64(slot >= 0);
-    const int ncol = 8 * (r16 >> 2) + (r16 & 3);        // this lane's column of B within 32 (+ 4 for the pair's second)
-    for (int64_t n0 = nb + 64 * (wave / WM); n0 < ne; n0 += 64 * WN) {
-        v4i old[2];
+    // this lane's part of y: rows i and i + 8, 8 columns; a row without an
+    // adapter keeps base's bits (and is left alone in place)
+    const int yr = lane >> 3, yc = 8 * (lane & 7);
+    int has[2];
+    bool live[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int64_t n = n0 + 32 * u + 8 * grp;
-            old[u] = p.base && live && n < ne ? *reinterpret_cast<const v4i*>(p.base + m * p.ldbase + n) : v4i{0, 0, 0, 0};
-        }
-        float o[2][8];
+    for (int u = 0; u < 2; ++u) {
+        has[u] = __shfl(slot, yr + 8 * u) >= 0;
+        live[u] = m0 + yr + 8 * u < M && (has[u] || p.base != p.y);
+    }
+    const uint16_t* const base = p.base ? p.base + (m0 + yr) * p.ldbase + yc : nullptr;
+    uint16_t* const y = p.y + (m0 + yr) * p.ldy + yc;
+    v4i next[2];
+    auto fetch = [&](int64_t n0) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            next[u] = base && live[u] && n0 + yc < ne ? *reinterpret_cast<const v4i*>(base + 8 * u * p.ldbase + n0)
+                                                      : v4i{0, 0, 0, 0};
+    };
+    // B's fragments: tile (u, h) holds columns n0 + 32 u + 16 h + r16
+    v4i bf[2][2][RC];
+    auto load_b = [&](int cur, int64_t n0) {
+        const uint16_t* const b = p.b + (int64_t)cur * N * R + 8 * grp;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[u][e] = 0.0f;
-        for (uint64_t todo = used; todo;) {
-            const int cur = __builtin_amdgcn_readlane(slot, __builtin_ctzll(todo));
-            todo &= ~__builtin_amdgcn_ballot_w64(slot == cur);
-            const uint16_t* const b = p.b + (int64_t)cur * N * R + 8 * grp;
-            const float s = p.scale ? p.scale[cur] : 1.0f;
-            v4i bf[2][2][RC];
+            for (int h = 0; h < 2; ++h) {
+                const int64_t n = n0 + 32 * u + 16 * h + r16;
+                const uint16_t* const row = b + (n < N ? n : N - 1) * R;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+                for (int c = 0; c < RC; ++c)
+                    bf[u][h][c] = 32 * c + 8 * grp < R ? *reinterpret_cast<const v4i*>(row + 32 * c) : v4i{0, 0, 0, 0};
+            }
+    };
+    auto multiply = [&](int cur, float s, v4f (&o)[2][2]) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t n = n0 + 32 * u + 4 * h + ncol;
-                    const uint16_t* const row = b + (n < N ? n : N - 1) * R;
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int c = 0; c < RC; ++c)
-                        bf[u][h][c] = 32 * c + 8 * grp < R ? *reinterpret_cast<const v4i*>(row + 32 * c) : v4i{0, 0, 0, 0};
+            for (int h = 0; h < 2; ++h) {
+                v4f acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < RC; ++c) {
+                    acc = mfma16(bf[u][h][c], tl[c], acc);
+                    acc = mfma16(bf[u][h][c], th[c], acc);
                 }
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+                for (int e = 0; e < 4; ++e) o[u][h][e] = slot == cur ? acc[e] * s : o[u][h][e];
+            }
+    };
+    // the tile's only adapter (-1: several, or none): its next columns of B
+    // are loaded while these are written (larger ranks' fragments would cost
+    // a wave of the SIMD's four: rank 64, 1111 rows, 32 us against 26)
+    int one = used ? __builtin_amdgcn_readlane(slot, __builtin_ctzll(used)) : -1;
+    if (RC > 1 || (used & ~__builtin_amdgcn_ballot_w64(slot == one))) one = -1;
+    const float scale1 = one >= 0 && p.scale ? p.scale[one] : 1.0f;
+    if (one >= 0) load_b(one, nb + 64 * (wave / WM));
+    fetch(nb + 64 * (wave / WM));
+    for (int64_t n0 = nb + 64 * (wave / WM); n0 < ne; n0 += 64 * WN) {
+        v4i old[2]{next[0], next[1]};
+        v4f o[2][2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    v4f acc{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < RC; ++c) {
-                        acc = mfma16(bf[u][h][c], tl[c], acc);
-                        acc = mfma16(bf[u][h][c], th[c], acc);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[u][4 * h + e] = slot == cur ? acc[e] * s : o[u][4 * h + e];
-                }
+        for (int u = 0; u < 2; ++u) o[u][0] = o[u][1] = v4f{0.f, 0.f, 0.f, 0.f};
+        if (one >= 0) {
+            multiply(one, scale1, o);
+            load_b(one, n0 + 64 * WN);
+        } else {
+            for (uint64_t todo = used; todo;) {
+                const int cur = __builtin_amdgcn_readlane(slot, __builtin_ctzll(todo));
+                todo &= ~__builtin_amdgcn_ballot_w64(slot == cur);
+                load_b(cur, n0);
+                multiply(cur, p.scale ? p.scale[cur] : 1.0f, o);
+            }
         }
-        // a row without an adapter keeps its bits (and is left alone in place)
+        fetch(n0 + 64 * WN);
+        // o[u][h][e]: row r16, column 32 u + 16 h + 4 grp + e
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<v4f*>(out + Pitch * r16 + 32 * u + 16 * h + 4 * grp) = o[u][h];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int64_t n = n0 + 32 * u + 8 * grp;
-            if (!live || n >= ne) continue;
+            const v4f d0 = *reinterpret_cast<const v4f*>(out + Pitch * (yr + 8 * u) + yc);
+            const v4f d1 = *reinterpret_cast<const v4f*>(out + Pitch * (yr + 8 * u) + yc + 4);
             v4i v = old[u];
-            if (slot >= 0) {
+            if (has[u]) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint32_t w = (uint32_t)old[u][q];
-                    v[q] = (int)pack_bf16(bf16_lo(w) + o[u][2 * q], bf16_hi(w) + o[u][2 * q + 1]);
+                    const v4f& d = q < 2 ? d0 : d1;
+                    v[q] = (int)pack_bf16(bf16_lo(w) + d[2 * (q & 1)], bf16_hi(w) + d[2 * (q & 1) + 1]);
                 }
             }
-            *reinterpret_cast<v4i*>(p.y + m * p.ldy + n) = v;
+            if (live[u] && n0 + yc < ne) *reinterpret_cast<v4i*>(y + 8 * u * p.ldy + n0) = v;
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
+}
+
+// T as the sum of its K ranges' partial sums.
+__global__ __launch_bounds__(256) void k_lora_sum(const float* parts, int splits, int64_t n, float* t)
+{
+    const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (e >= n) return;
+    v4f v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const v4f*>(parts + s * n + e);
+    *reinterpret_cast<v4f*>(t + e) = v;
 }
 
 // ---------------------------------------------------------------------------
@@ -436,9 +496,12 @@ __global__ __launch_bounds__(256) void k_lora_transpose(LoraTranspose p)
 // rows, skips the chunks without a row of l and zeroes other adapters' rows
 // in both operands (an infinity there must not meet a zero).  Row ranges
 // (gridDim.z) leave partial sums, joined in a fixed order by k_lora_join.
+// Bound by reading D (once, past the caches): 8192 x (4096 + 11008), rank 16,
+// 247 MB: 51 us, 4.9 TB/s; 63 us through the caches and with a chunk's loads
+// waiting for its rows' adapters.
 // ---------------------------------------------------------------------------
 template <int RT, int NT>
-__global__ __launch_bounds__(256) void k_lora_outer(LoraOuter p)
+__global__ __launch_bounds__(256, RT == 1 ? 3 : RT == 2 ? 2 : 1) void k_lora_outer(LoraOuter p)
 {
     __shared__ v4f red[8 * RT * 64];
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, grp = lane >> 4;
@@ -457,56 +520,93 @@ __global__ __launch_bounds__(256) void k_lora_outer(LoraOuter p)
     for (int ci = 0; ci < 8; ++ci)
 #pragma unroll
         for (int j = 0; j < RT; ++j) acc[ci][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    int any = 0;
-    for (int64_t mc = mb + 32 * wave; mc < me; mc += 128) {
-        const int s = lane < 32 ? row_slot(p.slots, mc + lane, me, p.adapters) : -1;
-        const uint32_t rows = (uint32_t)__builtin_amdgcn_ballot_w64(s == l);
-        if (rows == 0) continue;
-        any = 1;
-        const uint32_t keep = (rows >> (8 * grp)) & 0xFFu;
-        v4i d[8];
-        float pv[RT][8];
+    // A chunk is loaded while the one before is multiplied, and its rows'
+    // adapters while that one is loaded.
+    v4i d[8];
+    float pv[RT][8];
+    int pcol[RT];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t m = mc + 8 * grp + j < M ? mc + 8 * grp + j : M - 1;
-            d[j] = *reinterpret_cast<const v4i*>(job.d + m * job.ldd + cl);
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-                const int r = 16 * (rg * RT + t) + r16;
-                pv[t][j] = job.p[m * R + (r < R ? r : R - 1)];
-            }
-        }
-        if (rows != 0xFFFFFFFFu) {
+    for (int t = 0; t < RT; ++t) {
+        const int r = 16 * (rg * RT + t) + r16;
+        pcol[t] = r < R ? r : R - 1;
+    }
+    auto load = [&](int64_t mc) {
+        if (mc + 32 <= M) {
+            const uint16_t* const row = job.d + (mc + 8 * grp) * job.ldd + cl;
+            const float* const pr = job.p + (mc + 8 * grp) * R;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const bool in = (keep >> j) & 1;
-                d[j] = in ? d[j] : v4i{0, 0, 0, 0};
+                d[j] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(row + j * job.ldd));
 #pragma unroll
-                for (int t = 0; t < RT; ++t) pv[t][j] = in ? pv[t][j] : 0.0f;
+                for (int t = 0; t < RT; ++t) pv[t][j] = pr[j * R + pcol[t]];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int64_t m = mc + 8 * grp + j < M ? mc + 8 * grp + j : M - 1;
+                d[j] = *reinterpret_cast<const v4i*>(job.d + m * job.ldd + cl);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) pv[t][j] = job.p[m * R + pcol[t]];
             }
         }
+    };
+    // a chunk's adapters, one row a lane, read here and looked at a chunk
+    // later: waiting for them at once would wait for the rows as well
+    auto slots_of = [&](int64_t mc) { return p.slots[mc + (lane & 31) < M ? mc + (lane & 31) : M - 1]; };
+    auto rows_of = [&](int s, int64_t mc) {
+        return (uint32_t)__builtin_amdgcn_ballot_w64(lane < 32 && s == l && mc + lane < me);
+    };
+    int any = 0;
+    int64_t mc = mb + 32 * wave;
+    uint32_t rows = 0;
+    int ahead = -1;
+    if (mc < me) {
+        rows = rows_of(slots_of(mc), mc);
+        if (rows) load(mc);
+        ahead = slots_of(mc + 128);
+    }
+    for (; mc < me; mc += 128) {
+        const uint32_t now = rows;
+        v4i f[8];
         v4i pf[RT][NT];
+        if (now) {
+            any = 1;
+            const uint32_t keep = (now >> (8 * grp)) & 0xFFu;
+            if (now != 0xFFFFFFFFu) {
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+                for (int j = 0; j < 8; ++j) {
+                    const bool in = (keep >> j) & 1;
+                    d[j] = in ? d[j] : v4i{0, 0, 0, 0};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t x0[NT], x1[NT];
-                bf16_terms<NT>(pv[t][2 * q], x0);
-                bf16_terms<NT>(pv[t][2 * q + 1], x1);
-#pragma unroll
-                for (int i = 0; i < NT; ++i) pf[t][i][q] = (int)(x0[i] | (x1[i] << 16));
+                    for (int t = 0; t < RT; ++t) pv[t][j] = in ? pv[t][j] : 0.0f;
+                }
             }
-#pragma unroll
-        for (int ci = 0; ci < 8; ++ci) {
-            v4i f;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                f[q] = (int)__builtin_amdgcn_perm((uint32_t)d[2 * q + 1][ci >> 1], (uint32_t)d[2 * q][ci >> 1],
-                                                  (ci & 1) ? 0x07060302u : 0x05040100u);
 #pragma unroll
             for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int i = NT - 1; i >= 0; --i) acc[ci][t] = mfma16(f, pf[t][i], acc[ci][t]);
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t x[NT];
+                    bf16_terms<NT>(pv[t][2 * q], pv[t][2 * q + 1], x);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) pf[t][i][q] = (int)x[i];
+                }
+#pragma unroll
+            for (int ci = 0; ci < 8; ++ci)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    f[ci][q] = (int)__builtin_amdgcn_perm((uint32_t)d[2 * q + 1][ci >> 1], (uint32_t)d[2 * q][ci >> 1],
+                                                          (ci & 1) ? 0x07060302u : 0x05040100u);
+        }
+        rows = rows_of(ahead, mc + 128);
+        ahead = slots_of(mc + 256);
+        if (rows) load(mc + 128);
+        if (now) {
+#pragma unroll
+            for (int ci = 0; ci < 8; ++ci)
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int i = NT - 1; i >= 0; --i) acc[ci][t] = mfma16(f[ci], pf[t][i], acc[ci][t]);
         }
     }
     any = __syncthreads_or(any);
@@ -594,10 +694,12 @@ __global__ __launch_bounds__(256) void k_lora_join(LoraOuter p, int splits)
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 static int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
 
-// K ranges: enough workgroups for the device (two of four waves on a CU, or
-// many small ones for a few rows), none with less than one chunk a wave, at
-// most 32 partial sums for the reader to join; then the adapters of a tile
-// side by side while that leaves the device unfilled.
+// K ranges: about two workgroups of four waves for a CU (or many small ones
+// for a few rows), none with less than one chunk a wave, at most 32 partial
+// sums for the reader to join; four for a CU where each still has four chunks
+// a wave or more (8192 rows of 11008: 42 us against 47; of 4096, where it would
+// not: 25 against 18).  Then the adapters of a tile side by side while that
+// leaves the device unfilled.
 LoraDownShape lora_down_shape(int64_t m, int64_t k, int rank, int64_t adapters)
 {
     LoraDownShape s;
@@ -605,6 +707,8 @@ LoraDownShape lora_down_shape(int64_t m, int64_t k, int rank, int64_t adapters)
     const int64_t rows = s.few ? 16 : kDownRows, waves = s.few ? kFewWaves : kDownWaves;
     const int64_t tiles = cdiv(m, rows);
     s.splits = clamp64(512 / tiles, 1, clamp64(cdiv(k, 128 * waves), 1, 32));
+    const int64_t deep = clamp64(1024 / tiles, 1, k / (4 * 128 * waves));
+    if (!s.few && deep > s.splits) s.splits = deep < 32 ? deep : 32;
     s.kstep = cdiv(cdiv(k, s.splits), 128) * 128;
     s.splits = cdiv(k, s.kstep);
     int64_t most = m < rows ? m : rows;
@@ -613,14 +717,21 @@ LoraDownShape lora_down_shape(int64_t m, int64_t k, int rank, int64_t adapters)
     return s;
 }
 
-// The row ranges of the gradient sums: enough workgroups to fill the device
-// when the rows of the adapters are about even, at least 256 rows each (two
-// chunks a wave).  Many adapters fill it by themselves, and a range costs a
-// partial sum of every adapter's gradient.
+static int outer_rt(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
+
+// The row ranges of the gradient sums, at least 256 rows each (two chunks a
+// wave).  A range's rows are mostly one adapter's, so about column tiles x
+// ranges workgroups have work whatever the number of adapters: as many as run
+// at once (three, two or one on a CU, by their registers), since a second,
+// half-empty round costs as much as the first.  A range also costs a partial sum of
+// every adapter's gradient: 256 MB of them at most.
 int64_t lora_outer_splits(int64_t m, int64_t n, int64_t k, int rank, int64_t adapters)
 {
-    const int64_t groups = (cdiv(n, 128) + cdiv(k, 128)) * adapters * cdiv(rank, 64);
-    return clamp64(2048 / groups, 1, clamp64(m / 256, 1, 16));
+    const int rt = outer_rt(rank);
+    const int64_t tiles = (cdiv(n, 128) + cdiv(k, 128)) * cdiv(rank, 16 * rt);
+    const int64_t fit = 256 * (rt == 1 ? 3 : rt == 2 ? 2 : 1) / tiles;
+    const int64_t part = 4 * adapters * rank * (n + k);
+    return clamp64(fit, 1, clamp64(m / 256, 1, clamp64((int64_t(256) << 20) / part, 1, 16)));
 }
 
 template <int RT>
@@ -651,8 +762,19 @@ static hipError_t run_up(const LoraUp& in, hipStream_t s)
     LoraUp p = in;
     const int64_t step = 64 * (4 / WM), rows = cdiv(p.m, 16 * WM);
     const int64_t least = step > 4 * p.rank ? step : 4 * p.rank;
-    const int64_t blocks = clamp64(2048 / rows, cdiv(p.n, 512), cdiv(p.n, least));
+    const int64_t blocks = clamp64(1024 / rows, cdiv(p.n, 512), cdiv(p.n, least));
     p.ncols = cdiv(cdiv(p.n, blocks), step) * step;
+    // every column block reads its rows' T: past 16 MB of partial sums (from
+    // the caches) a launch that joins them once costs less than the difference
+    if (p.splits > 1 && 4 * p.m * p.rank * p.splits * cdiv(p.n, p.ncols) > (int64_t(16) << 20)) {
+        const int64_t n = p.m * p.rank;
+        hipLaunchKernelGGL(k_lora_sum, dim3((unsigned)cdiv(n, 1024)), dim3(256), 0, s, p.t, p.splits, n, p.t_out);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        p.t = p.t_out;
+        p.splits = 1;
+        p.t_out = nullptr;
+    }
     const dim3 grid((unsigned)cdiv(p.n, p.ncols), (unsigned)rows);
     hipLaunchKernelGGL((k_lora_up<WM, RC>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
@@ -691,8 +813,9 @@ hipError_t launch_lora_outer(const LoraOuter& in, int64_t splits, hipStream_t s)
     p.tiles[1] = (int32_t)cdiv(p.job[1].c, 128);
     p.mstep = cdiv(cdiv(p.m, splits), 128) * 128;
     hipError_t e;
-    if (p.rank <= 16) e = p.out_bf16 ? run_outer<1, 2>(p, splits, s) : run_outer<1, 3>(p, splits, s);
-    else if (p.rank <= 32) e = p.out_bf16 ? run_outer<2, 2>(p, splits, s) : run_outer<2, 3>(p, splits, s);
+    const int rt = outer_rt(p.rank);
+    if (rt == 1) e = p.out_bf16 ? run_outer<1, 2>(p, splits, s) : run_outer<1, 3>(p, splits, s);
+    else if (rt == 2) e = p.out_bf16 ? run_outer<2, 2>(p, splits, s) : run_outer<2, 3>(p, splits, s);
     else e = p.out_bf16 ? run_outer<4, 2>(p, splits, s) : run_outer<4, 3>(p, splits, s);
     if (e != hipSuccess || splits == 1) return e;
     const int64_t most = p.adapters * p.rank * (p.job[0].c > p.job[1].c ? p.job[0].c : p.job[1].c);
