@@ -15,6 +15,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -58,6 +59,11 @@ class Fp4NormC(ctypes.Structure):
                 ("weight_dtype", ctypes.c_int32)]
 
 
+# Fp4NormC's layout; packing it costs a third of filling a ctypes.Structure.
+_NORM_ARGS = struct.Struct("@PqPqqqPPPffiii4x")
+assert _NORM_ARGS.size == ctypes.sizeof(Fp4NormC)
+
+
 class Fp4Error(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -77,7 +83,7 @@ def lib():
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, u64, u32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_uint32
     f32 = ctypes.c_float
-    T, LB, NA = ctypes.POINTER(Fp4TensorC), ctypes.POINTER(Fp4LoraBankC), ctypes.POINTER(Fp4NormC)
+    T, LB = ctypes.POINTER(Fp4TensorC), ctypes.POINTER(Fp4LoraBankC)
     sig = {
         "fp4_version": (i32, []),
         "fp4_status_string": (ctypes.c_char_p, [i32]),
@@ -102,9 +108,9 @@ def lib():
         "fp4_token_logprobs_workspace": (i64, [i64, i64, i32]),
         "fp4_token_logprobs": (i32, [vp, i32, i64, i64, i64, vp, f32, i32, vp, vp, vp, vp, vp, vp, i64, vp]),
         "fp4_token_logprobs_backward": (i32, [vp, i32, i64, i64, i64, vp, f32, vp, vp, vp, vp, vp, i64, vp]),
-        "fp4_residual_norm": (i32, [NA, vp, i64, vp, i64, vp, vp]),
+        "fp4_residual_norm": (i32, [vp, vp, i64, vp, i64, vp, vp]),
         "fp4_residual_norm_workspace": (i64, [i64, i64, i32]),
-        "fp4_residual_norm_backward": (i32, [NA, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp]),
+        "fp4_residual_norm_backward": (i32, [vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -595,7 +601,7 @@ def fp4_lora_backward(dy: torch.Tensor, x: torch.Tensor, t: torch.Tensor, bank: 
     L = lib()
     with _allocating(stream, dev):
         if dx is None:
-            dx = torch.empty((m, tb.k), dtype=torch.bfloat16, device=dev)
+            dx = _empty_as(x)
         else:
             _check_dense_out(dx, (m, tb.k), (torch.bfloat16,), "fp4_lora_backward")
         da = torch.empty(bank.a.shape, dtype=grad_dtype, device=dev)
@@ -673,7 +679,7 @@ def fp4_token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor | Non
                      *(t for t in (tokens, grad_logprob, grad_entropy, out) if t is not None))
     with _allocating(stream, dev):
         if out is None:
-            out = torch.empty((n, v), dtype=logits.dtype, device=dev)
+            out = _empty_as(logits)
         elif out.dtype != logits.dtype or not _is_rows(out, v, n):
             raise ValueError(f"{what}: out must be [{n}, {v}] of the logits' dtype with unit column stride")
         st = lib().fp4_token_logprobs_backward(logits.data_ptr(), DTYPE[logits.dtype], _ld(logits), n, v, _ptr(tokens),
@@ -684,17 +690,22 @@ def fp4_token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor | Non
     return out
 
 
-def _norm_args(what: str, x, res, w_pre, w_post, gate, alpha, eps) -> Fp4NormC:
+def _norm_args(what: str, x, res, w_pre, w_post, gate, alpha, eps) -> bytes:
     if x.dtype not in DTYPE or not _is_rows(x) or res.dtype not in DTYPE or not _is_rows(res, x.shape[1], x.shape[0]):
         raise ValueError(f"{what}: x and res must be float32 or bfloat16 [rows, cols] tensors with unit column stride")
     m, c = x.shape
-    if w_pre.dtype not in DTYPE or not _is_vector(w_pre, c, w_pre.dtype) or \
-            (w_post is not None and not _is_vector(w_post, c, w_pre.dtype)):
+    wd = w_pre.dtype
+    if wd not in DTYPE or not _is_vector(w_pre, c, wd) or (w_post is not None and not _is_vector(w_post, c, wd)):
         raise ValueError(f"{what}: weights must be dense [{c}] vectors of one dtype, float32 or bfloat16")
     if gate is not None and not _is_vector(gate, m, torch.float32):
         raise ValueError(f"{what}: gate must be float32 [{m}]")
-    return Fp4NormC(x.data_ptr(), _ld(x), res.data_ptr(), _ld(res), m, c, w_pre.data_ptr(), _ptr(w_post), _ptr(gate),
-                    alpha, eps, DTYPE[x.dtype], DTYPE[res.dtype], DTYPE[w_pre.dtype])
+    return _NORM_ARGS.pack(x.data_ptr(), _ld(x), res.data_ptr(), _ld(res), m, c, w_pre.data_ptr(),
+                           0 if w_post is None else w_post.data_ptr(), 0 if gate is None else gate.data_ptr(),
+                           alpha, eps, DTYPE[x.dtype], DTYPE[res.dtype], DTYPE[wd])
+
+
+def _empty_as(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def fp4_residual_norm(x: torch.Tensor, res: torch.Tensor, w_pre: torch.Tensor, w_post: torch.Tensor | None = None,
@@ -706,10 +717,9 @@ def fp4_residual_norm(x: torch.Tensor, res: torch.Tensor, w_pre: torch.Tensor, w
     dev = _on_device("fp4_residual_norm", x, res, w_pre, *(t for t in (w_post, gate) if t is not None))
     m, c = x.shape
     with _allocating(stream, dev):
-        h = torch.empty((m, c), dtype=res.dtype, device=dev)
-        n = torch.empty((m, c), dtype=x.dtype, device=dev)
+        h, n = _empty_as(res), _empty_as(x)
         stats = torch.empty((m, 2), dtype=torch.float32, device=dev)
-        st = lib().fp4_residual_norm(ctypes.byref(args), h.data_ptr(), c, n.data_ptr(), c, stats.data_ptr(),
+        st = lib().fp4_residual_norm(args, h.data_ptr(), c, n.data_ptr(), c, stats.data_ptr(),
                                      _stream(stream, dev))
     _check(st, "fp4_residual_norm")
     return h, n, stats
@@ -742,13 +752,12 @@ def fp4_residual_norm_backward(dn: torch.Tensor | None, dh: torch.Tensor | None,
     dev = _on_device(what, x, res, w_pre, stats, *(t for t in (dn, dh, w_post, gate) if t is not None))
     L = lib()
     with _allocating(stream, dev):
-        dx = torch.empty((m, c), dtype=x.dtype, device=dev)
-        dres = torch.empty((m, c), dtype=res.dtype, device=dev)
+        dx, dres = _empty_as(x), _empty_as(res)
         dw_pre = torch.empty(c, dtype=torch.float32, device=dev)
         dw_post = torch.empty(c, dtype=torch.float32, device=dev) if w_post is not None else None
-        dgate = torch.empty(m, dtype=torch.float32, device=dev) if gate is not None else None
+        dgate = _empty_as(gate) if gate is not None else None
         ws = _space(L.fp4_residual_norm_workspace(m, c, w_post is not None), dev, what)
-        st = L.fp4_residual_norm_backward(ctypes.byref(args), stats.data_ptr(), _ptr(dn), 0 if dn is None else _ld(dn),
+        st = L.fp4_residual_norm_backward(args, stats.data_ptr(), _ptr(dn), 0 if dn is None else _ld(dn),
                                           _ptr(dh), 0 if dh is None else _ld(dh), dx.data_ptr(), c, dres.data_ptr(), c,
                                           dw_pre.data_ptr(), _ptr(dw_post), _ptr(dgate), _ptr(ws),
                                           0 if ws is None else ws.numel(), _stream(stream, dev))

@@ -70,8 +70,10 @@ LoraSpace lora_space(int32_t call, int64_t m, int64_t n, int64_t k, int64_t rank
     if (w.down.splits > 1 || call == FP4_LORA_WO_GEMM) w.t = w.take(4 * w.down.splits * m * rank);
     if (back) {
         w.dt = w.take(4 * m * rank);
-        w.at = w.take(2 * adapters * rank * k);
-        w.bt = w.take(2 * adapters * rank * n);
+        if (!lora_across(m)) {
+            w.at = w.take(2 * adapters * rank * k);
+            w.bt = w.take(2 * adapters * rank * n);
+        }
         w.outer_splits = lora_outer_splits(m, n, k, (int)rank, adapters);
         if (w.outer_splits > 1) {
             w.part0 = w.take(4 * w.outer_splits * adapters * rank * k);
@@ -180,18 +182,23 @@ fp4_status fp4_lora_backward(const uint16_t* dy, int64_t ld_dy, const uint16_t* 
     hipStream_t s = (hipStream_t)stream;
     float* const dt = at<float>(workspace, w.dt);
     if (m > 0) {
+        const bool across = lora_across(m);
         uint16_t* const a_t = at<uint16_t>(workspace, w.at);
         uint16_t* const b_t = at<uint16_t>(workspace, w.bt);
-        st = hip_status(launch_lora_transpose(bank->a, a_t, bank->b, b_t, bank->adapters, bank->rank, bank->k, bank->n, s));
-        if (st != FP4_OK) return st;
+        if (!across) {
+            st = hip_status(launch_lora_transpose(bank->a, a_t, bank->b, b_t, bank->adapters, bank->rank, bank->k, bank->n, s));
+            if (st != FP4_OK) return st;
+        }
         // dT = s dy B
         float* const parts = w.down.splits > 1 ? at<float>(workspace, w.t) : dt;
-        st = hip_status(launch_lora_down(down_of(dy, ld_dy, m, bank->n, b_t, bank, slots, bank->scale, parts), w.down, s));
+        LoraDown d = down_of(dy, ld_dy, m, bank->n, across ? bank->b : b_t, bank, slots, bank->scale, parts);
+        d.across = across;
+        st = hip_status(launch_lora_down(d, w.down, s));
         if (st != FP4_OK) return st;
         // dx = base + dT A
         LoraUp u{};
         u.t = parts; u.splits = (int32_t)w.down.splits; u.m = m; u.n = bank->k;
-        u.b = a_t; u.adapters = bank->adapters; u.rank = (int32_t)bank->rank;
+        u.b = across ? bank->a : a_t; u.across = across; u.adapters = bank->adapters; u.rank = (int32_t)bank->rank;
         u.slots = slots;
         u.base = dx_base; u.ldbase = ld_dx_base; u.y = dx; u.ldy = ld_dx;
         u.t_out = w.down.splits > 1 ? dt : nullptr;

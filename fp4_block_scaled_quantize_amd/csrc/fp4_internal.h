@@ -155,6 +155,7 @@ struct LoraDown {
     const float* scale;        // null: 1
     float* t;                  // [splits, m, rank]
     int64_t kstep;
+    int32_t across;            // a is [adapters, k, rank] instead
 };
 // At most 16 rows or tiles of more, K ranges of kstep, z adapters of a tile at once.
 struct LoraDownShape { bool few; int64_t splits, kstep, z; };
@@ -170,8 +171,10 @@ struct LoraUp {
     uint16_t* y; int64_t ldy;
     float* t_out;              // the joined T [m, rank], if not null
     int64_t ncols;             // columns of a workgroup
+    int32_t across;            // b is [adapters, rank, n] instead
 };
 hipError_t launch_lora_up(const LoraUp& p, hipStream_t s);
+bool lora_across(int64_t m);
 
 struct LoraTranspose {
     const uint16_t* src[2]; uint16_t* dst[2];

@@ -50,6 +50,20 @@ __device__ __forceinline__ void bf16_terms(float a, float b, uint32_t (&out)[NT]
     }
 }
 
+// Eight elements `stride` apart as a fragment: an operand whose contraction
+// runs across its rows (TR below).  A backward call of few rows takes B and A
+// that way; for more rows they are transposed once (k_lora_transpose).
+__device__ __forceinline__ v4i gather8(const uint16_t* p, int64_t stride)
+{
+    uint16_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = p[i * stride];
+    v4i v;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = (int)(e[2 * q] | ((uint32_t)e[2 * q + 1] << 16));
+    return v;
+}
+
 // ---------------------------------------------------------------------------
 // T = x A_l^T for at most 16 rows: one workgroup per K range, its eight waves
 // on every eighth batch of 128 elements, joined through LDS in a fixed order.
@@ -62,7 +76,7 @@ __device__ __forceinline__ void bf16_terms(float a, float b, uint32_t (&out)[NT]
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
 
-template <int RT>
+template <int RT, bool TR>
 __global__ __launch_bounds__(64 * kFewWaves) void k_lora_down_few(LoraDown p)
 {
     constexpr int NW = kFewWaves;
@@ -81,10 +95,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_lora_down_few(LoraDown p)
     }
 
     const int64_t kb = (int64_t)blockIdx.y * p.kstep, ke = kb + p.kstep < K ? kb + p.kstep : K;
-    const uint16_t* const xr = p.x + (r16 < M ? r16 : M - 1) * p.ldx + 8 * grp;
+    const uint16_t* const xr = p.x + (r16 < M ? r16 : M - 1) * p.ldx;
     int64_t ar[RT];
 #pragma unroll
-    for (int j = 0; j < RT; ++j) ar[j] = (int64_t)(16 * j + r16 < R ? 16 * j + r16 : R - 1) * K + 8 * grp;
+    for (int j = 0; j < RT; ++j) ar[j] = (int64_t)(16 * j + r16 < R ? 16 * j + r16 : R - 1) * (TR ? 1 : K);
 
     uint64_t todo = __builtin_amdgcn_ballot_w64(slot >= 0);
     for (unsigned nth = 0; todo; ++nth) {
@@ -98,18 +112,26 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_lora_down_few(LoraDown p)
         for (int j = 0; j < RT; ++j) acc[j] = v4f{0.f, 0.f, 0.f, 0.f};
         for (int64_t k = kb + 128 * wave; k < ke; k += 128 * NW) {
             const v4i zero{0, 0, 0, 0};
-            v4i xf[4], af[4][RT];
+            constexpr int U = TR ? (RT > 2 ? 1 : 2) : 4;       // steps whose loads leave together
+#pragma unroll 1
+            for (int u0 = 0; u0 < 4; u0 += U) {
+                v4i xf[U], af[U][RT];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const bool in = k + 32 * u + 8 * grp < ke;     // 8 elements, all in or all out
-                xf[u] = in ? *reinterpret_cast<const v4i*>(xr + k + 32 * u) : zero;
+                for (int u = 0; u < U; ++u) {
+                    const int64_t c = k + 32 * (u0 + u) + 8 * grp;
+                    const bool in = c < ke;                    // 8 elements, all in or all out
+                    xf[u] = in ? *reinterpret_cast<const v4i*>(xr + c) : zero;
 #pragma unroll
-                for (int j = 0; j < RT; ++j) af[u][j] = in ? *reinterpret_cast<const v4i*>(a + ar[j] + k + 32 * u) : zero;
+                    for (int j = 0; j < RT; ++j)
+                        af[u][j] = !in  ? zero
+                                   : TR ? gather8(a + c * R + ar[j], R)
+                                        : *reinterpret_cast<const v4i*>(a + ar[j] + c);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < RT; ++j) acc[j] = mfma16(af[u][j], xf[u], acc[j]);
             }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int j = 0; j < RT; ++j) acc[j] = mfma16(af[u][j], xf[u], acc[j]);
         }
         // acc[j][e] = T[m = r16][r = 16 j + 4 grp + e]
 #pragma unroll
@@ -157,7 +179,7 @@ __device__ __forceinline__ void wait_loads()
     asm volatile("" ::: "memory");
 }
 
-template <int RT>
+template <int RT, bool TR>
 __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraDown p)
 {
     constexpr int NW = kDownWaves, MI = kDownRows / 16, ND = kDownSlot / 1024;
@@ -198,7 +220,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraDown p)
     };
     int64_t ar[RT];
 #pragma unroll
-    for (int j = 0; j < RT; ++j) ar[j] = (int64_t)(16 * j + r16 < R ? 16 * j + r16 : R - 1) * K;
+    for (int j = 0; j < RT; ++j) ar[j] = (int64_t)(16 * j + r16 < R ? 16 * j + r16 : R - 1) * (TR ? 1 : K);
 
     uint64_t todo = __builtin_amdgcn_ballot_w64(slot >= 0);
     for (unsigned nth = 0; todo; ++nth) {
@@ -222,7 +244,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraDown p)
             for (int u = 0; u < 4; ++u) {
                 const int64_t c = k + 32 * u + 8 * grp < ke ? k + 32 * u + 8 * grp : ke - 8;
 #pragma unroll
-                for (int j = 0; j < RT; ++j) af[u][j] = *reinterpret_cast<const v4i*>(a + ar[j] + c);
+                for (int j = 0; j < RT; ++j)
+                    af[u][j] = TR ? gather8(a + c * R + ar[j], R) : *reinterpret_cast<const v4i*>(a + ar[j] + c);
             }
             // Every load is issued unconditionally (the last chunk is brought
             // again instead of one past the end), so that the number in flight
@@ -285,7 +308,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraDown p)
 // one whose B is multiplied drop the result (a select, so that nothing of one
 // adapter reaches another's rows).
 // ---------------------------------------------------------------------------
-template <int WM, int RC>
+template <int WM, int RC, bool TR>
 __global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
 {
     constexpr int WN = 4 / WM;                          // waves side by side along the columns
@@ -356,16 +379,19 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
     // B's fragments: tile (u, h) holds columns n0 + 32 u + 16 h + r16
     v4i bf[2][2][RC];
     auto load_b = [&](int cur, int64_t n0) {
-        const uint16_t* const b = p.b + (int64_t)cur * N * R + 8 * grp;
+        const uint16_t* const b = p.b + (int64_t)cur * N * R;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t n = n0 + 32 * u + 16 * h + r16;
-                const uint16_t* const row = b + (n < N ? n : N - 1) * R;
+                const int64_t at = n0 + 32 * u + 16 * h + r16, n = at < N ? at : N - 1;
 #pragma unroll
-                for (int c = 0; c < RC; ++c)
-                    bf[u][h][c] = 32 * c + 8 * grp < R ? *reinterpret_cast<const v4i*>(row + 32 * c) : v4i{0, 0, 0, 0};
+                for (int c = 0; c < RC; ++c) {
+                    const int r = 32 * c + 8 * grp;
+                    bf[u][h][c] = r >= R ? v4i{0, 0, 0, 0}
+                                  : TR   ? gather8(b + r * N + n, N)
+                                         : *reinterpret_cast<const v4i*>(b + n * R + r);
+                }
             }
     };
     auto multiply = [&](int cur, float s, v4f (&o)[2][2]) {
@@ -717,6 +743,8 @@ LoraDownShape lora_down_shape(int64_t m, int64_t k, int rank, int64_t adapters)
     return s;
 }
 
+constexpr int64_t kAcrossRows = 256;
+
 static int outer_rt(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
 
 // The row ranges of the gradient sums, at least 256 rows each (two chunks a
@@ -734,29 +762,35 @@ int64_t lora_outer_splits(int64_t m, int64_t n, int64_t k, int rank, int64_t ada
     return clamp64(fit, 1, clamp64(m / 256, 1, clamp64((int64_t(256) << 20) / part, 1, 16)));
 }
 
-template <int RT>
+template <int RT, bool TR>
 static hipError_t run_down(const LoraDown& p, const LoraDownShape& sh, hipStream_t s)
 {
     const dim3 grid((unsigned)(sh.few ? 1 : cdiv(p.m, kDownRows)), (unsigned)sh.splits, (unsigned)sh.z);
-    if (sh.few) hipLaunchKernelGGL((k_lora_down_few<RT>), grid, dim3(64 * kFewWaves), 0, s, p);
-    else hipLaunchKernelGGL((k_lora_down<RT>), grid, dim3(64 * kDownWaves), 0, s, p);
+    if (sh.few) hipLaunchKernelGGL((k_lora_down_few<RT, TR>), grid, dim3(64 * kFewWaves), 0, s, p);
+    else hipLaunchKernelGGL((k_lora_down<RT, TR>), grid, dim3(64 * kDownWaves), 0, s, p);
     return hipGetLastError();
+}
+
+template <bool TR>
+static hipError_t down_by_rank(const LoraDown& p, const LoraDownShape& sh, hipStream_t s)
+{
+    if (p.rank <= 16) return run_down<1, TR>(p, sh, s);
+    if (p.rank <= 32) return run_down<2, TR>(p, sh, s);
+    if (p.rank <= 64) return run_down<4, TR>(p, sh, s);
+    return run_down<8, TR>(p, sh, s);
 }
 
 hipError_t launch_lora_down(const LoraDown& in, const LoraDownShape& sh, hipStream_t s)
 {
     LoraDown p = in;
     p.kstep = sh.kstep;
-    if (p.rank <= 16) return run_down<1>(p, sh, s);
-    if (p.rank <= 32) return run_down<2>(p, sh, s);
-    if (p.rank <= 64) return run_down<4>(p, sh, s);
-    return run_down<8>(p, sh, s);
+    return p.across ? down_by_rank<true>(p, sh, s) : down_by_rank<false>(p, sh, s);
 }
 
 // Columns of a workgroup: 512 when the row tiles alone fill the device (the
 // rows' T is then read once for eight steps of a wave), fewer where they do
 // not, but at least four for every element of a row of T.
-template <int WM, int RC>
+template <int WM, int RC, bool TR>
 static hipError_t run_up(const LoraUp& in, hipStream_t s)
 {
     LoraUp p = in;
@@ -776,16 +810,27 @@ static hipError_t run_up(const LoraUp& in, hipStream_t s)
         p.t_out = nullptr;
     }
     const dim3 grid((unsigned)cdiv(p.n, p.ncols), (unsigned)rows);
-    hipLaunchKernelGGL((k_lora_up<WM, RC>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_lora_up<WM, RC, TR>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
+}
+
+template <int WM, bool TR>
+static hipError_t up_by_rank(const LoraUp& p, hipStream_t s)
+{
+    if (p.rank <= 32) return run_up<WM, 1, TR>(p, s);
+    if (p.rank <= 64) return run_up<WM, 2, TR>(p, s);
+    return run_up<WM, 4, TR>(p, s);
 }
 
 hipError_t launch_lora_up(const LoraUp& p, hipStream_t s)
 {
-    const int rc = p.rank <= 32 ? 1 : p.rank <= 64 ? 2 : 4;
-    if (p.m <= 16) return rc == 1 ? run_up<1, 1>(p, s) : rc == 2 ? run_up<1, 2>(p, s) : run_up<1, 4>(p, s);
-    return rc == 1 ? run_up<4, 1>(p, s) : rc == 2 ? run_up<4, 2>(p, s) : run_up<4, 4>(p, s);
+    if (p.m <= 16) return p.across ? up_by_rank<1, true>(p, s) : up_by_rank<1, false>(p, s);
+    return p.across ? up_by_rank<4, true>(p, s) : up_by_rank<4, false>(p, s);
 }
+
+// A backward call of few rows reads B and A across their rows (eight loads for
+// a fragment) instead of transposing them first.
+bool lora_across(int64_t m) { return m <= kAcrossRows; }
 
 hipError_t launch_lora_transpose(const uint16_t* a, uint16_t* at, const uint16_t* b, uint16_t* bt, int64_t adapters,
                                  int64_t rank, int64_t k, int64_t n, hipStream_t s)
