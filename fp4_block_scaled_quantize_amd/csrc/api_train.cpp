@@ -20,6 +20,7 @@ constexpr int64_t kMaxDim = int64_t(1) << 24;         // k and n of a bank
 constexpr int64_t kMaxElems = int64_t(1) << 40;       // elements of one tensor: byte offsets stay far from 63 bits
 constexpr int32_t kMaxRank = 128, kMaxTop = 32;
 constexpr int64_t kMaxNormCols = 32768;
+constexpr int64_t kMaxLineRows = int64_t(1) << 22;    // rows with a workgroup each: below 2^32 threads at 1024
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 int64_t up16(int64_t b) { return (b + 15) / 16 * 16; }
@@ -70,7 +71,7 @@ LoraSpace lora_space(int32_t call, int64_t m, int64_t n, int64_t k, int64_t rank
     if (w.down.splits > 1 || call == FP4_LORA_WO_GEMM) w.t = w.take(4 * w.down.splits * m * rank);
     if (back) {
         w.dt = w.take(4 * m * rank);
-        if (!lora_across(m)) {
+        if (!lora_across(m, rank)) {
             w.at = w.take(2 * adapters * rank * k);
             w.bt = w.take(2 * adapters * rank * n);
         }
@@ -175,6 +176,8 @@ fp4_status fp4_lora_backward(const uint16_t* dy, int64_t ld_dy, const uint16_t* 
     if ((st = check_rows(dx, ld_dx, m, bank->k)) != FP4_OK) return st;
     if (dx_base && (st = check_rows(dx_base, ld_dx_base, m, bank->k)) != FP4_OK) return st;
     if (dx_base && dx_base == dx && ld_dx_base != ld_dx) return FP4_ERR_SHAPE;
+    // the gradient sums read x and dy after dx is written
+    if (m && (dx == x || dx == dy)) return FP4_ERR_INVALID_ARG;
     if ((!t && m) || !da || !db) return FP4_ERR_INVALID_ARG;
     if (!aligned(t, 16) || !aligned(da, 16) || !aligned(db, 16)) return FP4_ERR_ALIGN;
     const LoraSpace w = lora_space(FP4_LORA_BACKWARD, m, bank->n, bank->k, bank->rank, bank->adapters);
@@ -182,7 +185,7 @@ fp4_status fp4_lora_backward(const uint16_t* dy, int64_t ld_dy, const uint16_t* 
     hipStream_t s = (hipStream_t)stream;
     float* const dt = at<float>(workspace, w.dt);
     if (m > 0) {
-        const bool across = lora_across(m);
+        const bool across = lora_across(m, bank->rank);
         uint16_t* const a_t = at<uint16_t>(workspace, w.at);
         uint16_t* const b_t = at<uint16_t>(workspace, w.bt);
         if (!across) {
@@ -243,7 +246,7 @@ static fp4_status check_logits(const void* z, int32_t dtype, int64_t ld, int64_t
     if (!dtype_ok(dtype)) return FP4_ERR_INVALID_ARG;
     if (!(temperature > 0.0f) || !isfinite(temperature) || !isfinite(1.0f / temperature)) return FP4_ERR_INVALID_ARG;
     if (rows < 0 || vocab < 1 || ld < vocab) return FP4_ERR_SHAPE;
-    if (rows >= (int64_t(1) << 31) || vocab >= (int64_t(1) << 27) || ld > kMaxElems / (rows ? rows : 1))
+    if (rows >= kMaxLineRows || vocab >= (int64_t(1) << 27) || ld > kMaxElems / (rows ? rows : 1))
         return FP4_ERR_UNSUPPORTED;
     if (!z && rows) return FP4_ERR_INVALID_ARG;
     if (!aligned(z, (uintptr_t)esize(dtype))) return FP4_ERR_ALIGN;
@@ -253,7 +256,7 @@ static fp4_status check_logits(const void* z, int32_t dtype, int64_t ld, int64_t
 int64_t fp4_token_logprobs_workspace(int64_t rows, int64_t vocab, int32_t top)
 {
     if (rows < 0 || vocab < 1) return FP4_ERR_SHAPE;
-    if (top < 0 || top > kMaxTop) return FP4_ERR_UNSUPPORTED;
+    if (top < 0 || top > kMaxTop || rows >= kMaxLineRows || vocab >= (int64_t(1) << 27)) return FP4_ERR_UNSUPPORTED;
     const int64_t pieces = logprob_pieces(rows, vocab);
     return pieces == 1 ? 0 : rows * pieces * (16 + 8 * (int64_t)top);
 }
@@ -330,7 +333,7 @@ static fp4_status check_norm(const fp4_norm* a, NormLaunch* p, bool* vec)
     if (!dtype_ok(a->x_dtype) || !dtype_ok(a->res_dtype) || !dtype_ok(a->weight_dtype)) return FP4_ERR_INVALID_ARG;
     if (!isfinite(a->alpha) || !isfinite(a->eps) || a->eps < 0.0f) return FP4_ERR_INVALID_ARG;
     if (a->rows < 0 || a->cols < 1) return FP4_ERR_SHAPE;
-    if (a->cols > kMaxNormCols || a->rows >= (int64_t(1) << 31)) return FP4_ERR_UNSUPPORTED;
+    if (a->cols > kMaxNormCols || a->rows >= kMaxLineRows) return FP4_ERR_UNSUPPORTED;
     if (!a->w_pre || (a->rows && (!a->x || !a->res))) return FP4_ERR_INVALID_ARG;
     *vec = a->cols % 8 == 0;
     fp4_status st = check_norm_rows(a->x, a->x_dtype, a->ld_x, a->rows, a->cols, vec);
@@ -371,7 +374,7 @@ fp4_status fp4_residual_norm(const fp4_norm* args, void* h, int64_t ld_h, void* 
 int64_t fp4_residual_norm_workspace(int64_t rows, int64_t cols, int32_t post)
 {
     if (rows < 0 || cols < 1) return FP4_ERR_SHAPE;
-    if (cols > kMaxNormCols || rows >= (int64_t(1) << 31)) return FP4_ERR_UNSUPPORTED;
+    if (cols > kMaxNormCols || rows >= kMaxLineRows) return FP4_ERR_UNSUPPORTED;
     return up16(4 * norm_groups(rows, cols) * (post ? 2 : 1) * cols);
 }
 

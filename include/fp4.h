@@ -440,7 +440,8 @@ FP4_API fp4_status fp4_lora_apply(const uint16_t* x, int64_t ldx, int64_t m, con
  *   da[l] = sum_i dT_i^T x_i,  db[l] = s_l sum_i dy_i^T T_i
  * over the rows i of adapter l (zero for an adapter without rows).  t is
  * fp4_lora_apply's T; dx_base is the gradient that arrives at x through the
- * shared projection (null for zero; it may be dx).  da, db have the bank's
+ * shared projection (null for zero; it may be dx; dx may be neither x nor
+ * dy).  da, db have the bank's
  * shapes in grad_dtype, are written whole and 16-byte aligned.  The sums are
  * taken in a fixed order: the same inputs give the same bits.
  */
@@ -475,7 +476,8 @@ FP4_API fp4_status fp4_wo_gemm_lora(const uint16_t* x, int64_t ldx, int64_t m, c
  * A logit of -inf has probability 0 and adds nothing.  A row of only -inf
  * has no probability: entropy 0, log probabilities -inf.  A NaN or +inf
  * makes its own row's results NaN.  Sums in binary32.
- * workspace: as above, fp4_token_logprobs_workspace bytes.
+ * Fewer than 2^22 rows and 2^27 tokens.  workspace: as above,
+ * fp4_token_logprobs_workspace bytes.
  */
 FP4_API int64_t fp4_token_logprobs_workspace(int64_t rows, int64_t vocab, int32_t top);
 FP4_API fp4_status fp4_token_logprobs(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
@@ -507,7 +509,8 @@ FP4_API fp4_status fp4_token_logprobs_backward(const void* logits, int32_t dtype
  *   h = alpha res + gate u  (gate [rows], binary32; null for 1)
  *   n = RMSNorm(h) w_pre,  RMSNorm(v) = v / sqrt(mean v^2 + eps)
  * x and n in x_dtype, res and h in res_dtype, the weights in weight_dtype
- * (each f32 or bf16); n comes from the unrounded h.  cols at most 32768, any
+ * (each f32 or bf16); n comes from the unrounded h.  Fewer than 2^22 rows;
+ * cols at most 32768, any
  * value and alignment of elements (rows of whole 16-byte vectors, cols % 8
  * == 0, are read as vectors).  stats [rows, 2] = {1 / sqrt(mean x^2 + eps)
  * (1 without w_post), 1 / sqrt(mean h^2 + eps)} for the backward call.  h may

@@ -44,7 +44,7 @@ def test_apply_refuses_no_bank():
     assert fq.lib().fp4_lora_apply(FAKE, 256, 4, None, FAKE, None, 0, FAKE, 64, FAKE, FAKE, ROOM, None) == -1
 
 
-def _backward(m=32, dy=FAKE, ldd=64, x=FAKE, ldx=256, t=FAKE, dxb=None, ldxb=256, dx=FAKE, lddx=256, da=FAKE, db=FAKE,
+def _backward(m=32, dy=FAKE, ldd=64, x=FAKE, ldx=256, t=FAKE, dxb=None, ldxb=256, dx=FAKE + 64, lddx=256, da=FAKE, db=FAKE,
               gd=0, ws=FAKE, room=ROOM, slots=FAKE):
     return fq.lib().fp4_lora_backward(dy, ldd, x, ldx, m, t, ctypes.byref(_bank()), slots, dxb, ldxb, dx, lddx, da, db, gd,
                                       ws, room, None)
@@ -53,7 +53,7 @@ def _backward(m=32, dy=FAKE, ldd=64, x=FAKE, ldx=256, t=FAKE, dxb=None, ldxb=256
 @pytest.mark.parametrize("kw,want", [
     (dict(gd=2), -1), (dict(m=-1), -3), (dict(slots=None), -1), (dict(dy=None), -1), (dict(ldd=56), -3),
     (dict(dy=FAKE + 8), -4), (dict(x=None), -1), (dict(ldx=255), -3), (dict(dx=None), -1), (dict(lddx=260), -4),
-    (dict(dxb=FAKE + 8), -4), (dict(dxb=FAKE, ldxb=264), -3), (dict(t=None), -1), (dict(da=None), -1), (dict(db=None), -1),
+    (dict(dxb=FAKE + 8), -4), (dict(dxb=FAKE + 64, ldxb=264), -3), (dict(dx=FAKE), -1), (dict(dx=FAKE, x=FAKE + 32), -1), (dict(t=None), -1), (dict(da=None), -1), (dict(db=None), -1),
     (dict(da=FAKE + 8), -4), (dict(ws=None), -1), (dict(room=100), -1), (dict(ws=FAKE + 8), -4),
 ])
 def test_backward_rejects_before_launch(kw, want):
@@ -97,7 +97,7 @@ def _lp(z=FAKE, dt=1, ld=1000, n=4, v=1000, tok=FAKE, temp=1.0, top=3, lp=FAKE, 
 @pytest.mark.parametrize("kw,want", [
     (dict(dt=2), -1), (dict(temp=0.0), -1), (dict(temp=-1.0), -1), (dict(temp=float("nan")), -1),
     (dict(temp=float("inf")), -1), (dict(temp=1e-45), -1), (dict(n=-1), -3), (dict(v=0), -3), (dict(ld=999), -3),
-    (dict(v=1 << 27, ld=1 << 27), -2), (dict(z=None), -1), (dict(z=FAKE + 1), -4), (dict(dt=0, z=FAKE + 2), -4),
+    (dict(v=1 << 27, ld=1 << 27), -2), (dict(n=1 << 22), -2), (dict(z=None), -1), (dict(z=FAKE + 1), -4), (dict(dt=0, z=FAKE + 2), -4),
     (dict(top=-1), -2), (dict(top=33), -2), (dict(v=2, ld=2), -3), (dict(ent=None), -1), (dict(st=None), -1),
     (dict(lp=None), -1), (dict(ids=None), -1), (dict(best=None), -1), (dict(tok=FAKE + 4), -4), (dict(ent=FAKE + 2), -4),
     (dict(v=20000, ld=20000, ws=None), -1), (dict(v=20000, ld=20000, room=8), -1),
@@ -129,7 +129,7 @@ def _norm(x=FAKE, ldx=64, r=FAKE, ldr=64, rows=4, cols=64, w2=FAKE, w1=None, gat
 
 @pytest.mark.parametrize("kw,want", [
     (dict(xd=3), -1), (dict(rd=-1), -1), (dict(wd=2), -1), (dict(alpha=float("nan")), -1), (dict(eps=-1.0), -1),
-    (dict(eps=float("inf")), -1), (dict(rows=-1), -3), (dict(cols=0), -3), (dict(cols=32769, ldx=40000, ldr=40000), -2),
+    (dict(eps=float("inf")), -1), (dict(rows=-1), -3), (dict(cols=0), -3), (dict(cols=32769, ldx=40000, ldr=40000), -2), (dict(rows=1 << 22), -2),
     (dict(w2=None), -1), (dict(x=None), -1), (dict(r=None), -1), (dict(ldx=63), -3), (dict(ldr=63), -3),
     (dict(x=FAKE + 1), -4), (dict(r=FAKE + 2), -4), (dict(w1=FAKE + 1), -4), (dict(gate=FAKE + 2), -4),
 ])
