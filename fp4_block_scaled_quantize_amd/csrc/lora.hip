@@ -303,23 +303,40 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraDown p)
 // lane, pass through the wave's own 4 KB of LDS and come back as 8 columns a
 // lane, 8 lanes a row.  8192 x 4096, rank 16, 134 MB: 29 us, 4.6 TB/s; the same
 // loads and stores without the products take 28.8.
-// The WM waves of a workgroup on neighbouring rows read the same part of B,
-// which the first brings into the cache.  Rows of another adapter than the
+// The WM waves of a workgroup on neighbouring rows read the same part of B:
+// from the cache up to rank 32; above, a step's columns of B outweigh those of
+// y and come through LDS once for all four (SH; 1111 rows of nine requests,
+// rank 64, 11008 columns: 21 us against 25).  Rows of another adapter than the
 // one whose B is multiplied drop the result (a select, so that nothing of one
 // adapter reaches another's rows).
 // ---------------------------------------------------------------------------
-template <int WM, int RC, bool TR>
+template <int WM, int RC, bool TR, bool SH>
 __global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
 {
     constexpr int WN = 4 / WM;                          // waves side by side along the columns
     constexpr int Pitch = 68;                           // floats: 17 times 16 bytes
     __shared__ __align__(16) float tile[4][16 * Pitch];
+    static_assert(!SH || (WM == 4 && !TR && RC > 1), "neighbouring rows share B's fragments");
+    __shared__ __align__(16) uint8_t bsh[SH ? 2 * 64 * 64 * RC : 16];
     const int lane = threadIdx.x & 63, r16 = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t M = p.m, N = p.n;
     const int R = p.rank;
     const int64_t m0 = ((int64_t)blockIdx.y * WM + wave % WM) * 16, m = m0 + r16;
-    if (m0 >= M) return;                                // no barrier below: waves are on their own
+    // SH: the adapters of the workgroup's 64 rows, the j-th in lane j, if they
+    // are at most four (0 in `kinds`: more, or none)
+    int kinds = 0, kind = -1;
+    if constexpr (SH) {
+        const int ws = row_slot(p.slots, (int64_t)blockIdx.y * 64 + lane, M, p.adapters);
+        uint64_t todo = __builtin_amdgcn_ballot_w64(ws >= 0);
+        for (; todo && kinds < 4; ++kinds) {
+            const int cur = __builtin_amdgcn_readlane(ws, __builtin_ctzll(todo));
+            kind = lane == kinds ? cur : kind;
+            todo &= ~__builtin_amdgcn_ballot_w64(ws == cur);
+        }
+        if (todo) kinds = 0;
+    }
+    if (m0 >= M && kinds == 0) return;                  // no barrier below: waves are on their own
     const int64_t nb = (int64_t)blockIdx.x * p.ncols, ne = nb + p.ncols < N ? nb + p.ncols : N;
     const int slot = row_slot(p.slots, m, M, p.adapters);   // the same in the four lanes of a row
     float* const out = tile[wave];
@@ -409,31 +426,7 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
                 for (int e = 0; e < 4; ++e) o[u][h][e] = slot == cur ? acc[e] * s : o[u][h][e];
             }
     };
-    // the tile's only adapter (-1: several, or none): its next columns of B
-    // are loaded while these are written (larger ranks' fragments would cost
-    // a wave of the SIMD's four: rank 64, 1111 rows, 32 us against 26)
-    int one = used ? __builtin_amdgcn_readlane(slot, __builtin_ctzll(used)) : -1;
-    if (RC > 1 || (used & ~__builtin_amdgcn_ballot_w64(slot == one))) one = -1;
-    const float scale1 = one >= 0 && p.scale ? p.scale[one] : 1.0f;
-    if (one >= 0) load_b(one, nb + 64 * (wave / WM));
-    fetch(nb + 64 * (wave / WM));
-    for (int64_t n0 = nb + 64 * (wave / WM); n0 < ne; n0 += 64 * WN) {
-        v4i old[2]{next[0], next[1]};
-        v4f o[2][2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) o[u][0] = o[u][1] = v4f{0.f, 0.f, 0.f, 0.f};
-        if (one >= 0) {
-            multiply(one, scale1, o);
-            load_b(one, n0 + 64 * WN);
-        } else {
-            for (uint64_t todo = used; todo;) {
-                const int cur = __builtin_amdgcn_readlane(slot, __builtin_ctzll(todo));
-                todo &= ~__builtin_amdgcn_ballot_w64(slot == cur);
-                load_b(cur, n0);
-                multiply(cur, p.scale ? p.scale[cur] : 1.0f, o);
-            }
-        }
-        fetch(n0 + 64 * WN);
+    auto finish = [&](int64_t n0, const v4i (&old)[2], const v4f (&o)[2][2]) {
         // o[u][h][e]: row r16, column 32 u + 16 h + 4 grp + e
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -459,6 +452,91 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
+    };
+    if constexpr (SH) {
+        // An adapter's 64 columns of B lie in LDS once for the four waves,
+        // brought ahead by direct loads (16-byte piece c of column n at c ^ (n
+        // % pieces), the fragment reads' banks apart); two barriers each.
+        if (kinds) {
+            constexpr int P = 4 * RC, Buf = 64 * 64 * RC;
+            auto bring = [&](int cur, int64_t n0, int k) {
+                const uint16_t* const b = p.b + (int64_t)cur * N * R;
+#pragma unroll
+                for (int q = 0; q < RC; ++q) {
+                    const int at = 64 * (wave * RC + q) + lane, row = at / P, piece = (at & (P - 1)) ^ (row & (P - 1));
+                    const int64_t n = n0 + row < N ? n0 + row : N - 1;
+                    __builtin_amdgcn_global_load_lds(b + n * R + (8 * piece < R ? 8 * piece : 0),
+                                                     (lds_ptr_t)(bsh + k * Buf + 1024 * (wave * RC + q)), 16, 0, 0);
+                }
+            };
+            auto meet = [] {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+            };
+            bring(__builtin_amdgcn_readlane(kind, 0), nb, 0);
+            fetch(nb);
+            int k = 0;
+            for (int64_t n0 = nb; n0 < ne; n0 += 64) {
+                const v4i old[2]{next[0], next[1]};
+                v4f o[2][2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) o[u][0] = o[u][1] = v4f{0.f, 0.f, 0.f, 0.f};
+                for (int j = 0; j < kinds; ++j, k ^= 1) {
+                    const int cur = __builtin_amdgcn_readlane(kind, j);
+                    meet();                             // the other buffer has been read
+                    if (j + 1 < kinds) bring(__builtin_amdgcn_readlane(kind, j + 1), n0, k ^ 1);
+                    else bring(__builtin_amdgcn_readlane(kind, 0), n0 + 64 < ne ? n0 + 64 : n0, k ^ 1);
+                    wait_loads<RC>();                   // this wave's part of B
+                    meet();
+                    if (!__builtin_amdgcn_ballot_w64(slot == cur)) continue;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int row = 32 * u + 16 * h + r16;
+#pragma unroll
+                            for (int c = 0; c < RC; ++c) {
+                                bf[u][h][c] = *reinterpret_cast<const v4i*>(bsh + k * Buf + 64 * RC * row +
+                                                                            16 * ((4 * c + grp) ^ (row & (P - 1))));
+                                if (32 * c + 8 * grp >= R) bf[u][h][c] = v4i{0, 0, 0, 0};
+                            }
+                        }
+                    multiply(cur, p.scale ? p.scale[cur] : 1.0f, o);
+                }
+                fetch(n0 + 64);
+                finish(n0, old, o);
+            }
+            wait_loads<0>();                            // the last bring, before the LDS is given up
+            return;
+        }
+    }
+    // the tile's only adapter (-1: several, or none): its next columns of B
+    // are loaded while these are written (larger ranks' fragments would cost
+    // a wave of the SIMD's four: rank 64, 1111 rows, 32 us against 26)
+    int one = used ? __builtin_amdgcn_readlane(slot, __builtin_ctzll(used)) : -1;
+    if (RC > 1 || (used & ~__builtin_amdgcn_ballot_w64(slot == one))) one = -1;
+    const float scale1 = one >= 0 && p.scale ? p.scale[one] : 1.0f;
+    if (one >= 0) load_b(one, nb + 64 * (wave / WM));
+    fetch(nb + 64 * (wave / WM));
+    for (int64_t n0 = nb + 64 * (wave / WM); n0 < ne; n0 += 64 * WN) {
+        v4i old[2]{next[0], next[1]};
+        v4f o[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) o[u][0] = o[u][1] = v4f{0.f, 0.f, 0.f, 0.f};
+        if (one >= 0) {
+            multiply(one, scale1, o);
+            load_b(one, n0 + 64 * WN);
+        } else {
+            for (uint64_t todo = used; todo;) {
+                const int cur = __builtin_amdgcn_readlane(slot, __builtin_ctzll(todo));
+                todo &= ~__builtin_amdgcn_ballot_w64(slot == cur);
+                load_b(cur, n0);
+                multiply(cur, p.scale ? p.scale[cur] : 1.0f, o);
+            }
+        }
+        fetch(n0 + 64 * WN);
+        finish(n0, old, o);
     }
 }
 
@@ -790,7 +868,7 @@ hipError_t launch_lora_down(const LoraDown& in, const LoraDownShape& sh, hipStre
 // Columns of a workgroup: 512 when the row tiles alone fill the device (the
 // rows' T is then read once for eight steps of a wave), fewer where they do
 // not, but at least four for every element of a row of T.
-template <int WM, int RC, bool TR>
+template <int WM, int RC, bool TR, bool SH = false>
 static hipError_t run_up(const LoraUp& in, hipStream_t s)
 {
     LoraUp p = in;
@@ -810,16 +888,17 @@ static hipError_t run_up(const LoraUp& in, hipStream_t s)
         p.t_out = nullptr;
     }
     const dim3 grid((unsigned)cdiv(p.n, p.ncols), (unsigned)rows);
-    hipLaunchKernelGGL((k_lora_up<WM, RC, TR>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_lora_up<WM, RC, TR, SH>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
 template <int WM, bool TR>
 static hipError_t up_by_rank(const LoraUp& p, hipStream_t s)
 {
+    constexpr bool SH = WM == 4 && !TR;
     if (p.rank <= 32) return run_up<WM, 1, TR>(p, s);
-    if (p.rank <= 64) return run_up<WM, 2, TR>(p, s);
-    return run_up<WM, 4, TR>(p, s);
+    if (p.rank <= 64) return run_up<WM, 2, TR, SH>(p, s);
+    return run_up<WM, 4, TR, SH>(p, s);
 }
 
 hipError_t launch_lora_up(const LoraUp& p, hipStream_t s)
