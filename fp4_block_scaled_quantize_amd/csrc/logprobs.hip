@@ -187,21 +187,37 @@ struct TopList {
         if (cnt > top) cnt = top;
         if (cnt == top) raise(buf[top - 1]);
     }
-    // every lane offers one element (`in`: it has one)
-    __device__ __forceinline__ void offer(bool in, float z, uint32_t idx, int lane)
+    // Every lane offers those of its N elements that may be above the
+    // threshold (a NaN passes), one a turn: few lanes have more than a couple,
+    // where visiting the N places for the wave would find one in nearly each.
+    // index(e): the place of element e; have: bit e set where there is one.
+    // A list well past its length is cut at the end: the sooner the threshold
+    // rises, the fewer elements reach the buffer.
+    template <int N, typename F>
+    __device__ __forceinline__ void offer(const float (&f)[N], uint32_t have, int lane, F index)
     {
-        in = in && !(z < value);                       // NaN passes
-        if (!__builtin_amdgcn_ballot_w64(in)) return;
-        const uint64_t key = in ? sort_key(z, idx) : 0;
-        uint64_t want = __builtin_amdgcn_ballot_w64(key > thr);
-        if (!want) return;
-        if (cnt + __builtin_popcountll(want) > kLpBuf) {
-            reduce(lane);
-            want = __builtin_amdgcn_ballot_w64(key > thr);
-            if (!want) return;
+        static_assert(N <= 32, "a bit for each element");
+        uint32_t mine = 0;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const uint32_t up = !(f[e] < value);
+            mine |= up << e;
         }
-        if (key > thr) buf[cnt + __builtin_popcountll(want & ((1ull << lane) - 1))] = key;
-        cnt += __builtin_popcountll(want);
+        mine &= have;
+        for (;;) {
+            const bool more = __builtin_amdgcn_ballot_w64(mine != 0) != 0;
+            if (cnt > (more ? kLpBuf - 64 : top + 32)) reduce(lane);
+            if (!more) break;
+            const int e = mine ? __builtin_ctz(mine) : 0;
+            float v = f[0];
+#pragma unroll
+            for (int i = 1; i < N; ++i) v = e == i ? f[i] : v;
+            const uint64_t key = mine ? sort_key(v, index(e)) : 0;
+            const uint64_t want = __builtin_amdgcn_ballot_w64(key > thr);
+            if (key > thr) buf[cnt + __builtin_popcountll(want & ((1ull << lane) - 1))] = key;
+            cnt += __builtin_popcountll(want);
+            mine &= mine - 1;
+        }
     }
     // a first threshold from the lanes' largest logits: below the smallest of
     // those that fewer than `top` lanes exceed
@@ -360,47 +376,39 @@ __global__ __launch_bounds__(THREADS) void k_lp_rows(LogprobLaunch p)
     bool first = true;
     auto round = [&](int64_t r0, auto whole) {             // whole: every thread has all of its vectors
         bool in[kLpVec];
-        float f[kLpVec][VN], best = -INFINITY;
+        float f[kLpVec * VN], best = -INFINITY;
+        uint32_t have = 0;
 #pragma unroll
         for (int u = 0; u < kLpVec; ++u) {
             in[u] = whole || r0 + (int64_t)u * THREADS + tid < nvec;
-            L::unpack(next[u], f[u]);
-            if (!in[u]) {
+            float v[VN];
+            L::unpack(next[u], v);
 #pragma unroll
-                for (int j = 0; j < VN; ++j) f[u][j] = -INFINITY;
-            }
+            for (int j = 0; j < VN; ++j) f[u * VN + j] = in[u] ? v[j] : -INFINITY;
+            have |= in[u] ? ((1u << VN) - 1) << (u * VN) : 0u;
         }
         fetch(r0 + kRound);
 #pragma unroll
-        for (int u = 0; u < kLpVec; ++u)
-#pragma unroll
-            for (int j = 0; j < VN; ++j) best = fmaxf(best, f[u][j]);
+        for (int j = 0; j < kLpVec * VN; ++j) best = fmaxf(best, f[j]);
         a.raise(best, k);
         if (__builtin_amdgcn_ballot_w64(a.far())) {
 #pragma unroll
-            for (int u = 0; u < kLpVec; ++u)
-#pragma unroll
-                for (int j = 0; j < VN; ++j) {
-                    if (a.far()) a.template add<true>(f[u][j], k);
-                    else a.template add<false>(f[u][j], k);
-                }
+            for (int j = 0; j < kLpVec * VN; ++j) {
+                if (a.far()) a.template add<true>(f[j], k);
+                else a.template add<false>(f[j], k);
+            }
         } else {
 #pragma unroll
-            for (int u = 0; u < kLpVec; ++u)
-#pragma unroll
-                for (int j = 0; j < VN; ++j) a.template add<false>(f[u][j], k);
+            for (int j = 0; j < kLpVec * VN; ++j) a.template add<false>(f[j], k);
         }
         if (TOP) {
             if (first) list.start(in[0], best);
             first = false;
             // a NaN is above everything and `best` drops it: look at the sum
-            if (__builtin_amdgcn_ballot_w64(!(best < list.value) || a.s != a.s)) {
-#pragma unroll
-                for (int u = 0; u < kLpVec; ++u)
-#pragma unroll
-                    for (int j = 0; j < VN; ++j)
-                        list.offer(in[u], f[u][j], (uint32_t)(vb + (r0 + (int64_t)u * THREADS + tid) * VN + j), lane);
-            }
+            if (__builtin_amdgcn_ballot_w64(!(best < list.value) || a.s != a.s))
+                list.offer(f, have, lane, [&](int j) {
+                    return (uint32_t)(vb + (r0 + (int64_t)(j / VN) * THREADS + tid) * VN + j % VN);
+                });
         }
     };
     int64_t r0 = 0;
@@ -415,7 +423,10 @@ __global__ __launch_bounds__(THREADS) void k_lp_rows(LogprobLaunch p)
         a.raise(v, k);
         if (a.far()) a.template add<true>(v, k);
         else a.template add<false>(v, k);
-        if (TOP) list.offer(in, v, (uint32_t)i, lane);
+        if (TOP) {
+            const float one[1]{v};
+            list.offer(one, in, lane, [&](int) { return (uint32_t)i; });
+        }
     }
     // threads of the wave, then the waves
     Sums r = a.about_max(k);
@@ -435,7 +446,9 @@ __global__ __launch_bounds__(THREADS) void k_lp_rows(LogprobLaunch p)
     for (int w = 0; w < NW; ++w) sums_merge(r, sm[w][0], sm[w][1], sm[w][2], k);
     if (gridDim.y == 1) {
         if (tid == 0) finish_row(p, row, r, given);
-        if (TOP)
+        if (TOP && NW == 1) {                              // the wave's list is the row's
+            if (lane < p.top) put_top(p, row, r, lane, lists[lane]);
+        } else if (TOP)
             best_of_lists(lists, NW, p.top, cand, &count, tid, THREADS,
                           [&](int rank, uint64_t key) { put_top(p, row, r, rank, key); });
         return;
@@ -568,10 +581,11 @@ __global__ __launch_bounds__(256) void k_lp_backward(LogprobGradLaunch p)
 // ---------------------------------------------------------------------------
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+constexpr int64_t kLpWaveVocab = 2048;
+
 // A row stays whole when the rows alone fill the device; else it is cut so
 // that about 512 workgroups run, none with less than 4096 elements (two bf16
-// vectors a thread: a wave offers its elements to its top list one after the
-// other, which is what a lone row waits for).
+// vectors a thread).
 int64_t logprob_pieces(int64_t rows, int64_t vocab)
 {
     if (rows < 1 || rows >= 512) return 1;
@@ -587,7 +601,10 @@ static hipError_t run_logprobs(LogprobLaunch p, int64_t pieces, hipStream_t s)
     p.piece = cdiv(cdiv(p.vocab, pieces), 64) * 64;
     pieces = cdiv(p.vocab, p.piece);
     const dim3 grid((unsigned)p.rows, (unsigned)pieces);
-    hipLaunchKernelGGL((k_lp_rows<BF16, TOP, 256>), grid, dim3(256), 0, s, p);
+    // a short row of many is one wave's: nothing to join (4235 rows of 142: 14
+    // us against 53 with four waves a row)
+    if (pieces == 1 && p.vocab <= kLpWaveVocab) hipLaunchKernelGGL((k_lp_rows<BF16, TOP, 64>), grid, dim3(64), 0, s, p);
+    else hipLaunchKernelGGL((k_lp_rows<BF16, TOP, 256>), grid, dim3(256), 0, s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || pieces == 1) return e;
     hipLaunchKernelGGL((k_lp_join<BF16, TOP>), dim3((unsigned)p.rows), dim3(TOP ? kLpJoin : 64), 0, s, p, (int)pieces);

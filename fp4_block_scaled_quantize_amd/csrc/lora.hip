@@ -718,52 +718,52 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : RT == 2 ? 2 : 1) void k_lora_out
         if (blockIdx.x == 0 && rg == 0 && tid == 0) p.flags[(int64_t)blockIdx.z * p.adapters + l] = (uint32_t)any;
         if (!any) return;
     }
-    // waves 1, 2, 3 onto wave 0, in that order
-    for (int w = 1; w < 4; ++w) {
+    // Each wave joins a quarter of the tiles (the 2 RT from 2 RT wave on, by t
+    // first): in three turns every wave passes the quarter of the wave s
+    // places on, and the sums are its own + 1, 2, 3 places before, in order.
+    constexpr int Q = 2 * RT;
+    v4f sum[Q];
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
         if (wave == w) {
 #pragma unroll
-            for (int ci = 0; ci < 8; ++ci)
-#pragma unroll
-                for (int t = 0; t < RT; ++t) red[(ci * RT + t) * 64 + lane] = acc[ci][t];
+            for (int i = 0; i < Q; ++i) sum[i] = acc[(Q * w + i) % 8][(Q * w + i) / 8];
         }
+#pragma unroll
+    for (int s = 1; s < 4; ++s) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            if (wave == w) {
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    const int at = Q * ((w + s) & 3) + i;
+                    red[(Q * w + i) * 64 + lane] = acc[at % 8][at / 8];
+                }
+            }
         __syncthreads();
-        if (wave == 0) {
 #pragma unroll
-            for (int ci = 0; ci < 8; ++ci)
-#pragma unroll
-                for (int t = 0; t < RT; ++t) acc[ci][t] += red[(ci * RT + t) * 64 + lane];
-        }
+        for (int i = 0; i < Q; ++i) sum[i] += red[(Q * ((wave - s) & 3) + i) * 64 + lane];
         __syncthreads();
     }
-    if (wave) return;
-    // acc[ci][t][e] = G[c = c0 + 32 grp + 8 e + ci][r = 16 (rg RT + t) + r16]
+    // tile at = 8 t + ci: sum[at][e] = G[c = c0 + 32 grp + 8 e + ci][r = 16 (rg RT + t) + r16]
     const float s = job.scale ? job.scale[l] : 1.0f;
     float* const part = gridDim.z > 1 ? job.part + (int64_t)blockIdx.z * p.adapters * R * C : nullptr;
+    const int t0 = Q * wave / 8, ci0 = Q * wave % 8;       // a quarter is Q consecutive columns of one t (all 8 from rank 64 on)
+    const int r = 16 * (rg * RT + t0) + r16;
+    if (r >= R) return;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-        const int r = 16 * (rg * RT + t) + r16;
-        if (r >= R) continue;
+    for (int e = 0; e < 4; ++e) {
+        const int64_t c = c0 + 32 * grp + 8 * e + ci0;
+        if (c >= C) continue;
+        // dA [R, C]: consecutive elements; dB [C, R]: one of each row, 16 lanes side by side
+        const int64_t at = (int64_t)l * R * C + (job.by_col ? c * R + r : (int64_t)r * C + c);
+        const int64_t step = job.by_col ? R : 1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t c = c0 + 32 * grp + 8 * e;
-            if (c >= C) continue;
-            float v[8];
-#pragma unroll
-            for (int ci = 0; ci < 8; ++ci) v[ci] = acc[ci][t][e] * s;
-            // dA [R, C]: 8 consecutive elements; dB [C, R]: one element each of 8 rows, 16 lanes side by side
-            const int64_t at = (int64_t)l * R * C + (job.by_col ? c * R + r : (int64_t)r * C + c);
-            const int64_t step = job.by_col ? R : 1;
-            if (part) {
-#pragma unroll
-                for (int ci = 0; ci < 8; ++ci) part[at + ci * step] = v[ci];
-            } else if (p.out_bf16) {
-#pragma unroll
-                for (int ci = 0; ci < 8; ++ci)
-                    reinterpret_cast<uint16_t*>(job.out)[at + ci * step] = (uint16_t)f32_to_bf16_rne(v[ci]);
-            } else {
-#pragma unroll
-                for (int ci = 0; ci < 8; ++ci) reinterpret_cast<float*>(job.out)[at + ci * step] = v[ci];
-            }
+        for (int i = 0; i < Q; ++i) {
+            const float v = sum[i][e] * s;
+            if (part) part[at + i * step] = v;
+            else if (p.out_bf16) reinterpret_cast<uint16_t*>(job.out)[at + i * step] = (uint16_t)f32_to_bf16_rne(v);
+            else reinterpret_cast<float*>(job.out)[at + i * step] = v;
         }
     }
 }
@@ -874,7 +874,9 @@ static hipError_t run_up(const LoraUp& in, hipStream_t s)
     LoraUp p = in;
     const int64_t step = 64 * (4 / WM), rows = cdiv(p.m, 16 * WM);
     const int64_t least = step > 4 * p.rank ? step : 4 * p.rank;
-    const int64_t blocks = clamp64(1024 / rows, cdiv(p.n, 512), cdiv(p.n, least));
+    int64_t blocks = clamp64(1024 / rows, cdiv(p.n, 512), cdiv(p.n, least));
+    // two workgroups a CU come before that
+    if (blocks * rows < 512) blocks = clamp64(cdiv(512, rows), blocks, cdiv(p.n, step));
     p.ncols = cdiv(cdiv(p.n, blocks), step) * step;
     // every column block reads its rows' T: past 16 MB of partial sums (from
     // the caches) a launch that joins them once costs less than the difference
