@@ -82,6 +82,8 @@ SHAPES = [  # m, n, k, rank, adapters, slots
     (16, 1000, 520, 32, 16, "mixed"), (17, 256, 256, 8, 2, "runs"), (33, 40, 2056, 72, 5, "mixed"),
     (63, 248, 136, 40, 2, "none"), (64, 264, 384, 64, 1, "one"), (65, 512, 200, 16, 3, "runs"),
     (130, 264, 520, 8, 3, "runs"), (200, 1032, 4096, 32, 2, "mixed"), (300, 776, 776, 128, 3, "runs"),
+    (2100, 1032, 136, 16, 3, "runs"), (2050, 520, 264, 24, 2, "mixed"), (3000, 776, 136, 32, 40, "mixed"),
+    (2048, 512, 40, 8, 1, "none"), (2500, 600, 72, 16, 1, "one"),
     (513, 136, 264, 56, 40, "mixed"), (1100, 264, 392, 16, 4, "runs"), (2050, 264, 136, 48, 2, "mixed"),
 ]
 
