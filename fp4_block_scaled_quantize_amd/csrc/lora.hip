@@ -71,7 +71,7 @@ __device__ __forceinline__ v4i gather8(const uint16_t* p, int64_t stride)
 // fragment as they come from memory; nothing is staged, and a batch's loads
 // leave together: latency is what such a call waits for.  Rows of several
 // adapters run the K range once for each (gridDim.z of them side by side) and
-// keep each row's own.  With gridDim.y > 1 the K ranges' partial sums are left
+// keep each row's own.  With gridDim.x > 1 the K ranges' partial sums are left
 // for the reader of T to join.
 // ---------------------------------------------------------------------------
 constexpr int kFewWaves = 8;
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_lora_down_few(LoraDown p)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t M = p.m, K = p.k;
     const int R = p.rank;
-    float* const t = p.t + (int64_t)blockIdx.y * M * R;
+    float* const t = p.t + (int64_t)blockIdx.x * M * R;
     const int slot = lane < 16 ? row_slot(p.slots, lane, M, p.adapters) : -1;
 
     if (blockIdx.z == 0) {                    // rows without an adapter
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_lora_down_few(LoraDown p)
                 for (int r = lane; r < R; r += 64) t[i * R + r] = 0.0f;
     }
 
-    const int64_t kb = (int64_t)blockIdx.y * p.kstep, ke = kb + p.kstep < K ? kb + p.kstep : K;
+    const int64_t kb = (int64_t)blockIdx.x * p.kstep, ke = kb + p.kstep < K ? kb + p.kstep : K;
     const uint16_t* const xr = p.x + (r16 < M ? r16 : M - 1) * p.ldx;
     int64_t ar[RT];
 #pragma unroll
@@ -156,12 +156,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_lora_down_few(LoraDown p)
 // waves on every fourth chunk of 128 elements.  Bound by reading x, which
 // wants whole lines: fragments taken straight from memory touch 64 bytes of
 // 16 rows at a time (8192 rows of 11008, rank 16: 71 us that way, 42 so, 4.3
-// TB/s).  So a wave brings
-// its next chunk (32 rows x 256 bytes) into LDS with direct loads of four rows
+// TB/s).  So a wave brings its next chunk (32 rows x 256 bytes) into LDS with direct loads of four rows
 // each while it multiplies the one before; A's fragments, shared by all row
 // tiles, come from the cache.  A 16-byte piece c of row r lies at c ^ (r % 16),
 // so that the 16 rows of a fragment read fall on distinct banks (the lanes
-// pick their global pieces accordingly).  Adapters and K ranges as above.
+// pick their global pieces accordingly).  Adapters and K ranges as above; a
+// tile's K ranges are neighbours in the grid, so that what is read at one time
+// are longer pieces of fewer rows (47 us with the tiles first).
 // ---------------------------------------------------------------------------
 constexpr int kDownWaves = 4, kDownRows = 32;
 constexpr int kDownSlot = kDownRows * 256;              // bytes of a chunk
@@ -188,10 +189,10 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraDown p)
     static_assert(NW * MI * RT * 1024 <= NW * 2 * kDownSlot, "partial tiles fit");
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, grp = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t m0 = (int64_t)blockIdx.x * kDownRows;
+    const int64_t m0 = (int64_t)blockIdx.y * kDownRows;
     const int64_t M = p.m, K = p.k;
     const int R = p.rank;
-    float* const t = p.t + (int64_t)blockIdx.y * M * R;
+    float* const t = p.t + (int64_t)blockIdx.x * M * R;
     const int slot = lane < kDownRows ? row_slot(p.slots, m0 + lane, M, p.adapters) : -1;
 
     if (blockIdx.z == 0) {                    // rows without an adapter
@@ -200,7 +201,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraDown p)
                 for (int r = lane; r < R; r += 64) t[(m0 + i) * R + r] = 0.0f;
     }
 
-    const int64_t kb = (int64_t)blockIdx.y * p.kstep, ke = kb + p.kstep < K ? kb + p.kstep : K;
+    const int64_t kb = (int64_t)blockIdx.x * p.kstep, ke = kb + p.kstep < K ? kb + p.kstep : K;
     uint8_t* const ring = lds + wave * 2 * kDownSlot;
     // direct load q of a chunk: lane l brings piece (l % 16) ^ (row % 16) of row 4 q + l / 16
     const uint16_t* xr[ND];
@@ -843,7 +844,7 @@ int64_t lora_outer_splits(int64_t m, int64_t n, int64_t k, int rank, int64_t ada
 template <int RT, bool TR>
 static hipError_t run_down(const LoraDown& p, const LoraDownShape& sh, hipStream_t s)
 {
-    const dim3 grid((unsigned)(sh.few ? 1 : cdiv(p.m, kDownRows)), (unsigned)sh.splits, (unsigned)sh.z);
+    const dim3 grid((unsigned)sh.splits, (unsigned)(sh.few ? 1 : cdiv(p.m, kDownRows)), (unsigned)sh.z);
     if (sh.few) hipLaunchKernelGGL((k_lora_down_few<RT, TR>), grid, dim3(64 * kFewWaves), 0, s, p);
     else hipLaunchKernelGGL((k_lora_down<RT, TR>), grid, dim3(64 * kDownWaves), 0, s, p);
     return hipGetLastError();
