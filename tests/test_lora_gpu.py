@@ -296,3 +296,54 @@ def test_side_stream_and_graph_replay():
         for u, v in zip(step(), want):
             assert torch.equal(u, v)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("m", [4, 20])
+def test_offsets_past_32_bits(m):
+    """Rows far apart in one large allocation, and a bank of more than 2^31
+    elements: the last rows and the last adapters are the ones in use."""
+    g = torch.Generator().manual_seed(m)
+    la, n, k, r = 16384, 1032, 256, 128
+    assert la * n * r > 2 ** 31
+    x, dy = _randn(g, m, k), _randn(g, m, n)
+    some = {la - 1: 0, 3: 1, la - 9: 2}
+    a, b, sc = _bank(g, 3, n, k, r)
+    ad = torch.zeros(la, r, k, dtype=torch.bfloat16, device="cuda")
+    bd = torch.zeros(la, n, r, dtype=torch.bfloat16, device="cuda")
+    sd = torch.ones(la, device="cuda")
+    for at, i in some.items():
+        ad[at], bd[at], sd[at] = a[i].cuda(), b[i].cuda(), sc[i].cuda()
+    few = torch.randint(-1, 3, (m,), generator=g).to(torch.int32)
+    few[:4] = torch.tensor([0, 1, 2, -1])
+    slots = torch.full((m,), -1, dtype=torch.int32)
+    for at, i in some.items():
+        slots[few == i] = at
+    far = (2 ** 31 + 2 ** 26) // (m - 1) // 8 * 8
+    assert far * (m - 1) > 2 ** 31
+
+    def spread(v):
+        w = torch.empty(far * (m - 1) + v.shape[1], dtype=torch.bfloat16, device="cuda").as_strided((m, v.shape[1]), (far, 1))
+        w.copy_(v)
+        return w
+
+    bank, sl = fq.LoraBank(ad, bd, sd), slots.cuda()
+    xd, dyd = spread(x), spread(dy)
+    y, t = fq.fp4_lora_apply(xd, bank, sl, base=dyd, out=spread(torch.zeros_like(dy)))
+    y64, t64, my, mt = _forward64(x, a, b, sc, few, dy)
+    _close(t, t64, mt, 1e-5, torch.float32, "t")
+    _close(y, y64, my + dy.to(F).abs(), 3e-5, torch.bfloat16, "y")
+    dx, da, db = fq.fp4_lora_backward(dyd, xd, t, bank, sl)
+    dx64, da64, db64, mdx, mda, mdb = _backward64(dy, x, t.cpu(), a, b, sc, few, None)
+    _close(dx, dx64, mdx, 3e-5, torch.bfloat16, "dx")
+    used, which = torch.tensor(list(some), device="cuda"), list(some.values())
+    rest = torch.ones(la, dtype=torch.bool, device="cuda")
+    rest[used] = False
+    for got, want, mag, what in ((da, da64, mda, "da"), (db, db64, mdb, "db")):
+        assert not got.flatten(1).any(1)[rest].any(), what
+        _close(got[used], want[which], mag[which], 3e-5, torch.float32, what)
+    if m <= 16:
+        q = fq.fp4_quantize(_randn(g, n, k, sd=0.05).cuda(), 16, "e4m3", amax="current")
+        y = fq.fp4_wo_gemm_lora(x.cuda(), q, bank, sl)
+        w64 = _dequant64(q)
+        y64, _, my, _ = _forward64(x, a, b, sc, few, x.to(F) @ w64.t())
+        _close(y, y64, my + x.to(F).abs() @ w64.abs().t(), 3e-5, torch.bfloat16, "wo y")

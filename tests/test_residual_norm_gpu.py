@@ -194,3 +194,31 @@ def test_empty_batch_streams_and_replay():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all(torch.equal(a, b) for a, b in zip(_run_cuda(i), want))
         torch.cuda.synchronize()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: rows of zeros, which give and add zeros, and
+    three last rows like any others; then rows far apart in one allocation."""
+    rows, cols = 65600, 32768
+    assert (rows - 3) * cols > 2 ** 31
+    i = _inputs(3, cols, BF, BF, BF, True, True, 21)
+    d = _cuda(i)
+    for k in ("x", "res", "dn", "dh"):
+        v = torch.zeros(rows, cols, dtype=BF, device="cuda")
+        v[-3:] = d[k]
+        d[k] = v
+    d["gate"] = torch.cat([torch.ones(rows - 3, device="cuda"), d["gate"]])
+    h, n, _, dx, dres, dw2, dw1, dg = _run_cuda(d)
+    want = _reference(i, 0.5, 1e-6)
+    for k, v in dict(h=h, n=n, dx=dx, dres=dres).items():
+        assert not v[:-3].any(), k
+        _close(v[-3:], want[k], k)
+    for k, v in dict(dw_pre=dw2, dw_post=dw1, dgate=dg[-3:]).items():
+        _close(v, want[k], k)
+    j = dict(_cuda(i), gate=d["gate"][-3:])
+    for k in ("x", "res", "dn", "dh"):
+        j[k] = d[k].flatten().as_strided((3, cols), (2 ** 30, 1))
+        j[k].copy_(i[k])
+    h, n, _, dx, dres, dw2, dw1, dg = _run_cuda(j)
+    for k, v in dict(h=h, n=n, dx=dx, dres=dres, dw_pre=dw2, dw_post=dw1, dgate=dg).items():
+        _close(v, want[k], k)

@@ -234,3 +234,34 @@ def test_no_tokens_empty_batch_and_replay():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all(torch.equal(a, b) for a, b in zip(step(), want))
         torch.cuda.synchronize()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 logits: rows of zeros, whose results are known, and three
+    last rows like any others; then rows far apart in one allocation."""
+    g = torch.Generator().manual_seed(8)
+    n, v = 16400, 131000
+    assert (n - 3) * v > 2 ** 31
+    last = (torch.randn(3, v, generator=g) * 3).to(torch.bfloat16)
+    z = torch.zeros(n, v, dtype=torch.bfloat16, device="cuda")
+    z[-3:] = last.cuda()
+    tok = torch.randint(0, v, (n,), generator=g)
+    gl, ge = torch.randn(n, generator=g), torch.randn(n, generator=g)
+    f = fq.fp4_token_logprobs(z, tok.cuda(), top=2)
+    logv = float(torch.log(torch.tensor(v, dtype=F)))
+    _near(f.logprob[:-3], torch.full((n - 3,), -logv, dtype=F), "logprob of zeros")
+    _near(f.entropy[:-3], torch.full((n - 3,), logv, dtype=F), "entropy of zeros")
+    assert (f.top_ids[:-3].cpu() == torch.tensor([0, 1])).all()
+    hit, ent, ids, best, *_ = _reference(last, tok[-3:], 1.0, 2)
+    _near(f.logprob[-3:], hit, "logprob")
+    _near(f.entropy[-3:], ent, "entropy")
+    assert torch.equal(f.top_ids[-3:].cpu().long(), ids)
+    _near(f.top_logprobs[-3:], best, "top_logprobs")
+    dz = fq.fp4_token_logprobs_backward(z, tok.cuda(), f, gl.cuda(), ge.cuda())[-3:].cpu()
+    end = fq.fp4_token_logprobs(last.cuda(), tok[-3:].cuda(), top=2)
+    want = fq.fp4_token_logprobs_backward(last.cuda(), tok[-3:].cuda(), end, gl[-3:].cuda(), ge[-3:].cuda()).cpu()
+    # the two calls may add a row in other pieces: both are within 5e-5 + half a step of the formula's
+    assert torch.isclose(dz.float(), want.float(), rtol=2.0 ** -7 + 2e-4, atol=1e-9).all()
+    wide = z.flatten().as_strided((3, v), (2 ** 30, 1))
+    wide.copy_(last)
+    _check(wide, tok[-3:], top=2)
