@@ -244,7 +244,8 @@ fp4_status fp4_wo_gemm_lora(const uint16_t* x, int64_t ldx, int64_t m, const fp4
 static fp4_status check_logits(const void* z, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab, float temperature)
 {
     if (!dtype_ok(dtype)) return FP4_ERR_INVALID_ARG;
-    if (!(temperature > 0.0f) || !isfinite(temperature) || !isfinite(1.0f / temperature)) return FP4_ERR_INVALID_ARG;
+    // the kernels work with log2(e) / temperature
+    if (!(temperature > 0.0f) || !isfinite(temperature) || !isfinite(2.0f / temperature)) return FP4_ERR_INVALID_ARG;
     if (rows < 0 || vocab < 1 || ld < vocab) return FP4_ERR_SHAPE;
     if (rows >= kMaxLineRows || vocab >= (int64_t(1) << 27) || ld > kMaxElems / (rows ? rows : 1))
         return FP4_ERR_UNSUPPORTED;

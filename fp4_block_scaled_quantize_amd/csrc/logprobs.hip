@@ -53,24 +53,29 @@ struct Logit<false> {
 // Running sums in log2 units, about the maximum m (or -inf).
 struct Sums { float m, s, w; };
 
-constexpr float kLpFar = 1e30f;        // beyond it m k may leave binary32
+constexpr float kLpFar = 1e8f;         // beyond it RN(m k) is more than 4 from m k, far beyond it infinite
 
 // A thread's sums while it reads: about h = RN(m k) instead of m k, so that
 // an element costs one fused product and no subtraction (h only has to be
-// near the maximum); a maximum beyond kLpFar is subtracted first instead.
+// near the maximum); where m k is beyond kLpFar (a row of masks, a
+// temperature near zero) the maximum is subtracted first instead.
 struct Running {
     float m, h, s, w;
-    __device__ __forceinline__ bool far() const { return fabsf(m) > kLpFar && m != -INFINITY; }
+    __device__ __forceinline__ bool far(float k) const { return fabsf(m) * k > kLpFar && m != -INFINITY; }
     // raise the maximum to `to`
     __device__ __forceinline__ void raise(float to, float k)
     {
         if (!(to > m)) return;
-        const bool was = far(), first = m == -INFINITY;
+        const bool was = far(k), first = m == -INFINITY;
         const float m1 = m, h1 = h;
         m = to;
-        h = far() ? 0.0f : to * k;
+        const bool now = far(k);
+        h = now ? 0.0f : to * k;
         if (first) return;                             // nothing but zeros (or NaN) summed yet
-        const float d = fmaxf(was || far() ? (m1 - to) * k : h1 - h, -1000.0f), f = __builtin_amdgcn_exp2f(d);
+        float d = h1 - h;
+        if (was || now) d = was && now ? (m1 - to) * k : was ? __builtin_fmaf(m1, k, -h) : __builtin_fmaf(-to, k, h1);
+        d = fmaxf(d, -1000.0f);
+        const float f = __builtin_amdgcn_exp2f(d);
         w = f * __builtin_fmaf(d, s, w);
         s *= f;
     }
@@ -85,7 +90,7 @@ struct Running {
     // the sums about m k itself
     __device__ __forceinline__ Sums about_max(float k) const
     {
-        if (far() || m == -INFINITY) return Sums{m, s, w};
+        if (far(k) || m == -INFINITY) return Sums{m, s, w};
         const float d = __builtin_fmaf(m, k, -h), f = __builtin_amdgcn_exp2f(-d);
         return Sums{m, s * f, f * __builtin_fmaf(-d, s, w)};
     }
@@ -391,10 +396,10 @@ __global__ __launch_bounds__(THREADS) void k_lp_rows(LogprobLaunch p)
 #pragma unroll
         for (int j = 0; j < kLpVec * VN; ++j) best = fmaxf(best, f[j]);
         a.raise(best, k);
-        if (__builtin_amdgcn_ballot_w64(a.far())) {
+        if (__builtin_amdgcn_ballot_w64(a.far(k))) {
 #pragma unroll
             for (int j = 0; j < kLpVec * VN; ++j) {
-                if (a.far()) a.template add<true>(f[j], k);
+                if (a.far(k)) a.template add<true>(f[j], k);
                 else a.template add<false>(f[j], k);
             }
         } else {
@@ -421,7 +426,7 @@ __global__ __launch_bounds__(THREADS) void k_lp_rows(LogprobLaunch p)
         const bool in = tid < nh + nt;
         const float v = in ? L::one(z + i) : -INFINITY;
         a.raise(v, k);
-        if (a.far()) a.template add<true>(v, k);
+        if (a.far(k)) a.template add<true>(v, k);
         else a.template add<false>(v, k);
         if (TOP) {
             const float one[1]{v};
@@ -524,17 +529,20 @@ __global__ __launch_bounds__(256) void k_lp_backward(LogprobGradLaunch p)
     const float gl = p.g_logprob && t >= 0 && t < p.vocab && !empty ? p.g_logprob[row] : 0.0f;
     const float ge = p.g_entropy && !empty ? p.g_entropy[row] : 0.0f;
     const bool none = gl == 0.0f && ge == 0.0f;
-    const float k = c * kLog2e, logs2 = logs * kLog2e;
+    // probabilities times 2^16, which costs nothing: the instruction flushes
+    // powers below 2^-126, that a large coefficient would make visible
+    const float k = c * kLog2e, logs2 = __builtin_fmaf(logs, kLog2e, -16.0f);
     const float m0 = m == -INFINITY ? 0.0f : m;
-    // -c (gl + ge (log p + H)) as u + v log2 p
-    const float cu = -c * __builtin_fmaf(ge, ent, gl), cv = -c * ge * kLn2;
-    auto grad = [&](float x) {
+    // -2^-16 (gl + ge (log p + H)) as u + v (log2 p + 16); c comes last, where it is large (a
+    // temperature near zero) it must not overflow against p = 0
+    const float gv = -ge * kLn2 * 0x1p-16f, gu = __builtin_fmaf(-16.0f, gv, -__builtin_fmaf(ge, ent, gl) * 0x1p-16f);
+    auto grad = [&](float x, bool hit) {
         const float l2 = (x - m0) * k - logs2;
-        return __builtin_amdgcn_exp2f(l2) * __builtin_fmaf(cv, fmaxf(l2, -1000.0f), cu);
+        return c * __builtin_fmaf(__builtin_amdgcn_exp2f(l2), __builtin_fmaf(gv, fmaxf(l2, -1000.0f), gu), hit ? gl : 0.0f);
     };
     auto put = [&](int64_t i) {
         float g = 0.0f;
-        if (!none) g = grad(L::one(z + i)) + (i == t ? c * gl : 0.0f);
+        if (!none) g = grad(L::one(z + i), i == t);
         if constexpr (BF16) dz[i] = (uint16_t)f32_to_bf16_rne(g);
         else dz[i] = g;
     };
@@ -562,7 +570,7 @@ __global__ __launch_bounds__(256) void k_lp_backward(LogprobGradLaunch p)
                 L::unpack(raw[u], f);
                 const int64_t at = t - (vb + i * VN);
 #pragma unroll
-                for (int j = 0; j < VN; ++j) f[j] = grad(f[j]) + (at == j ? c * gl : 0.0f);
+                for (int j = 0; j < VN; ++j) f[j] = grad(f[j], at == j);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     if constexpr (BF16) out[q] = (int)pack_bf16(f[2 * q], f[2 * q + 1]);

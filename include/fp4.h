@@ -475,7 +475,8 @@ FP4_API fp4_status fp4_wo_gemm_lora(const uint16_t* x, int64_t ldx, int64_t m, c
  *     which the backward call reads
  * A logit of -inf has probability 0 and adds nothing.  A row of only -inf
  * has no probability: entropy 0, log probabilities -inf.  A NaN or +inf
- * makes its own row's results NaN.  Sums in binary32.
+ * makes its own row's results NaN.  Sums in binary32.  temperature > 0, and
+ * 2 / temperature is finite.
  * Fewer than 2^22 rows and 2^27 tokens.  workspace: as above,
  * fp4_token_logprobs_workspace bytes.
  */

@@ -265,3 +265,30 @@ def test_offsets_past_32_bits():
     wide = z.flatten().as_strided((3, v), (2 ** 30, 1))
     wide.copy_(last)
     _check(wide, tok[-3:], top=2)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("temp", [1e-37, 1e-30, 1e-12, 1e30])
+@pytest.mark.parametrize("n,v", [(4, 1000), (2, 9000)])
+def test_far_temperatures(dtype, temp, n, v):
+    """z / temperature may leave binary32 where (z - max) / temperature does
+    not matter any more: one token takes all, or all are alike."""
+    g = torch.Generator().manual_seed(v)
+    z = (torch.randn(n, v, generator=g) * 30).to(dtype)
+    z[1] -= 500
+    _check(z, _tokens(g, n, v), temp, 3)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,v", [(1, 700), (1, 9000), (1, 30011)])
+def test_far_logits(dtype, n, v):
+    """Rows of masks and rows of large logits, whose distances still matter,
+    rising and in any order."""
+    g = torch.Generator().manual_seed(v)
+    r = torch.randn(v, generator=g)
+    rows = [r * 0 - 1e10, r * 0 - 3e12, torch.where(r > 0, -1e10, r), r * 3 + 2e9, r * 1e12, r * 40 - 6.93e7, r * 40 + 6.93e7,
+            torch.sort(r).values * 40 - 6.93e7, torch.sort(r).values * 3e7, torch.sort(r.abs()).values * 1e9 - 1e9]
+    z = torch.stack(rows).to(dtype)
+    for i in range(len(rows)):
+        _check(z[i:i + 1], torch.tensor([v // 3]), 1.0, 2)
+    _check(z, torch.arange(len(rows)) * 7, 0.25, 2)

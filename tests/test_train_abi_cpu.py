@@ -96,7 +96,7 @@ def _lp(z=FAKE, dt=1, ld=1000, n=4, v=1000, tok=FAKE, temp=1.0, top=3, lp=FAKE, 
 
 @pytest.mark.parametrize("kw,want", [
     (dict(dt=2), -1), (dict(temp=0.0), -1), (dict(temp=-1.0), -1), (dict(temp=float("nan")), -1),
-    (dict(temp=float("inf")), -1), (dict(temp=1e-45), -1), (dict(n=-1), -3), (dict(v=0), -3), (dict(ld=999), -3),
+    (dict(temp=float("inf")), -1), (dict(temp=1e-45), -1), (dict(temp=4e-39), -1), (dict(n=-1), -3), (dict(v=0), -3), (dict(ld=999), -3),
     (dict(v=1 << 27, ld=1 << 27), -2), (dict(n=1 << 22), -2), (dict(z=None), -1), (dict(z=FAKE + 1), -4), (dict(dt=0, z=FAKE + 2), -4),
     (dict(top=-1), -2), (dict(top=33), -2), (dict(v=2, ld=2), -3), (dict(ent=None), -1), (dict(st=None), -1),
     (dict(lp=None), -1), (dict(ids=None), -1), (dict(best=None), -1), (dict(tok=FAKE + 4), -4), (dict(ent=FAKE + 2), -4),
