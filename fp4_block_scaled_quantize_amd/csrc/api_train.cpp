@@ -71,7 +71,7 @@ LoraSpace lora_space(int32_t call, int64_t m, int64_t n, int64_t k, int64_t rank
     if (w.down.splits > 1 || call == FP4_LORA_WO_GEMM) w.t = w.take(4 * w.down.splits * m * rank);
     if (back) {
         w.dt = w.take(4 * m * rank);
-        if (!lora_across(m, rank)) {
+        if (!lora_across(m, k, rank)) {
             w.at = w.take(2 * adapters * rank * k);
             w.bt = w.take(2 * adapters * rank * n);
         }
@@ -185,7 +185,7 @@ fp4_status fp4_lora_backward(const uint16_t* dy, int64_t ld_dy, const uint16_t* 
     hipStream_t s = (hipStream_t)stream;
     float* const dt = at<float>(workspace, w.dt);
     if (m > 0) {
-        const bool across = lora_across(m, bank->rank);
+        const bool across = lora_across(m, bank->k, bank->rank);
         uint16_t* const a_t = at<uint16_t>(workspace, w.at);
         uint16_t* const b_t = at<uint16_t>(workspace, w.bt);
         if (!across) {

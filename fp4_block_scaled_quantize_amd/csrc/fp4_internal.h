@@ -174,7 +174,7 @@ struct LoraUp {
     int32_t across;            // b is [adapters, rank, n] instead
 };
 hipError_t launch_lora_up(const LoraUp& p, hipStream_t s);
-bool lora_across(int64_t m, int64_t rank);
+bool lora_across(int64_t m, int64_t k, int64_t rank);
 
 struct LoraTranspose {
     const uint16_t* src[2]; uint16_t* dst[2];

@@ -52,7 +52,7 @@ __device__ __forceinline__ void bf16_terms(float a, float b, uint32_t (&out)[NT]
 
 // Eight elements `stride` apart as a fragment: an operand whose contraction
 // runs across its rows (TR below).  A backward call of few rows takes B and A
-// that way; for more rows they are transposed once (k_lora_transpose).
+// that way; for more work they are transposed once (k_lora_transpose).
 __device__ __forceinline__ v4i gather8(const uint16_t* p, int64_t stride)
 {
     uint16_t e[8];
@@ -822,8 +822,6 @@ LoraDownShape lora_down_shape(int64_t m, int64_t k, int rank, int64_t adapters)
     return s;
 }
 
-constexpr int64_t kAcrossRows = 256;
-
 static int outer_rt(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 4; }
 
 // The row ranges of the gradient sums, at least 256 rows each (two chunks a
@@ -845,8 +843,12 @@ template <int RT, bool TR>
 static hipError_t run_down(const LoraDown& p, const LoraDownShape& sh, hipStream_t s)
 {
     const dim3 grid((unsigned)sh.splits, (unsigned)(sh.few ? 1 : cdiv(p.m, kDownRows)), (unsigned)sh.z);
-    if (sh.few) hipLaunchKernelGGL((k_lora_down_few<RT, TR>), grid, dim3(64 * kFewWaves), 0, s, p);
-    else hipLaunchKernelGGL((k_lora_down<RT, TR>), grid, dim3(64 * kDownWaves), 0, s, p);
+    if constexpr (!TR || RT <= 4)             // the rule of lora_across
+        if (sh.few) {
+            hipLaunchKernelGGL((k_lora_down_few<RT, TR>), grid, dim3(64 * kFewWaves), 0, s, p);
+            return hipGetLastError();
+        }
+    hipLaunchKernelGGL((k_lora_down<RT, TR>), grid, dim3(64 * kDownWaves), 0, s, p);
     return hipGetLastError();
 }
 
@@ -901,7 +903,8 @@ static hipError_t up_by_rank(const LoraUp& p, hipStream_t s)
     constexpr bool SH = WM == 4 && !TR;
     if (p.rank <= 32) return run_up<WM, 1, TR>(p, s);
     if (p.rank <= 64) return run_up<WM, 2, TR, SH>(p, s);
-    return run_up<WM, 4, TR, SH>(p, s);
+    if constexpr (WM == 1 && TR) return hipErrorInvalidValue;     // not by lora_across
+    else return run_up<WM, 4, TR, SH>(p, s);
 }
 
 hipError_t launch_lora_up(const LoraUp& p, hipStream_t s)
@@ -910,11 +913,18 @@ hipError_t launch_lora_up(const LoraUp& p, hipStream_t s)
     return p.across ? up_by_rank<4, true>(p, s) : up_by_rank<4, false>(p, s);
 }
 
-// A backward call of few rows and a rank up to 64 reads B and A across their
-// rows (eight loads for a fragment) instead of transposing them first, which
-// saves a launch.  200 rows, 11008 x 4096: rank 16 28.4 us against 31.2, rank 64
-// 47.3 against 49.2, but rank 128 98.7 against 82.1.
-bool lora_across(int64_t m, int64_t rank) { return m <= kAcrossRows && rank <= 64; }
+// A backward call reads B and A across their rows (eight loads for a fragment)
+// instead of transposing them first, which saves a launch, while that work
+// (rows times columns of dx) is small: 200 rows, 11008 x 4096: rank 16 28.4 us
+// against 31.2, rank 128 72.6 against 78.0; 2048 rows, 1024 x 1024, rank 16:
+// 25.8 against 30.2; but 1024 rows, 4096 x 11008, rank 16: 50.0 against 47.3, and
+// 8192 rows, 1024 x 1024: 43.4 against 41.9.  Up to 16 rows, whose T is one
+// launch of little work, ranks above 64 gather too much (16 rows, 520 x 1000,
+// rank 80: 33.2 against 29.0).
+bool lora_across(int64_t m, int64_t k, int64_t rank)
+{
+    return m * k <= (int64_t(1) << 22) && (m > 16 || rank <= 64);
+}
 
 hipError_t launch_lora_transpose(const uint16_t* a, uint16_t* at, const uint16_t* b, uint16_t* bt, int64_t adapters,
                                  int64_t rank, int64_t k, int64_t n, hipStream_t s)

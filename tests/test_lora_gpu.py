@@ -84,6 +84,8 @@ SHAPES = [  # m, n, k, rank, adapters, slots
     (130, 264, 520, 8, 3, "runs"), (200, 1032, 4096, 32, 2, "mixed"), (300, 776, 776, 128, 3, "runs"),
     (2100, 1032, 136, 16, 3, "runs"), (2050, 520, 264, 24, 2, "mixed"), (3000, 776, 136, 32, 40, "mixed"),
     (2048, 512, 40, 8, 1, "none"), (2500, 600, 72, 16, 1, "one"),
+    (1100, 264, 3848, 16, 4, "runs"), (2050, 72, 2104, 40, 3, "mixed"), (600, 136, 7208, 128, 2, "runs"), (4200, 520, 1032, 24, 5, "runs"),
+    (530, 136, 8200, 72, 2, "one"), (9, 520, 264, 96, 3, "mixed"),
     (513, 136, 264, 56, 40, "mixed"), (1100, 264, 392, 16, 4, "runs"), (2050, 264, 136, 48, 2, "mixed"),
 ]
 
