@@ -602,7 +602,7 @@ __global__ __launch_bounds__(256) void k_lora_transpose(LoraTranspose p)
 // in both operands (an infinity there must not meet a zero).  Row ranges
 // (gridDim.z) leave partial sums, joined in a fixed order by k_lora_join.
 // Bound by reading D (once, past the caches): 8192 x (4096 + 11008), rank 16,
-// 247 MB: 51 us, 4.9 TB/s; 63 us through the caches and with a chunk's loads
+// 247 MB: 48 us, 5.1 TB/s; 63 us through the caches and with a chunk's loads
 // waiting for its rows' adapters.
 // ---------------------------------------------------------------------------
 template <int RT, int NT>
@@ -802,8 +802,8 @@ static int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo :
 // K ranges: about two workgroups of four waves for a CU (or many small ones
 // for a few rows), none with less than one chunk a wave, at most 32 partial
 // sums for the reader to join; four for a CU where each still has four chunks
-// a wave or more (8192 rows of 11008: 42 us against 47; of 4096, where it would
-// not: 25 against 18).  Then the adapters of a tile side by side while that
+// a wave or more (8192 rows of 11008: 42 us against 48; of 4096, where it would
+// not: 20 against 18).  Then the adapters of a tile side by side while that
 // leaves the device unfilled.
 LoraDownShape lora_down_shape(int64_t m, int64_t k, int rank, int64_t adapters)
 {
