@@ -589,7 +589,19 @@ __global__ __launch_bounds__(256) void k_lp_backward(LogprobGradLaunch p)
 // ---------------------------------------------------------------------------
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int64_t kLpWaveVocab = 2048;
+// Whether a whole row is one wave's instead of four's: without top alternatives
+// where it is short (8192 rows of 9000, bf16: 33 us against 47; of 32000 100
+// against 94).  With them four waves keep four lists, each of which takes in
+// its first few hundred logits, and wait to join them, so one is better
+// wherever the rows alone fill the device (top 1: 4235 rows of 142 14 us
+// against 53, 1500 of 9000 17 against 26, 5030 of 21562 59 against 93, 8192 of
+// 32000 119 against 169; but 600 of 12000, top 20, 22 against 17, 600 of 30000 29
+// against 22, 1061 of 115285 89 against 74).
+static bool row_is_a_wave(int64_t rows, int64_t vocab, bool top)
+{
+    if (!top) return vocab <= 16384;
+    return vocab <= 4096 || rows >= (vocab <= 16384 ? 1024 : 2000);
+}
 
 // A row stays whole when the rows alone fill the device; else it is cut so
 // that about 512 workgroups run, none with less than 4096 elements (two bf16
@@ -609,9 +621,8 @@ static hipError_t run_logprobs(LogprobLaunch p, int64_t pieces, hipStream_t s)
     p.piece = cdiv(cdiv(p.vocab, pieces), 64) * 64;
     pieces = cdiv(p.vocab, p.piece);
     const dim3 grid((unsigned)p.rows, (unsigned)pieces);
-    // a short row of many is one wave's: nothing to join (4235 rows of 142: 14
-    // us against 53 with four waves a row)
-    if (pieces == 1 && p.vocab <= kLpWaveVocab) hipLaunchKernelGGL((k_lp_rows<BF16, TOP, 64>), grid, dim3(64), 0, s, p);
+    const bool wave = pieces == 1 && row_is_a_wave(p.rows, p.vocab, TOP);
+    if (wave) hipLaunchKernelGGL((k_lp_rows<BF16, TOP, 64>), grid, dim3(64), 0, s, p);
     else hipLaunchKernelGGL((k_lp_rows<BF16, TOP, 256>), grid, dim3(256), 0, s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || pieces == 1) return e;

@@ -292,3 +292,29 @@ def test_far_logits(dtype, n, v):
     for i in range(len(rows)):
         _check(z[i:i + 1], torch.tensor([v // 3]), 1.0, 2)
     _check(z, torch.arange(len(rows)) * 7, 0.25, 2)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,v", [(600, 6001), (515, 16383), (2003, 16500), (1999, 16500)])
+def test_many_rows(dtype, n, v):
+    """Many rows at once: the last ones against binary64, all of them against
+    the same rows in small batches, which are cut another way."""
+    g = torch.Generator(device="cuda").manual_seed(n + v)
+    z = (torch.randn(n, v, generator=g, device="cuda") * 3).to(dtype)
+    tok = torch.randint(0, v, (n,), generator=g, device="cuda")
+    f = fq.fp4_token_logprobs(z, tok, temperature=0.8, top=20)
+    hit, ent, ids, best, *_ = _reference(z[-16:].cpu(), tok[-16:].cpu(), 0.8, 20)
+    _near(f.logprob[-16:], hit, "logprob")
+    _near(f.entropy[-16:], ent, "entropy")
+    assert torch.equal(f.top_ids[-16:].cpu().long(), ids)
+    _near(f.top_logprobs[-16:], best, "top_logprobs")
+    none = fq.fp4_token_logprobs(z, tok, temperature=0.8)
+    for a in range(0, n, 256):
+        few = fq.fp4_token_logprobs(z[a:a + 256], tok[a:a + 256], temperature=0.8, top=20)
+        assert torch.equal(f.top_ids[a:a + 256], few.top_ids)
+        for what in ("logprob", "entropy", "top_logprobs"):        # each within 5e-5 of the formula
+            one, two = getattr(f, what)[a:a + 256], getattr(few, what)
+            assert ((one - two).abs() <= 1e-4 + two.abs() * 2.0 ** -21).all(), what
+        for what in ("logprob", "entropy"):
+            one, two = getattr(none, what)[a:a + 256], getattr(few, what)
+            assert ((one - two).abs() <= 1e-4 + two.abs() * 2.0 ** -21).all(), what
