@@ -51,8 +51,8 @@ __device__ __forceinline__ void bf16_terms(float a, float b, uint32_t (&out)[NT]
 }
 
 // Eight elements `stride` apart as a fragment: an operand whose contraction
-// runs across its rows (TR below).  A backward call of few rows takes B and A
-// that way; for more work they are transposed once (k_lora_transpose).
+// runs across its rows (TR below).  A small backward call takes B and A
+// that way; for a larger one they are transposed once (k_lora_transpose).
 __device__ __forceinline__ v4i gather8(const uint16_t* p, int64_t stride)
 {
     uint16_t e[8];
