@@ -8,9 +8,9 @@
 //   backward  dT = s_l dy B_l,  dx = base + dT A_l,
 //             dA_l = sum_i dT_i^T x_i,  dB_l = s_l sum_i dy_i^T T_i
 // T and dT stay in binary32.  Where one enters a bf16 matrix instruction it
-// goes in as a sum of bf16 terms, t = hi + lo (16 significant bits; plus a
-// third term, 24 bits, for gradients returned in binary32), so the results
-// are rounded once, at the end.
+// goes in as the sum of three bf16 terms, which hold its 24 bits, so the
+// results are rounded once, at the end.  (Two terms, 16 bits, rounded about one
+// output in a thousand the other way and saved nothing that showed.)
 #include "fp4_device.hpp"
 #include "fp4_internal.h"
 
@@ -33,17 +33,17 @@ __device__ __forceinline__ int row_slot(const int32_t* slots, int64_t row, int64
     return s >= 0 && s < adapters ? s : -1;
 }
 
-// Two values as NT bf16 terms each, packed (a in the low half): each term the
-// rounding of what the ones before leave.  A value that rounds to infinity
+// Two values as three bf16 terms each, packed (a in the low half): each term
+// the rounding of what the ones before leave.  A value that rounds to infinity
 // leaves nothing, so that it stays one.
-template <int NT>
-__device__ __forceinline__ void bf16_terms(float a, float b, uint32_t (&out)[NT])
+constexpr int kTerms = 3;
+__device__ __forceinline__ void bf16_terms(float a, float b, uint32_t (&out)[kTerms])
 {
     constexpr float kTop = 3.3961775e38f;               // the midpoint above the largest bf16
     const bool fa = !(fabsf(a) >= kTop), fb = !(fabsf(b) >= kTop);
     out[0] = pack_bf16(a, b);
 #pragma unroll
-    for (int i = 1; i < NT; ++i) {
+    for (int i = 1; i < kTerms; ++i) {
         a = fa ? a - bf16_lo(out[i - 1]) : 0.0f;
         b = fb ? b - bf16_hi(out[i - 1]) : 0.0f;
         out[i] = pack_bf16(a, b);
@@ -297,8 +297,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraDown p)
 }
 
 // ---------------------------------------------------------------------------
-// y = base + s_l T B_l^T: a wave owns 16 rows, holds their T as hi and lo
-// fragments and walks the columns 64 at a time.  Bound by memory, so the wave
+// y = base + s_l T B_l^T: a wave owns 16 rows, holds their T as fragments of
+// its terms and walks the columns 64 at a time.  Bound by memory, so the wave
 // is kept small (many in flight) and base and y move in whole 128-byte lines:
 // the products, which leave the matrix instructions as 4 columns of a row a
 // lane, pass through the wave's own 4 KB of LDS and come back as 8 columns a
@@ -311,8 +311,10 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraDown p)
 // one whose B is multiplied drop the result (a select, so that nothing of one
 // adapter reaches another's rows).
 // ---------------------------------------------------------------------------
+// Four waves a SIMD up to rank 32, which the compiler would pass by four
+// registers.
 template <int WM, int RC, bool TR, bool SH>
-__global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
+__global__ __launch_bounds__(256, RC == 1 && !TR ? 4 : 1) void k_lora_up(LoraUp p)
 {
     constexpr int WN = 4 / WM;                          // waves side by side along the columns
     constexpr int Pitch = 68;                           // floats: 17 times 16 bytes
@@ -342,7 +344,7 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
     const int slot = row_slot(p.slots, m, M, p.adapters);   // the same in the four lanes of a row
     float* const out = tile[wave];
 
-    v4i th[RC], tl[RC];
+    v4i tf[RC][kTerms];
     {
         v4f v[RC][2];
 #pragma unroll
@@ -367,10 +369,10 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                uint32_t x[2];
-                bf16_terms<2>(v[c][q >> 1][2 * (q & 1)], v[c][q >> 1][2 * (q & 1) + 1], x);
-                th[c][q] = (int)x[0];
-                tl[c][q] = (int)x[1];
+                uint32_t x[kTerms];
+                bf16_terms(v[c][q >> 1][2 * (q & 1)], v[c][q >> 1][2 * (q & 1) + 1], x);
+#pragma unroll
+                for (int i = 0; i < kTerms; ++i) tf[c][i][q] = (int)x[i];
             }
         }
     }
@@ -419,10 +421,9 @@ __global__ __launch_bounds__(256) void k_lora_up(LoraUp p)
             for (int h = 0; h < 2; ++h) {
                 v4f acc{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int c = 0; c < RC; ++c) {
-                    acc = mfma16(bf[u][h][c], tl[c], acc);
-                    acc = mfma16(bf[u][h][c], th[c], acc);
-                }
+                for (int c = 0; c < RC; ++c)
+#pragma unroll
+                    for (int i = kTerms - 1; i >= 0; --i) acc = mfma16(bf[u][h][c], tf[c][i], acc);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[u][h][e] = slot == cur ? acc[e] * s : o[u][h][e];
             }
@@ -605,7 +606,7 @@ __global__ __launch_bounds__(256) void k_lora_transpose(LoraTranspose p)
 // 247 MB: 48 us, 5.1 TB/s; 63 us through the caches and with a chunk's loads
 // waiting for its rows' adapters.
 // ---------------------------------------------------------------------------
-template <int RT, int NT>
+template <int RT>
 __global__ __launch_bounds__(256, RT == 1 ? 3 : RT == 2 ? 2 : 1) void k_lora_outer(LoraOuter p)
 {
     __shared__ v4f red[8 * RT * 64];
@@ -673,7 +674,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : RT == 2 ? 2 : 1) void k_lora_out
     for (; mc < me; mc += 128) {
         const uint32_t now = rows;
         v4i f[8];
-        v4i pf[RT][NT];
+        v4i pf[RT][kTerms];
         if (now) {
             any = 1;
             const uint32_t keep = (now >> (8 * grp)) & 0xFFu;
@@ -690,10 +691,10 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : RT == 2 ? 2 : 1) void k_lora_out
             for (int t = 0; t < RT; ++t)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t x[NT];
-                    bf16_terms<NT>(pv[t][2 * q], pv[t][2 * q + 1], x);
+                    uint32_t x[kTerms];
+                    bf16_terms(pv[t][2 * q], pv[t][2 * q + 1], x);
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) pf[t][i][q] = (int)x[i];
+                    for (int i = 0; i < kTerms; ++i) pf[t][i][q] = (int)x[i];
                 }
 #pragma unroll
             for (int ci = 0; ci < 8; ++ci)
@@ -711,7 +712,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : RT == 2 ? 2 : 1) void k_lora_out
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
 #pragma unroll
-                    for (int i = NT - 1; i >= 0; --i) acc[ci][t] = mfma16(f[ci], pf[t][i], acc[ci][t]);
+                    for (int i = kTerms - 1; i >= 0; --i) acc[ci][t] = mfma16(f[ci], pf[t][i], acc[ci][t]);
         }
     }
     any = __syncthreads_or(any);
@@ -937,11 +938,11 @@ hipError_t launch_lora_transpose(const uint16_t* a, uint16_t* at, const uint16_t
     return hipGetLastError();
 }
 
-template <int RT, int NT>
+template <int RT>
 static hipError_t run_outer(const LoraOuter& p, int64_t splits, hipStream_t s)
 {
     const dim3 grid((unsigned)(p.tiles[0] + p.tiles[1]), (unsigned)(p.adapters * cdiv(p.rank, 16 * RT)), (unsigned)splits);
-    hipLaunchKernelGGL((k_lora_outer<RT, NT>), grid, dim3(256), 0, s, p);
+    hipLaunchKernelGGL((k_lora_outer<RT>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
@@ -953,9 +954,9 @@ hipError_t launch_lora_outer(const LoraOuter& in, int64_t splits, hipStream_t s)
     p.mstep = cdiv(cdiv(p.m, splits), 128) * 128;
     hipError_t e;
     const int rt = outer_rt(p.rank);
-    if (rt == 1) e = p.out_bf16 ? run_outer<1, 2>(p, splits, s) : run_outer<1, 3>(p, splits, s);
-    else if (rt == 2) e = p.out_bf16 ? run_outer<2, 2>(p, splits, s) : run_outer<2, 3>(p, splits, s);
-    else e = p.out_bf16 ? run_outer<4, 2>(p, splits, s) : run_outer<4, 3>(p, splits, s);
+    if (rt == 1) e = run_outer<1>(p, splits, s);
+    else if (rt == 2) e = run_outer<2>(p, splits, s);
+    else e = run_outer<4>(p, splits, s);
     if (e != hipSuccess || splits == 1) return e;
     const int64_t most = p.adapters * p.rank * (p.job[0].c > p.job[1].c ? p.job[0].c : p.job[1].c);
     hipLaunchKernelGGL(k_lora_join, dim3((unsigned)clamp64(cdiv(most, 1024), 1, 2048)), dim3(256), 0, s, p, (int)splits);
