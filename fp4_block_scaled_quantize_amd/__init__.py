@@ -470,7 +470,8 @@ def _allocating(stream, device: torch.device):
     if stream is None:
         return _HERE_AND_NOW
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device)
+        # torch takes a pointer of 0 for none given and would make a new stream
+        stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
 
 
