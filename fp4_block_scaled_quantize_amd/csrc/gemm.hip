@@ -2041,7 +2041,10 @@ struct WoRow {
     static constexpr int WP = WB <= 64 ? 64 : 128;
 };
 
-template <int NW, int D, int RG, int XQ, int BLOCK, bool SPLIT, bool POW2, int ELEM = 0, int SUB = 1>
+// AD: the rows' adapters in the epilogue.  A form of its own: as a condition of
+// every launch it took a quarter of the plain product's waves by its registers
+// (18944 x 3584, 8 rows 15.8 us against 15.5, 16 rows 18.1 against 17.9).
+template <int NW, int D, int RG, int XQ, int BLOCK, bool SPLIT, bool POW2, int ELEM, int SUB, bool AD>
 __global__ __launch_bounds__(64 * NW) void k_wo_gemm(WoGemmLaunch p)
 {
     constexpr bool WIDE = ELEM >= 2;
@@ -2263,7 +2266,7 @@ __global__ __launch_bounds__(64 * NW) void k_wo_gemm(WoGemmLaunch p)
     // T [M, rank] of the rows' adapters, joined from its partial sums (four ranks
     // a thread: 16 rows of rank 32 in 19 sums 16.5 us, one a thread 18)
     float* const ts = reinterpret_cast<float*>(wo_ring) + NW * RG * 256;
-    if (p.ad.t) {
+    if constexpr (AD) {
         const int quads = (int)M * p.ad.rank / 4;
         for (int e = tid; e < quads; e += 64 * NW) {
             const v4f* const at = reinterpret_cast<const v4f*>(p.ad.t) + e;
@@ -2283,7 +2286,7 @@ __global__ __launch_bounds__(64 * NW) void k_wo_gemm(WoGemmLaunch p)
         const int64_t m = 4 * (l >> 4) + r, nn = n0 + 16 * g + (l & 15);
         if (m < M && nn < N) {
             float v = sum * gres;
-            if (p.ad.t) {
+            if constexpr (AD) {
                 const int sl = p.ad.slots[m];
                 if (sl >= 0 && sl < p.ad.adapters) {
                     const uint16_t* const b = p.ad.b + ((int64_t)sl * N + nn) * p.ad.rank;
@@ -2307,26 +2310,37 @@ __global__ __launch_bounds__(64 * NW) void k_wo_gemm(WoGemmLaunch p)
 template <int RG, int XQ, int ELEM, int SUB, int BLOCK>
 using WoSlotOf = WoSlot<RG, XQ, WoRow<ELEM, SUB>::WP, SUB, 128 * SUB / BLOCK>;
 
-// A ring of NW waves x D slots when it fits the LDS next to the scale
-// table, else four waves x two slots.
-template <int NW, int D, int RG, int XQ, int BLOCK, bool SPLIT, bool POW2, int ELEM, int SUB>
-static hipError_t launch_wo_k(const WoGemmLaunch& p, hipStream_t s)
+template <int NW, int D, int RG, int XQ, int BLOCK, bool SPLIT, bool POW2, int ELEM, int SUB, bool AD>
+static hipError_t launch_wo_a(const WoGemmLaunch& p, hipStream_t s)
 {
-    // the ring, later the partial tiles and the adapters' T (16 rows of up to 128)
+    // the ring, later the partial tiles and, with adapters, their T (16 rows of up to 128)
     constexpr size_t ring = (size_t)NW * D * WoSlotOf<RG, XQ, ELEM, SUB, BLOCK>::Bytes;
-    constexpr size_t tail = sizeof(float) * (NW * RG * 256 + 16 * 128);
+    constexpr size_t tail = sizeof(float) * (NW * RG * 256 + (AD ? 16 * 128 : 0));
+    static_assert(AD || ring >= tail, "partial tiles fit the ring");
     constexpr size_t sh = ring > tail ? ring : tail;
-    if constexpr (sh + sizeof(float) * 256 > 160 * 1024) {
-        static_assert(NW != 4 || D != 2, "the smallest ring fits");
-        return launch_wo_k<4, 2, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB>(p, s);
-    }
     if (sh > 64 * 1024) {
-        const hipError_t e = allow_lds(k_wo_gemm<NW, D, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB>, sh);
+        const hipError_t e = allow_lds(k_wo_gemm<NW, D, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB, AD>, sh);
         if (e != hipSuccess) return e;
     }
     const dim3 grid((unsigned)((p.n + 16 * RG - 1) / (16 * RG))), block(64 * NW);
-    hipLaunchKernelGGL((k_wo_gemm<NW, D, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB>), grid, block, sh, s, p);
+    hipLaunchKernelGGL((k_wo_gemm<NW, D, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB, AD>), grid, block, sh, s, p);
     return hipGetLastError();
+}
+
+// A ring of NW waves x D slots when it fits the LDS next to the scale
+// table, else four waves x two slots: the same with adapters as without, so
+// that a row that has none keeps the plain product's bits.
+template <int NW, int D, int RG, int XQ, int BLOCK, bool SPLIT, bool POW2, int ELEM, int SUB>
+static hipError_t launch_wo_k(const WoGemmLaunch& p, hipStream_t s)
+{
+    constexpr size_t ring = (size_t)NW * D * WoSlotOf<RG, XQ, ELEM, SUB, BLOCK>::Bytes;
+    if constexpr (ring + sizeof(float) * 256 > 160 * 1024) {
+        static_assert(NW != 4 || D != 2, "the smallest ring fits");
+        return launch_wo_k<4, 2, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB>(p, s);
+    } else {
+        if (p.ad.t) return launch_wo_a<NW, D, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB, true>(p, s);
+        return launch_wo_a<NW, D, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB, false>(p, s);
+    }
 }
 
 // Significant bits of the largest element of each grid (E2M1 2, INT4 3,
