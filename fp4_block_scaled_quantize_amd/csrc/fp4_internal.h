@@ -178,7 +178,7 @@ bool lora_across(int64_t m, int64_t k, int64_t rank);
 
 struct LoraTranspose {
     const uint16_t* src[2]; uint16_t* dst[2];
-    int64_t rows[2], cols[2], blocks[2];
+    int64_t rows[2], cols[2], blocks[2];                  // blocks: tiles of one adapter
 };
 hipError_t launch_lora_transpose(const uint16_t* a, uint16_t* at, const uint16_t* b, uint16_t* bt, int64_t adapters,
                                  int64_t rank, int64_t k, int64_t n, hipStream_t s);

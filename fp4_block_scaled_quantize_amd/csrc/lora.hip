@@ -555,7 +555,9 @@ __global__ __launch_bounds__(256) void k_lora_sum(const float* parts, int splits
 
 // ---------------------------------------------------------------------------
 // A_l [R, K] -> [K, R] and B_l [N, R] -> [R, N], 64 x 64 tiles through LDS:
-// the backward products contract over the other index of each.
+// the backward products contract over the other index of each.  gridDim.x are
+// one adapter's tiles, gridDim.y the adapters: the tiles of a whole bank may
+// pass the 2^32 threads that one dimension takes.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256) void k_lora_transpose(LoraTranspose p)
 {
@@ -564,9 +566,8 @@ __global__ __launch_bounds__(256) void k_lora_transpose(LoraTranspose p)
     const int which = b >= p.blocks[0];
     if (which) b -= p.blocks[0];
     const int64_t rows = p.rows[which], cols = p.cols[which];
-    const int64_t tr = (rows + 63) / 64, tc = (cols + 63) / 64;
-    const int64_t l = b / (tr * tc), in = b % (tr * tc);
-    const int64_t r0 = in / tc * 64, c0 = in % tc * 64;
+    const int64_t tc = (cols + 63) / 64, l = blockIdx.y;
+    const int64_t r0 = b / tc * 64, c0 = b % tc * 64;
     const uint16_t* const src = p.src[which] + l * rows * cols;
     uint16_t* const dst = p.dst[which] + l * rows * cols;
     for (int e = threadIdx.x; e < 64 * 8; e += 256) {
@@ -933,8 +934,9 @@ hipError_t launch_lora_transpose(const uint16_t* a, uint16_t* at, const uint16_t
     LoraTranspose p;
     p.src[0] = a; p.dst[0] = at; p.rows[0] = rank; p.cols[0] = k;
     p.src[1] = b; p.dst[1] = bt; p.rows[1] = n; p.cols[1] = rank;
-    for (int i = 0; i < 2; ++i) p.blocks[i] = adapters * cdiv(p.rows[i], 64) * cdiv(p.cols[i], 64);
-    hipLaunchKernelGGL(k_lora_transpose, dim3((unsigned)(p.blocks[0] + p.blocks[1])), dim3(256), 0, s, p);
+    for (int i = 0; i < 2; ++i) p.blocks[i] = cdiv(p.rows[i], 64) * cdiv(p.cols[i], 64);
+    const dim3 grid((unsigned)(p.blocks[0] + p.blocks[1]), (unsigned)adapters);
+    hipLaunchKernelGGL(k_lora_transpose, grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 
