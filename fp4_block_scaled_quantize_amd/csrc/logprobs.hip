@@ -529,16 +529,18 @@ __global__ __launch_bounds__(256) void k_lp_backward(LogprobGradLaunch p)
     const float gl = p.g_logprob && t >= 0 && t < p.vocab && !empty ? p.g_logprob[row] : 0.0f;
     const float ge = p.g_entropy && !empty ? p.g_entropy[row] : 0.0f;
     const bool none = gl == 0.0f && ge == 0.0f;
-    // probabilities times 2^16, which costs nothing: the instruction flushes
-    // powers below 2^-126, that a large coefficient would make visible
-    const float k = c * kLog2e, logs2 = __builtin_fmaf(logs, kLog2e, -16.0f);
+    // p is taken as the square of h = 2^(log2 p / 2): the instruction flushes
+    // powers below 2^-126, which a large coefficient would make visible.  (A
+    // power of p times 2^16 needs log2 p + 16, which in a confident row rounds
+    // log p and the entropy away.)
+    const float k = 0.5f * c * kLog2e, hlogs = 0.5f * logs * kLog2e;
     const float m0 = m == -INFINITY ? 0.0f : m;
-    // -2^-16 (gl + ge (log p + H)) as u + v (log2 p + 16); c comes last, where it is large (a
+    // -(gl + ge (log p + H)) as gu + gv (log2 p / 2); c comes last: where it is large (a
     // temperature near zero) it must not overflow against p = 0
-    const float gv = -ge * kLn2 * 0x1p-16f, gu = __builtin_fmaf(-16.0f, gv, -__builtin_fmaf(ge, ent, gl) * 0x1p-16f);
+    const float gv = -2.0f * kLn2 * ge, gu = -__builtin_fmaf(ge, ent, gl);
     auto grad = [&](float x, bool hit) {
-        const float l2 = (x - m0) * k - logs2;
-        return c * __builtin_fmaf(__builtin_amdgcn_exp2f(l2), __builtin_fmaf(gv, fmaxf(l2, -1000.0f), gu), hit ? gl : 0.0f);
+        const float l = (x - m0) * k - hlogs, h = __builtin_amdgcn_exp2f(l);
+        return c * __builtin_fmaf(h, h * __builtin_fmaf(gv, fmaxf(l, -1000.0f), gu), hit ? gl : 0.0f);
     };
     auto put = [&](int64_t i) {
         float g = 0.0f;
