@@ -8,7 +8,8 @@
 //   logprob(t) = d_t - log s,  entropy = log s - w / s
 //   dz_v = c (gl ([v = t] - p_v) - ge p_v (log p_v + entropy))
 // One pass over a row keeps the running (m, s, w) of every thread in
-// binary32: a larger maximum m' = m + D rescales s by f = exp(-c D) and w to
+// binary32 (a round of loads is summed on its own first, so that a thread's
+// sum of thousands of terms takes few roundings): a larger maximum m' = m + D rescales s by f = exp(-c D) and w to
 // f (w - c D s).  The kernels work in powers of two (k = c log2 e), where w
 // carries log2 units.
 #include <type_traits>
@@ -396,6 +397,11 @@ __global__ __launch_bounds__(THREADS) void k_lp_rows(LogprobLaunch p)
 #pragma unroll
         for (int j = 0; j < kLpVec * VN; ++j) best = fmaxf(best, f[j]);
         a.raise(best, k);
+        // the round's terms add up on their own before they join the row's: a
+        // thread's sum takes roundings for the terms of one round and for the
+        // rounds, not for thousands of terms
+        const float s = a.s, w = a.w;
+        a.s = a.w = 0.0f;
         if (__builtin_amdgcn_ballot_w64(a.far(k))) {
 #pragma unroll
             for (int j = 0; j < kLpVec * VN; ++j) {
@@ -406,6 +412,8 @@ __global__ __launch_bounds__(THREADS) void k_lp_rows(LogprobLaunch p)
 #pragma unroll
             for (int j = 0; j < kLpVec * VN; ++j) a.template add<false>(f[j], k);
         }
+        a.s += s;
+        a.w += w;
         if (TOP) {
             if (first) list.start(in[0], best);
             first = false;
