@@ -129,9 +129,15 @@ def _check(status: int, what: str):
         raise Fp4Error(status, what)
 
 
+# The handle of a device's current stream: torch's private call for it makes no
+# Stream object, whose cost a launch-bound call notices.
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream(stream, device: torch.device | None = None) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device.index)
+        return _current_handle(torch.cuda.current_device() if device is None else device.index)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

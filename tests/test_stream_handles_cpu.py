@@ -4,11 +4,14 @@ names it in.  Handle 0 is the default stream (what
 torch.cuda.current_stream().cuda_stream gives a caller who has set nothing);
 torch's ExternalStream(0) is not that stream but a new one."""
 import contextlib
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import fp4_block_scaled_quantize_amd as fq
+from tests.conftest import ROOT
 
 BF = torch.bfloat16
 
@@ -84,3 +87,18 @@ def test_memory_belongs_to_the_stream_of_the_handle(host, name, handle, owner):
     call()
     assert lib.streams == [handle]
     assert made and set(made) == {owner}
+
+
+def test_current_stream_without_torchs_private_call():
+    """The calls of every operator ask for the current stream's handle; a torch
+    that lacks the private function for it leaves the public one."""
+    code = (
+        "import torch\n"
+        "if hasattr(torch._C, '_cuda_getCurrentRawStream'):\n"
+        "    del torch._C._cuda_getCurrentRawStream\n"
+        "import fp4_block_scaled_quantize_amd as fq\n"
+        "class Stream:\n"
+        "    def __init__(self, index): self.cuda_stream = 70 + index\n"
+        "torch.cuda.current_stream, torch.cuda.current_device = Stream, lambda: 2\n"
+        "assert fq._stream(None, torch.device('cuda', 3)) == 73 and fq._stream(None) == 72\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
