@@ -13,7 +13,7 @@ namespace fp4 {
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline bool elem_is_8bit(int32_t e) { return e == FP4_ELEM_FP8_E4M3 || e == FP4_ELEM_INT8; }
 inline bool elem_is_6bit(int32_t e) { return e >= FP4_ELEM_FP6_E2M3 && e <= FP4_ELEM_INT6; }
-// the 8- and 6-bit grids: no two-orientation call and no weight-only GEMM
+// the 8- and 6-bit grids: their codes leave in wider pieces
 inline bool elem_is_wide(int32_t e) { return elem_is_8bit(e) || elem_is_6bit(e); }
 
 inline fp4_status check_tensor(const fp4_tensor* t, ScaleFmtHost* f)

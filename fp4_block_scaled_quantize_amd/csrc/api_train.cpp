@@ -410,7 +410,6 @@ fp4_status fp4_residual_norm_backward(const fp4_norm* args, const float* stats, 
     p.part = (float*)workspace;
     p.part_rows = args->w_post ? 2 : 1;
     p.groups = norm_groups(rows, cols);
-    // partial rows of odd widths start off the vectors' boundary
     return hip_status(launch_norm_backward(p, vec, (hipStream_t)stream));
 }
 

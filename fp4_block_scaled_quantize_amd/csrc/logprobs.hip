@@ -8,10 +8,10 @@
 //   logprob(t) = d_t - log s,  entropy = log s - w / s
 //   dz_v = c (gl ([v = t] - p_v) - ge p_v (log p_v + entropy))
 // One pass over a row keeps the running (m, s, w) of every thread in
-// binary32 (a round of loads is summed on its own first, so that a thread's
-// sum of thousands of terms takes few roundings): a larger maximum m' = m + D rescales s by f = exp(-c D) and w to
-// f (w - c D s).  The kernels work in powers of two (k = c log2 e), where w
-// carries log2 units.
+// binary32: a larger maximum m' = m + D rescales s by f = exp(-c D) and w to
+// f (w - c D s).  A round of loads is summed on its own first, so that a
+// thread's sum of thousands of terms takes few roundings.  The kernels work in
+// powers of two (k = c log2 e), where w carries log2 units.
 #include <type_traits>
 
 #include "fp4_device.hpp"
@@ -283,7 +283,8 @@ __device__ __forceinline__ void best_of_lists(const uint64_t* keys, int lists, i
     __syncthreads();
     for (int i = tid; i < lists * top; i += threads) {
         const uint64_t o = keys[i];
-        if (o != 0 && o >= low) few[atomicAdd(count, 1)] = o;      // their order does not matter
+        // an LDS counter: the places they get differ from run to run, the ranks below do not
+        if (o != 0 && o >= low) few[atomicAdd(count, 1)] = o;
     }
     __syncthreads();
     const int n = *count;
@@ -303,8 +304,6 @@ __device__ __forceinline__ void best_of_lists(const uint64_t* keys, int lists, i
     }
 }
 
-// Results of a row from its sums.  A row with no finite logit and no NaN holds no probability:
-// its entropy is 0 and every log probability -inf.
 // The row's token and its logit, fetched ahead of the sums by one thread.
 struct Given { bool is; float z; };
 
@@ -317,6 +316,8 @@ __device__ __forceinline__ Given given_token(const LogprobLaunch& p, int64_t row
     return Given{is, is ? Logit<BF16>::one((const T*)p.logits + row * p.ld + t) : 0.0f};
 }
 
+// Results of a row from its sums.  A row with no finite logit and no NaN holds
+// no probability: its entropy is 0 and every log probability -inf.
 __device__ __forceinline__ void finish_row(const LogprobLaunch& p, int64_t row, const Sums& r, const Given& g)
 {
     const float c = p.inv_temperature;
@@ -600,13 +601,14 @@ __global__ __launch_bounds__(256) void k_lp_backward(LogprobGradLaunch p)
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Whether a whole row is one wave's instead of four's: without top alternatives
-// where it is short (8192 rows of 9000, bf16: 33 us against 47; of 32000 100
-// against 94).  With them four waves keep four lists, each of which takes in
+// where it is short (8192 rows of 9000, bf16: 36 us against 49; of 32000 107
+// against 100).  With them four waves keep four lists, each of which takes in
 // its first few hundred logits, and wait to join them, so one is better
 // wherever the rows alone fill the device (top 1: 4235 rows of 142 14 us
-// against 53, 1500 of 9000 17 against 26, 5030 of 21562 59 against 93, 8192 of
-// 32000 119 against 169; but 600 of 12000, top 20, 22 against 17, 600 of 30000 29
-// against 22, 1061 of 115285 89 against 74).
+// against 52, 1500 of 9000 17 against 27, 5030 of 21562 65 against 101, 8192 of
+// 32000 121 against 177; but 600 of 12000, top 20, 22 against 17, 600 of 30000 38
+// against 27, 1061 of 115285 120 against 95).  All with logits that come from
+// memory.
 static bool row_is_a_wave(int64_t rows, int64_t vocab, bool top)
 {
     if (!top) return vocab <= 16384;

@@ -302,12 +302,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_lora_down(LoraDown p)
 // is kept small (many in flight) and base and y move in whole 128-byte lines:
 // the products, which leave the matrix instructions as 4 columns of a row a
 // lane, pass through the wave's own 4 KB of LDS and come back as 8 columns a
-// lane, 8 lanes a row.  8192 x 4096, rank 16, 134 MB: 29 us, 4.6 TB/s; the same
-// loads and stores without the products take 28.8.
+// lane, 8 lanes a row.  8192 x 4096, rank 16, 134 MB: 27 to 29 us, 4.6 to 5.0 TB/s,
+// what the same loads and stores take without the products.
 // The WM waves of a workgroup on neighbouring rows read the same part of B:
 // from the cache up to rank 32; above, a step's columns of B outweigh those of
 // y and come through LDS once for all four (SH; 1111 rows of nine requests,
-// rank 64, 11008 columns: 21 us against 25).  Rows of another adapter than the
+// rank 64, 11008 columns: 20 to 22 us against 25).  Rows of another adapter than the
 // one whose B is multiplied drop the result (a select, so that nothing of one
 // adapter reaches another's rows).
 // ---------------------------------------------------------------------------

@@ -13,10 +13,12 @@
 //   dr = alpha t,  dgate = q = sum(t u),  dw_pre = sum_rows dn h rho2
 //   dx = rho1 w_post gate t - x rho1^2 gate q / C,  dw_post = sum_rows gate t x rho1
 //
-// Memory bound: a row stays in registers between its loads and its stores,
-// one workgroup a row, so that every tensor crosses memory once.  8192 x
-// 4096, bf16 over a binary32 stream: forward 403 MB in 73 us, 5.5 TB/s, where
-// a large copy reaches 5.2.
+// Memory bound: a row stays with its workgroup between its loads and its
+// stores, so that every tensor crosses memory once (the backward pass of rows
+// above 16384 columns reads twice).  8192 x 4096, bf16 over a binary32 stream:
+// forward 403 MB in 73 us, 5.5 TB/s, where a large copy reaches 5.2.  It stays in
+// registers up to 32768 columns forward (16384 where rows are not whole aligned
+// vectors), 8192 (2048) backward; past them a part of it lies in scratch.
 #include "fp4_device.hpp"
 #include "fp4_internal.h"
 
@@ -352,7 +354,10 @@ static hipError_t norm_by_cols(const NormLaunch& p, int64_t cols, hipStream_t s)
 }
 
 // Backward: eight elements a thread as far as that goes: four operands of
-// sixteen would not leave four waves on a SIMD.
+// sixteen do not fit four waves on a SIMD, and spill.  8192 rows, bf16 over
+// binary32: 5120 columns 191 us (4.0 TB/s), 8192 256 (4.7), 12288 517 (3.5); 4096 rows
+// of 18432 2562 (0.5).  Rows that are not whole aligned vectors: 8192 x 4095
+// 289 us (2.1 TB/s), 8191 558 (2.2), 12287 1408 (1.3).
 template <bool XB, bool RB, bool VEC>
 static hipError_t norm_by_cols(const NormGradLaunch& p, int64_t cols, hipStream_t s)
 {

@@ -397,7 +397,10 @@ FP4_API fp4_status fp4_wo_gemm(const uint16_t* x, int64_t ldx, int64_t m, const 
  * with T, and every sum, in binary32.  Rows of one adapter need not be
  * adjacent; a batch that keeps each request's rows together is read fewest
  * times.  Nothing of one adapter or row reaches another row's results
- * (infinities and NaN included).  Rows without an adapter keep base.
+ * (infinities and NaN included).  Rows without an adapter keep base.  An
+ * infinity in dy, x, A or B makes what it enters infinite or NaN: T and dT meet
+ * it as a sum of three terms, which may leave NaN where their sum would leave
+ * an infinity.
  *
  * A bank: a [adapters, rank, k] and b [adapters, n, rank] in bf16, dense and
  * 16-byte aligned; scale [adapters] in binary32.  rank % 8 == 0 and at most
@@ -441,8 +444,8 @@ FP4_API fp4_status fp4_lora_apply(const uint16_t* x, int64_t ldx, int64_t m, con
  * over the rows i of adapter l (zero for an adapter without rows).  t is
  * fp4_lora_apply's T; dx_base is the gradient that arrives at x through the
  * shared projection (null for zero; it may be dx; dx may be neither x nor
- * dy).  da, db have the bank's
- * shapes in grad_dtype, are written whole and 16-byte aligned.  The sums are
+ * dy).  da, db have the bank's shapes in grad_dtype, are written whole and
+ * 16-byte aligned.  The sums are
  * taken in a fixed order: the same inputs give the same bits.
  */
 FP4_API fp4_status fp4_lora_backward(const uint16_t* dy, int64_t ld_dy, const uint16_t* x, int64_t ldx, int64_t m,
@@ -510,10 +513,11 @@ FP4_API fp4_status fp4_token_logprobs_backward(const void* logits, int32_t dtype
  *   h = alpha res + gate u  (gate [rows], binary32; null for 1)
  *   n = RMSNorm(h) w_pre,  RMSNorm(v) = v / sqrt(mean v^2 + eps)
  * x and n in x_dtype, res and h in res_dtype, the weights in weight_dtype
- * (each f32 or bf16); n comes from the unrounded h.  Fewer than 2^22 rows;
- * cols at most 32768, any
- * value and alignment of elements (rows of whole 16-byte vectors, cols % 8
- * == 0, are read as vectors).  stats [rows, 2] = {1 / sqrt(mean x^2 + eps)
+ * (each f32 or bf16); n comes from the unrounded h.  The squares are summed in
+ * binary32, so a row's norm must stay below 2^64.  Fewer than 2^22 rows;
+ * cols at most 32768, any value and alignment of elements (rows of whole
+ * 16-byte vectors, cols % 8 == 0, are read as vectors, others one element at a
+ * time).  stats [rows, 2] = {1 / sqrt(mean x^2 + eps)
  * (1 without w_post), 1 / sqrt(mean h^2 + eps)} for the backward call.  h may
  * be res and n may be x (same row strides). */
 typedef struct fp4_norm {
