@@ -7,7 +7,8 @@ missing or fails to load, every call raises.
 
 Names follow the C ABI: fp4_quantize, fp4_quantize_transposed, fp4_quantize_both, fp4_dequantize, fp4_gemm, fp4_wo_gemm,
 fp4_wo_gemm_lora, fp4_lora_apply, fp4_lora_backward, fp4_token_logprobs, fp4_token_logprobs_backward,
-fp4_residual_norm, fp4_residual_norm_backward, plus the amax state (per-tensor maximum refreshed every N calls,
+fp4_residual_norm, fp4_residual_norm_backward, fp4_gemm_epilogue, fp4_wo_gemm_epilogue, fp4_epilogue_backward,
+fp4_moe_route, fp4_moe, fp4_distill_loss, fp4_distill_loss_backward, plus the amax state (per-tensor maximum refreshed every N calls,
 ue5m3-fp4-pretraining "Что сделали").
 """
 from __future__ import annotations
@@ -31,6 +32,9 @@ TRANSFORM = {"none": 0, "rht": 1}
 ELEMENT = {"e2m1": 0, "int4": 1, "fp8_e4m3": 2, "int8": 3, "fp6_e2m3": 4, "fp6_e3m2": 5, "int6": 6}
 ELEMENT_BITS = {"e2m1": 4, "int4": 4, "fp8_e4m3": 8, "int8": 8, "fp6_e2m3": 6, "fp6_e3m2": 6, "int6": 6}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+ROUTE_SCORE = {"softmax": 0, "sigmoid": 1}
+DISTILL_REST = {"bucket": 0, "renormalize": 1}
 
 FP4_OK = 0
 
@@ -59,6 +63,17 @@ class Fp4NormC(ctypes.Structure):
                 ("weight_dtype", ctypes.c_int32)]
 
 
+class Fp4EpilogueC(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("bias_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("mul", ctypes.c_void_p), ("ld_mul", ctypes.c_int64), ("residual", ctypes.c_void_p),
+                ("ld_residual", ctypes.c_int64), ("pre", ctypes.c_void_p), ("ld_pre", ctypes.c_int64)]
+
+
+class Fp4MoeBankC(ctypes.Structure):
+    _fields_ = [("gate_up", ctypes.POINTER(Fp4TensorC)), ("down", ctypes.POINTER(Fp4TensorC)),
+                ("up_scale", ctypes.c_void_p), ("down_scale", ctypes.c_void_p), ("experts", ctypes.c_int64)]
+
+
 # Fp4NormC's layout; packing it costs a third of filling a ctypes.Structure.
 _NORM_ARGS = struct.Struct("@PqPqqqPPPffiii4x")
 assert _NORM_ARGS.size == ctypes.sizeof(Fp4NormC)
@@ -84,6 +99,7 @@ def lib():
     vp, i32, i64, u64, u32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_uint32
     f32 = ctypes.c_float
     T, LB = ctypes.POINTER(Fp4TensorC), ctypes.POINTER(Fp4LoraBankC)
+    EP, MB = ctypes.POINTER(Fp4EpilogueC), ctypes.POINTER(Fp4MoeBankC)
     sig = {
         "fp4_version": (i32, []),
         "fp4_status_string": (ctypes.c_char_p, [i32]),
@@ -111,6 +127,16 @@ def lib():
         "fp4_residual_norm": (i32, [vp, vp, i64, vp, i64, vp, vp]),
         "fp4_residual_norm_workspace": (i64, [i64, i64, i32]),
         "fp4_residual_norm_backward": (i32, [vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp]),
+        "fp4_gemm_epilogue": (i32, [T, T, EP, vp, i64, vp]),
+        "fp4_wo_gemm_epilogue": (i32, [vp, i64, i64, T, EP, vp, i64, vp]),
+        "fp4_epilogue_workspace": (i64, [i64, i64]),
+        "fp4_epilogue_backward": (i32, [vp, i64, vp, i64, vp, i64, i64, i64, i32, vp, i64, vp, i64, vp, vp, i64, vp]),
+        "fp4_moe_route": (i32, [vp, i32, i64, i64, i64, i32, i32, vp, i32, f32, vp, vp, vp]),
+        "fp4_moe_workspace": (i64, [i64, i32, i64]),
+        "fp4_moe": (i32, [vp, i64, i64, MB, vp, vp, i32, i32, vp, i64, vp, i64, vp, i64, vp]),
+        "fp4_distill_workspace": (i64, [i64, i64]),
+        "fp4_distill_loss": (i32, [vp, i32, i64, i64, i64, vp, vp, i32, f32, i32, vp, vp, vp, i64, vp]),
+        "fp4_distill_loss_backward": (i32, [vp, i32, i64, i64, i64, vp, vp, i32, f32, i32, vp, vp, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -772,8 +798,283 @@ def fp4_residual_norm_backward(dn: torch.Tensor | None, dh: torch.Tensor | None,
     return ResidualNormGrads(dx, dres, dw_pre, dw_post, dgate)
 
 
+# ---------------------------------------------------------------------------
+# Products with an epilogue, the mixture-of-experts layer and distillation.
+# Outputs and workspaces belong to the call's stream, as above.
+# ---------------------------------------------------------------------------
+def _one_of(what: str, name: str, value, table: dict) -> int:
+    if value not in table:
+        raise ValueError(f"{what}: {name} must be one of {sorted(table)}")
+    return table[value]
+
+
+def _bf16_rows(what: str, name: str, t: torch.Tensor, rows: int, cols: int):
+    if t.dtype != torch.bfloat16 or not _is_rows(t, cols, rows):
+        raise ValueError(f"{what}: {name} must be bf16 [{rows}, {cols}] with unit column stride")
+
+
+def _epilogue(what: str, m: int, n: int, bias, act, mul, residual, pre=None) -> Fp4EpilogueC:
+    a = _one_of(what, "act", act, ACT)
+    if bias is not None and (bias.dtype not in DTYPE or not _is_vector(bias, n, bias.dtype)):
+        raise ValueError(f"{what}: bias must be a dense float32 or bfloat16 [{n}]")
+    for t, name in ((mul, "mul"), (residual, "residual")):
+        if t is not None:
+            _bf16_rows(what, name, t, m, n)
+    return Fp4EpilogueC(_ptr(bias), 0 if bias is None else DTYPE[bias.dtype], a, _ptr(mul), 0 if mul is None else _ld(mul),
+                        _ptr(residual), 0 if residual is None else _ld(residual), _ptr(pre),
+                        0 if pre is None else _ld(pre))
+
+
+def fp4_gemm_epilogue(a: QTensor, b: QTensor, bias: torch.Tensor | None = None, act: str = "none",
+                      mul: torch.Tensor | None = None, residual: torch.Tensor | None = None, save_pre: bool = False,
+                      out: torch.Tensor | None = None, stream=None) -> tuple:
+    """(y, pre): y = residual + mul act(v) with v = A W^T + bias, and with
+    save_pre v itself in bf16 (else None), which fp4_epilogue_backward takes.
+    bias [N] float32 or bfloat16; mul and residual bf16 [M, N]; act: "none",
+    "relu", "silu", "gelu" or "gelu_tanh".  out may be mul or residual."""
+    what = "fp4_gemm_epilogue"
+    m, n = a.rows, b.rows
+    args = _epilogue(what, m, n, bias, act, mul, residual)
+    dev = _on_device(what, a.q, a.scales, a.tensor_scale, b.q, b.scales, b.tensor_scale,
+                     *(t for t in (bias, mul, residual, out) if t is not None))
+    ta, tb = a.c(), b.c()
+    with _allocating(stream, dev):
+        if out is None:
+            out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_dense_out(out, (m, n), (torch.bfloat16,), what)
+        pre = torch.empty((m, n), dtype=torch.bfloat16, device=dev) if save_pre else None
+        if pre is not None:
+            args.pre, args.ld_pre = _ptr(pre), _ld(pre)
+        st = lib().fp4_gemm_epilogue(ctypes.byref(ta), ctypes.byref(tb), ctypes.byref(args), out.data_ptr(), _ld(out),
+                                     _stream(stream, dev))
+    _check(st, what)
+    return out, pre
+
+
+def fp4_wo_gemm_epilogue(x: torch.Tensor, w: QTensor, bias: torch.Tensor | None = None, act: str = "none",
+                         mul: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """fp4_wo_gemm followed by the epilogue of fp4_gemm_epilogue: residual +
+    mul act(X W^T + bias) for at most 16 rows."""
+    what = "fp4_wo_gemm_epilogue"
+    if x.dtype != torch.bfloat16 or not _is_rows(x, w.cols):
+        raise ValueError(f"{what}: x must be bf16 [rows, {w.cols}] with unit column stride")
+    m, n = x.shape[0], w.rows
+    args = _epilogue(what, m, n, bias, act, mul, residual)
+    dev = _on_device(what, x, w.q, w.scales, w.tensor_scale, *(t for t in (bias, mul, residual, out) if t is not None))
+    tw = w.c()
+    with _allocating(stream, dev):
+        if out is None:
+            out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_dense_out(out, (m, n), (torch.bfloat16,), what)
+        st = lib().fp4_wo_gemm_epilogue(x.data_ptr(), _ld(x), m, ctypes.byref(tw), ctypes.byref(args), out.data_ptr(),
+                                        _ld(out), _stream(stream, dev))
+    _check(st, what)
+    return out
+
+
+@dataclass
+class EpilogueGrads:
+    """dpre and dmul in bf16 (dmul None without mul), dbias [N] in fp32 (None
+    where it was not asked for); the residual's gradient is dy."""
+    dpre: torch.Tensor
+    dbias: torch.Tensor | None
+    dmul: torch.Tensor | None
+
+
+def fp4_epilogue_backward(dy: torch.Tensor, pre: torch.Tensor | None, act: str = "none", mul: torch.Tensor | None = None,
+                          bias: bool = False, stream=None) -> EpilogueGrads:
+    """Gradients of fp4_gemm_epilogue for the gradient dy of its y: of pre
+    (which the products' backward GEMMs take), of the bias (bias=True) and of
+    mul.  With act "none" and no mul, dpre is dy and pre is not needed."""
+    what = "fp4_epilogue_backward"
+    a = _one_of(what, "act", act, ACT)
+    if dy.dtype != torch.bfloat16 or not _is_rows(dy):
+        raise ValueError(f"{what}: dy must be bf16 [rows, cols] with unit column stride")
+    m, n = dy.shape
+    reads = a != 0 or mul is not None
+    if reads and pre is None:
+        raise ValueError(f"{what}: pre is needed with an activation or mul")
+    for t, name in ((pre if reads else None, "pre"), (mul, "mul")):
+        if t is not None:
+            _bf16_rows(what, name, t, m, n)
+    dev = _on_device(what, dy, *(t for t in (pre if reads else None, mul) if t is not None))
+    if n == 0:
+        return EpilogueGrads(_empty_as(dy), torch.empty(0, dtype=torch.float32, device=dev) if bias else None,
+                             None if mul is None else _empty_as(mul))
+    L = lib()
+    with _allocating(stream, dev):
+        dpre = _empty_as(dy) if reads else None
+        dmul = _empty_as(mul) if mul is not None else None
+        dbias = torch.empty(n, dtype=torch.float32, device=dev) if bias else None
+        ws = _space(L.fp4_epilogue_workspace(m, n), dev, what) if bias else None
+        st = L.fp4_epilogue_backward(dy.data_ptr(), _ld(dy), _ptr(pre) if reads else None, _ld(pre) if reads else 0, _ptr(mul),
+                                     0 if mul is None else _ld(mul), m, n, a, _ptr(dpre), n, _ptr(dmul), n, _ptr(dbias),
+                                     _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream, dev))
+    _check(st, what)
+    return EpilogueGrads(dy if dpre is None else dpre, dbias, dmul)
+
+
+def fp4_moe_route(logits: torch.Tensor, top: int, score: str = "softmax", bias: torch.Tensor | None = None,
+                  renormalize: bool = True, scale: float = 1.0, stream=None) -> tuple:
+    """(ids, weights): the `top` experts of each row of logits [rows, experts]
+    (int32, largest first, ties to the lower index) and their weights (fp32).
+    score: "softmax" or "sigmoid"; bias (fp32 [experts]) takes part in the
+    choice alone; renormalize divides by the chosen scores' sum, scale
+    multiplies.  An expert at -inf is never chosen (id -1, weight 0 where
+    nothing is left)."""
+    what = "fp4_moe_route"
+    sc = _one_of(what, "score", score, ROUTE_SCORE)
+    if logits.dtype not in DTYPE or not _is_rows(logits) or logits.shape[1] < 1:
+        raise ValueError(f"{what}: logits must be a float32 or bfloat16 [rows, experts] tensor with unit column stride")
+    n, e = logits.shape
+    if bias is not None and not _is_vector(bias, e, torch.float32):
+        raise ValueError(f"{what}: bias must be float32 [{e}]")
+    dev = _on_device(what, logits, *(() if bias is None else (bias,)))
+    with _allocating(stream, dev):
+        ids = torch.empty((n, max(top, 0)), dtype=torch.int32, device=dev)
+        weights = torch.empty((n, max(top, 0)), dtype=torch.float32, device=dev)
+        st = lib().fp4_moe_route(logits.data_ptr(), DTYPE[logits.dtype], _ld(logits), n, e, top, sc, _ptr(bias),
+                                 int(renormalize), scale, ids.data_ptr(), weights.data_ptr(), _stream(stream, dev))
+    _check(st, what)
+    return ids, weights
+
+
+@dataclass
+class MoeBank:
+    """The experts of a layer: gate_up [experts * 2 F, H] (each expert's F gate
+    rows, then its F up rows) and down [experts * H, F], quantized on any
+    grid; up_scale, down_scale (fp32 [experts], None: 1) multiply an expert's
+    products, for experts quantized each with a tensor scale of its own."""
+    gate_up: QTensor
+    down: QTensor
+    experts: int
+    up_scale: torch.Tensor | None = None
+    down_scale: torch.Tensor | None = None
+
+    def tensors(self) -> list:
+        t = [self.gate_up.q, self.gate_up.scales, self.gate_up.tensor_scale, self.down.q, self.down.scales,
+             self.down.tensor_scale]
+        return t + [s for s in (self.up_scale, self.down_scale) if s is not None]
+
+    def c(self) -> Fp4MoeBankC:
+        e, h, f = self.experts, self.gate_up.cols, self.down.cols
+        if e < 1 or self.gate_up.rows != e * 2 * f or self.down.rows != e * h:
+            raise ValueError("MoeBank: gate_up is [experts * 2 F, H], down is [experts * H, F]")
+        for s in (self.up_scale, self.down_scale):
+            if s is not None and not _is_vector(s, e, torch.float32):
+                raise ValueError(f"MoeBank: scales must be float32 [{e}]")
+        return Fp4MoeBankC(ctypes.pointer(self.gate_up.c()), ctypes.pointer(self.down.c()), _ptr(self.up_scale),
+                           _ptr(self.down_scale), e)
+
+
+def fp4_moe(x: torch.Tensor, bank: MoeBank, ids: torch.Tensor, weights: torch.Tensor, act: str = "silu",
+            residual: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = residual + sum_k weights[:, k] D_e (act(G_e x) (U_e x)) with e =
+    ids[:, k] for at most 16 tokens x (bf16 [tokens, H]); ids (int32) and
+    weights (fp32) [tokens, top] as fp4_moe_route gives them (an id outside the
+    bank: none).  out may be residual or x."""
+    what = "fp4_moe"
+    a = _one_of(what, "act", act, ACT)
+    tb = bank.c()
+    h, f = bank.gate_up.cols, bank.down.cols
+    if x.dtype != torch.bfloat16 or not _is_rows(x, h):
+        raise ValueError(f"{what}: x must be bf16 [tokens, {h}] with unit column stride")
+    m = x.shape[0]
+    if ids.dim() != 2 or ids.dtype != torch.int32 or ids.shape[0] != m or not ids.is_contiguous() \
+            or weights.dtype != torch.float32 or weights.shape != ids.shape or not weights.is_contiguous():
+        raise ValueError(f"{what}: ids must be int32 and weights float32, both dense [{m}, top]")
+    if residual is not None:
+        _bf16_rows(what, "residual", residual, m, h)
+    dev = _on_device(what, x, ids, weights, *bank.tensors(), *(t for t in (residual, out) if t is not None))
+    top, L = ids.shape[1], lib()
+    with _allocating(stream, dev):
+        if out is None:
+            out = torch.empty((m, h), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_dense_out(out, (m, h), (torch.bfloat16,), what)
+        ws = _space(L.fp4_moe_workspace(m, top, f), dev, what)
+        st = L.fp4_moe(x.data_ptr(), _ld(x), m, ctypes.byref(tb), ids.data_ptr(), weights.data_ptr(), top, a,
+                       _ptr(residual), 0 if residual is None else _ld(residual), out.data_ptr(), _ld(out), _ptr(ws),
+                       0 if ws is None else ws.numel(), _stream(stream, dev))
+    _check(st, what)
+    return out
+
+
+@dataclass
+class DistillLoss:
+    """loss [rows] in fp32; stats [rows, 7] for the backward call."""
+    loss: torch.Tensor
+    stats: torch.Tensor
+
+
+def _distill(what: str, logits, top_ids, top_logprobs, rest) -> int:
+    r = _one_of(what, "rest", rest, DISTILL_REST)
+    if logits.dtype not in DTYPE or not _is_rows(logits) or logits.shape[1] < 1:
+        raise ValueError(f"{what}: logits must be a float32 or bfloat16 [rows, vocab] tensor with unit column stride")
+    n = logits.shape[0]
+    if top_ids.dim() != 2 or top_ids.dtype != torch.int32 or top_ids.shape[0] != n or not top_ids.is_contiguous() \
+            or top_logprobs.dtype != torch.float32 or top_logprobs.shape != top_ids.shape or not top_logprobs.is_contiguous():
+        raise ValueError(f"{what}: top_ids must be int32 and top_logprobs float32, both dense [{n}, top]")
+    return r
+
+
+def fp4_distill_loss(logits: torch.Tensor, top_ids: torch.Tensor, top_logprobs: torch.Tensor, temperature: float = 1.0,
+                     rest: str = "bucket", stream=None) -> DistillLoss:
+    """Each row's divergence of softmax(logits / temperature) from a teacher's
+    top log probabilities (its fp4_token_logprobs' top_ids and top_logprobs at
+    that temperature; an id outside the vocabulary is no entry).  rest:
+    "bucket" compares what neither lists as one more token, "renormalize"
+    divides the listed probabilities by their sum."""
+    what = "fp4_distill_loss"
+    r = _distill(what, logits, top_ids, top_logprobs, rest)
+    dev = _on_device(what, logits, top_ids, top_logprobs)
+    n, v = logits.shape
+    L = lib()
+    with _allocating(stream, dev):
+        ws = _space(L.fp4_distill_workspace(n, v), dev, what)
+        loss = torch.empty(n, dtype=torch.float32, device=dev)
+        stats = torch.empty((n, 7), dtype=torch.float32, device=dev)
+        st = L.fp4_distill_loss(logits.data_ptr(), DTYPE[logits.dtype], _ld(logits), n, v, top_ids.data_ptr(),
+                                top_logprobs.data_ptr(), top_ids.shape[1], temperature, r, loss.data_ptr(),
+                                stats.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream, dev))
+    _check(st, what)
+    return DistillLoss(loss, stats)
+
+
+def fp4_distill_loss_backward(logits: torch.Tensor, top_ids: torch.Tensor, top_logprobs: torch.Tensor, saved: DistillLoss,
+                              grad_loss: torch.Tensor, temperature: float = 1.0, rest: str = "bucket",
+                              out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of the logits for grad_loss (fp32 [rows]); the other
+    arguments are the forward call's, saved its result; out may be the
+    logits."""
+    what = "fp4_distill_loss_backward"
+    r = _distill(what, logits, top_ids, top_logprobs, rest)
+    n, v = logits.shape
+    if not _is_vector(grad_loss, n, torch.float32):
+        raise ValueError(f"{what}: grad_loss must be float32 [{n}]")
+    if tuple(saved.stats.shape) != (n, 7) or saved.stats.dtype != torch.float32 or not saved.stats.is_contiguous():
+        raise ValueError(f"{what}: saved is not the result of a forward call on these logits")
+    dev = _on_device(what, logits, top_ids, top_logprobs, saved.stats, grad_loss, *(() if out is None else (out,)))
+    with _allocating(stream, dev):
+        if out is None:
+            out = _empty_as(logits)
+        elif out.dtype != logits.dtype or not _is_rows(out, v, n):
+            raise ValueError(f"{what}: out must be [{n}, {v}] of the logits' dtype with unit column stride")
+        st = lib().fp4_distill_loss_backward(logits.data_ptr(), DTYPE[logits.dtype], _ld(logits), n, v, top_ids.data_ptr(),
+                                             top_logprobs.data_ptr(), top_ids.shape[1], temperature, r,
+                                             saved.stats.data_ptr(), grad_loss.data_ptr(), out.data_ptr(), _ld(out),
+                                             _stream(stream, dev))
+    _check(st, what)
+    return out
+
+
 __all__ = ["fp4_quantize", "fp4_quantize_transposed", "fp4_quantize_both", "fp4_dequantize", "fp4_gemm",
            "fp4_wo_gemm", "AmaxState", "QTensor", "Fp4Error", "SCALE_FORMATS", "lib", "status_string", "LIB_PATH",
            "set_exchange_wait", "set_gemm_small_outputs", "fp4_quantize_noalloc", "LoraBank", "fp4_wo_gemm_lora",
            "fp4_lora_apply", "fp4_lora_backward", "TokenLogprobs", "fp4_token_logprobs",
-           "fp4_token_logprobs_backward", "fp4_residual_norm", "ResidualNormGrads", "fp4_residual_norm_backward"]
+           "fp4_token_logprobs_backward", "fp4_residual_norm", "ResidualNormGrads", "fp4_residual_norm_backward",
+           "fp4_gemm_epilogue", "fp4_wo_gemm_epilogue", "EpilogueGrads", "fp4_epilogue_backward", "fp4_moe_route", "MoeBank",
+           "fp4_moe", "DistillLoss", "fp4_distill_loss", "fp4_distill_loss_backward"]

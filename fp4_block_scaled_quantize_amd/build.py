@@ -29,7 +29,8 @@ PER_FILE = {
     "quant.hip": ["-ffp-contract=off", "-mllvm", "-amdgpu-atomic-optimizer-strategy=None"],
     "api.cpp": ["-ffp-contract=off"],
 }
-SOURCES = ["quant.hip", "gemm.hip", "lora.hip", "logprobs.hip", "norm.hip", "api.cpp", "api_train.cpp"]
+SOURCES = ["quant.hip", "gemm.hip", "gemm_epilogue.hip", "moe.hip", "lora.hip", "logprobs.hip", "norm.hip", "epilogue.hip",
+           "distill.hip", "api.cpp", "api_train.cpp", "api_layer.cpp"]
 
 
 def hipcc() -> str:

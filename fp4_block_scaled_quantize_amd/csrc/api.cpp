@@ -62,7 +62,7 @@ struct fp4_amax_state {
 
 extern "C" {
 
-int32_t fp4_version(void) { return 108; }
+int32_t fp4_version(void) { return 109; }
 
 const char* fp4_status_string(fp4_status st)
 {
@@ -403,41 +403,17 @@ fp4_status fp4_dequantize(const fp4_tensor* in, void* y, int32_t y_dtype, int64_
 
 fp4_status fp4_gemm(const fp4_tensor* a, const fp4_tensor* b, uint16_t* c, int64_t ldc, void* stream)
 {
-    ScaleFmtHost fa, fb;
-    fp4_status st = check_tensor(a, &fa);
+    GemmLaunch p;
+    const fp4_status st = check_gemm(a, b, c, ldc, &p);
     if (st != FP4_OK) return st;
-    st = check_tensor(b, &fb);
-    if (st != FP4_OK) return st;
-    if (!c) return FP4_ERR_INVALID_ARG;
-    if (a->cols != b->cols) return FP4_ERR_SHAPE;
-    if (a->fmt.block != b->fmt.block) return FP4_ERR_UNSUPPORTED;
-    // transformed operands multiply to the same product only when both carry
-    // the same transform along K
-    if (a->fmt.element != b->fmt.element) return FP4_ERR_UNSUPPORTED;
-    if (a->fmt.transform != b->fmt.transform) return FP4_ERR_UNSUPPORTED;
-    if (a->fmt.transform != FP4_TRANSFORM_NONE && a->fmt.transform_signs != b->fmt.transform_signs)
-        return FP4_ERR_UNSUPPORTED;
-    if (a->cols % 128) return FP4_ERR_SHAPE;
-    if (ldc < b->rows) return FP4_ERR_SHAPE;
-    if (((uintptr_t)c & 1u) != 0) return FP4_ERR_ALIGN;
     if (a->rows == 0 || b->rows == 0) return FP4_OK;
     // an empty K: C is the empty sum, zero; no operand is read
     if (a->cols == 0) return hip_status(launch_fill_zero_bf16(c, ldc, a->rows, b->rows, (hipStream_t)stream));
-    if (!aligned16(a->q) || !aligned16(b->q) || ((uintptr_t)a->scales & 3u) || ((uintptr_t)b->scales & 3u))
-        return FP4_ERR_ALIGN;
-    GemmLaunch p;
-    p.qa = a->q; p.sa = a->scales; p.ga = a->tensor_scale;
-    p.qb = b->q; p.sb = b->scales; p.gb = b->tensor_scale;
-    p.m = a->rows; p.n = b->rows; p.k = a->cols;
-    p.block = a->fmt.block;
-    p.fa = fa; p.fb = fb;
-    p.c = c; p.ldc = ldc;
-    p.elem = a->fmt.element;
     hipStream_t s = (hipStream_t)stream;
     if (gemm_small_supported(p)) return hip_status(launch_gemm_small(p, s));
-    if (p.elem == FP4_ELEM_E2M1 && fa.is_e8m0 && fb.is_e8m0 && p.block == 32) return hip_status(launch_gemm_mx(p, s));
+    if (gemm_is_mx(p)) return hip_status(launch_gemm_mx(p, s));
     if (gemm_mx16_supported(p)) return hip_status(launch_gemm_mx16(p, s));
-    if (!gemm_dq_supported(fa, fb, p.elem)) return FP4_ERR_UNSUPPORTED;
+    if (!gemm_dq_supported(p.fa, p.fb, p.elem)) return FP4_ERR_UNSUPPORTED;
     return hip_status(launch_gemm_dq(p, s));
 }
 

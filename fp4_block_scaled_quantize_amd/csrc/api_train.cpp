@@ -17,13 +17,9 @@ namespace {
 constexpr int64_t kMaxRows = int64_t(1) << 20;        // rows of an adapter call (grid dimensions)
 constexpr int64_t kMaxAdapters = 16384;
 constexpr int64_t kMaxDim = int64_t(1) << 24;         // k and n of a bank
-constexpr int64_t kMaxElems = int64_t(1) << 40;       // elements of one tensor: byte offsets stay far from 63 bits
 constexpr int32_t kMaxRank = 128, kMaxTop = 32;
 constexpr int64_t kMaxNormCols = 32768;
-constexpr int64_t kMaxLineRows = int64_t(1) << 22;    // rows with a workgroup each: below 2^32 threads at 1024
 
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-int64_t up16(int64_t b) { return (b + 15) / 16 * 16; }
 
 // The bank itself; n % 8 only where rows of n elements are read as vectors.
 fp4_status check_bank(const fp4_lora_bank* b, bool vector_n)
@@ -85,13 +81,6 @@ LoraSpace lora_space(int32_t call, int64_t m, int64_t n, int64_t k, int64_t rank
     return w;
 }
 
-fp4_status check_space(const void* ws, int64_t have, int64_t need)
-{
-    if (need == 0) return FP4_OK;
-    if (!ws || have < need) return FP4_ERR_INVALID_ARG;
-    return aligned(ws, 16) ? FP4_OK : FP4_ERR_ALIGN;
-}
-
 template <typename T>
 T* at(void* ws, int64_t off) { return off < 0 ? nullptr : reinterpret_cast<T*>((uint8_t*)ws + off); }
 
@@ -110,9 +99,6 @@ fp4_status check_slots(const int32_t* slots, int64_t m)
     if (!slots && m) return FP4_ERR_INVALID_ARG;
     return aligned(slots, 4) ? FP4_OK : FP4_ERR_ALIGN;
 }
-
-bool dtype_ok(int32_t d) { return d == FP4_DTYPE_F32 || d == FP4_DTYPE_BF16; }
-int64_t esize(int32_t d) { return d == FP4_DTYPE_BF16 ? 2 : 4; }
 
 }  // namespace
 
@@ -241,19 +227,6 @@ fp4_status fp4_wo_gemm_lora(const uint16_t* x, int64_t ldx, int64_t m, const fp4
 }
 
 // ---------------------------------------------------------------------------
-static fp4_status check_logits(const void* z, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab, float temperature)
-{
-    if (!dtype_ok(dtype)) return FP4_ERR_INVALID_ARG;
-    // the kernels work with log2(e) / temperature
-    if (!(temperature > 0.0f) || !isfinite(temperature) || !isfinite(2.0f / temperature)) return FP4_ERR_INVALID_ARG;
-    if (rows < 0 || vocab < 1 || ld < vocab) return FP4_ERR_SHAPE;
-    if (rows >= kMaxLineRows || vocab >= (int64_t(1) << 27) || ld > kMaxElems / (rows ? rows : 1))
-        return FP4_ERR_UNSUPPORTED;
-    if (!z && rows) return FP4_ERR_INVALID_ARG;
-    if (!aligned(z, (uintptr_t)esize(dtype))) return FP4_ERR_ALIGN;
-    return FP4_OK;
-}
-
 int64_t fp4_token_logprobs_workspace(int64_t rows, int64_t vocab, int32_t top)
 {
     if (rows < 0 || vocab < 1) return FP4_ERR_SHAPE;

@@ -1,0 +1,152 @@
+// epilogue_device.hpp -- what follows a product's sums in registers: bias,
+// activation, multiplier and residual (gemm.hip's epilogue forms, epilogue.hip,
+// moe.hip).
+//
+//   v = sum + bias,  y = res + mul act(v)
+//
+// in binary32, each output rounded once.  The activations, with s(x) = 1 /
+// (1 + e^-x) and Phi the normal distribution:
+//   relu max(v, 0); silu v s(v); gelu v Phi(v) = v erfc(-v / sqrt 2) / 2;
+//   gelu_tanh v (1 + tanh u) / 2 = v s(2 u), u = sqrt(2 / pi) (v + 0.044715 v^3)
+// The last two are taken in the forms that keep their small values' bits at
+// far negative v, where 1 + erf and 1 + tanh cancel.
+#pragma once
+
+#include <type_traits>
+
+#include "fp4_device.hpp"
+#include "fp4_internal.h"
+
+namespace fp4 {
+
+constexpr float kEpiLog2e = 1.44269504088896340736f;
+constexpr float kTanhOuter = 1.59576912160573071176f;      // 2 sqrt(2 / pi)
+constexpr float kTanhCubic = 0.044715f;
+
+// {s(x), s(-x)}, neither by a subtraction
+struct Logistic { float up, down; };
+__device__ __forceinline__ Logistic logistic(float x)
+{
+    const float t = __builtin_amdgcn_exp2f(-fabsf(x) * kEpiLog2e), r = __builtin_amdgcn_rcpf(1.0f + t), l = t * r;
+    return x >= 0.0f || x != x ? Logistic{r, l} : Logistic{l, r};
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float v)
+{
+    if (ACT == kActRelu) return v < 0.0f ? 0.0f : v;         // NaN stays NaN
+    if (ACT == kActSilu) return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kEpiLog2e));
+    if (ACT == kActGelu) return 0.5f * v * erfcf(v * -0.70710678118654752440f);
+    if (ACT == kActGeluTanh) {
+        const float u = kTanhOuter * __builtin_fmaf(kTanhCubic * v * v, v, v);
+        return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-u * kEpiLog2e));
+    }
+    return v;
+}
+
+// The derivative.  gelu_tanh's is 0 or 1 in every bit of binary32 past |v| =
+// 30, where its polynomials would overflow against a zero.
+template <int ACT>
+__device__ __forceinline__ float act_slope(float v)
+{
+    if (ACT == kActRelu) return v <= 0.0f ? 0.0f : 1.0f;
+    if (ACT == kActSilu) {
+        const Logistic s = logistic(v);
+        return __builtin_fmaf(v * s.up, s.down, s.up);
+    }
+    if (ACT == kActGelu)
+        return __builtin_fmaf(v * 0.39894228040143267794f, __builtin_amdgcn_exp2f(-0.5f * kEpiLog2e * v * v),
+                              0.5f * erfcf(v * -0.70710678118654752440f));
+    if (ACT == kActGeluTanh) {
+        const float x = v > 30.0f ? 30.0f : v < -30.0f ? -30.0f : v;
+        const float q = kTanhCubic * x * x;
+        const Logistic s = logistic(kTanhOuter * __builtin_fmaf(q, x, x));
+        return __builtin_fmaf(x * s.up * s.down, kTanhOuter * __builtin_fmaf(3.0f, q, 1.0f), s.up);
+    }
+    return 1.0f;
+}
+
+// f(std::integral_constant<int, ACT>) for a run-time activation: the choice is
+// the same for every lane.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f)
+{
+    switch (act) {
+    case kActRelu: f(std::integral_constant<int, kActRelu>{}); break;
+    case kActSilu: f(std::integral_constant<int, kActSilu>{}); break;
+    case kActGelu: f(std::integral_constant<int, kActGelu>{}); break;
+    case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>{}); break;
+    default: f(std::integral_constant<int, kActNone>{}); break;
+    }
+}
+
+// W (1, 4 or 8) neighbouring bf16 elements, `full` as one load or store, else
+// the first `n`.
+template <int W>
+__device__ __forceinline__ void bf16_load(const uint16_t* p, bool full, int n, float (&o)[W])
+{
+    if (W > 1 && full) {
+        uint32_t d[W / 2 ? W / 2 : 1];
+        if constexpr (W == 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            d[0] = v.x; d[1] = v.y;
+        }
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) { o[2 * i] = bf16_lo(d[i]); o[2 * i + 1] = bf16_hi(d[i]); }
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i) o[i] = i < n ? bf16_lo(p[i]) : 0.0f;
+    }
+}
+template <int W>
+__device__ __forceinline__ void bf16_store(uint16_t* p, bool full, int n, const float (&v)[W])
+{
+    if (W > 1 && full) {
+        if constexpr (W == 8)
+            *reinterpret_cast<uint4*>(p) = uint4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                 pack_bf16(v[6], v[7])};
+        else
+            *reinterpret_cast<uint2*>(p) = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            if (i < n) p[i] = (uint16_t)f32_to_bf16_rne(v[i]);
+    }
+}
+
+__device__ __forceinline__ float epi_bias(const Epilogue& e, int64_t n)
+{
+    return e.bias_bf16 ? bf16_lo(((const uint16_t*)e.bias)[n]) : ((const float*)e.bias)[n];
+}
+
+// W outputs of row m from column n on, of N: `sum` the product, `bias` theirs
+// (zeros without one).
+template <int W>
+__device__ __forceinline__ void epi_put(const Epilogue& e, uint16_t* c, int64_t ldc, int64_t m, int64_t n, int64_t N,
+                                        const float (&sum)[W], const float (&bias)[W])
+{
+    const bool full = e.vec && n + W <= N;
+    const int have = N - n < W ? (int)(N - n) : W;
+    float v[W], mul[W], res[W];
+    if (e.mul) bf16_load<W>(e.mul + m * e.ld_mul + n, full, have, mul);
+    if (e.res) bf16_load<W>(e.res + m * e.ld_res + n, full, have, res);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = sum[i] + bias[i];
+    if (e.pre) bf16_store<W>(e.pre + m * e.ld_pre + n, full, have, v);
+    with_act(e.act, [&](auto act) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = act_value<decltype(act)::value>(v[i]);
+    });
+    if (e.mul)
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] *= mul[i];
+    if (e.res)
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] += res[i];
+    bf16_store<W>(c + m * ldc + n, full, have, v);
+}
+
+}  // namespace fp4

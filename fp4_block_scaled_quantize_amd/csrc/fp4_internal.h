@@ -141,6 +141,45 @@ struct WoGemmLaunch {
 };
 
 hipError_t launch_wo_gemm(const WoGemmLaunch& p, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// products with an epilogue (gemm_epilogue.hip, epilogue.hip)
+// ---------------------------------------------------------------------------
+// v = product + bias, y = res + mul act(v); null: no such part
+enum { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
+struct Epilogue {
+    const void* bias; int32_t bias_bf16;                  // [n]
+    int32_t act;
+    const uint16_t* mul; int64_t ld_mul;
+    const uint16_t* res; int64_t ld_res;
+    uint16_t* pre; int64_t ld_pre;                        // out: v
+    int32_t vec;               // rows of y, mul, res and pre are 16-byte aligned
+};
+struct GemmEpiLaunch : GemmLaunch { Epilogue ep; };
+struct WoEpiLaunch : WoGemmLaunch { Epilogue ep; };
+namespace epi {
+hipError_t launch_gemm_mx(const GemmEpiLaunch& p, hipStream_t s);
+hipError_t launch_gemm_mx16(const GemmEpiLaunch& p, hipStream_t s);
+hipError_t launch_gemm_dq(const GemmEpiLaunch& p, hipStream_t s);
+hipError_t launch_gemm_small(const GemmEpiLaunch& p, hipStream_t s);
+hipError_t launch_wo_gemm(const WoEpiLaunch& p, hipStream_t s);
+}  // namespace epi
+
+struct EpiGradLaunch {
+    const uint16_t* dy; int64_t lddy;
+    const uint16_t* pre; int64_t ldpre;
+    const uint16_t* mul; int64_t ldmul;
+    int64_t rows, cols;
+    int32_t act, vec;
+    uint16_t* dpre; int64_t lddpre;                       // null: not written
+    uint16_t* dmul; int64_t lddmul;
+    float* dbias;              // [cols], null: none
+    float* part;               // [groups, cols]
+    int64_t groups;
+};
+int64_t epilogue_groups(int64_t rows, int64_t cols);
+hipError_t launch_epilogue_backward(const EpiGradLaunch& p, hipStream_t s);
+
 // C[rows, cols] (bf16, row stride ld) = 0: the product over an empty K.
 hipError_t launch_fill_zero_bf16(uint16_t* c, int64_t ld, int64_t rows, int64_t cols, hipStream_t s);
 
@@ -253,5 +292,65 @@ struct NormGradLaunch {
 int64_t norm_groups(int64_t rows, int64_t cols);
 hipError_t launch_norm(const NormLaunch& p, bool vec, hipStream_t s);
 hipError_t launch_norm_backward(const NormGradLaunch& p, bool vec, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// mixture of experts (moe.hip)
+// ---------------------------------------------------------------------------
+constexpr int kMoeMaxTokens = 16, kMoeMaxTop = 16, kMoeMaxRouted = 1024;
+struct MoeWeights {
+    const uint8_t* q; const uint8_t* s; const float* g;
+    const float* scale;        // [experts], null: 1
+    int64_t expert_q, expert_s;                           // bytes from an expert to the next
+    ScaleFmtHost fmt;
+    int32_t block, elem;
+};
+struct MoeLaunch {
+    const uint16_t* x; int64_t ldx; int32_t m, top, experts;
+    const int32_t* ids; const float* weights;             // [m, top]
+    MoeWeights up, down;       // up: rows 0 .. ffn - 1 the gate, then the up projection
+    int64_t hidden, ffn;
+    int32_t act;
+    uint16_t* h;               // [2, m * top, ffn]
+    const uint16_t* res; int64_t ldres;                   // null: zero
+    uint16_t* y; int64_t ldy;
+};
+hipError_t launch_moe(const MoeLaunch& p, hipStream_t s);
+
+struct RouteLaunch {
+    const void* logits; int32_t bf16; int64_t ld, rows; int32_t experts, top;
+    int32_t sigmoid, renormalize;
+    const float* bias;         // [experts], null: none
+    float scale;
+    int32_t* ids; float* weights;                         // [rows, top]
+};
+hipError_t launch_moe_route(const RouteLaunch& p, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// distillation (distill.hip)
+// ---------------------------------------------------------------------------
+constexpr int kDistillMaxTop = 128, kDistillStats = 7;
+constexpr int64_t kDsMost = int64_t(1) << 18;             // elements of a forward piece at most: 32 KiB of bitmap
+struct DistillLaunch {
+    const void* logits; int32_t bf16; int64_t ld, rows, vocab;
+    const int32_t* ids; const float* logprobs; int32_t top;   // [rows, top]
+    float inv_temperature; int32_t renormalize;
+    // stats [rows, kDistillStats] = {largest logit, 1 / the sum about it, largest logit that is not listed, 1 / the
+    // sum of those about it, coefficient of a listed token's probability, of another's share, log of the list's mass}
+    float* loss; float* stats;
+    float* part;               // [rows, pieces, 2]
+    int64_t piece;
+};
+int64_t distill_pieces(int64_t rows, int64_t vocab);
+hipError_t launch_distill(const DistillLaunch& p, int64_t pieces, hipStream_t s);
+
+struct DistillGradLaunch {
+    const void* logits; int32_t bf16; int64_t ld, rows, vocab;
+    const int32_t* ids; const float* logprobs; int32_t top;
+    float inv_temperature;
+    const float* stats; const float* g_loss;
+    void* dlogits; int64_t ldd;
+    int64_t piece;
+};
+hipError_t launch_distill_backward(const DistillGradLaunch& p, hipStream_t s);
 
 }  // namespace fp4

@@ -38,15 +38,29 @@
 
 #include "fp4_device.hpp"
 #include "fp4_internal.h"
+#include "gemm_device.hpp"
+
+// This file is compiled twice: as it stands, and through gemm_epilogue.hip
+// with the product followed by bias, activation, multiplier and residual.  The
+// second set of kernels is one of its own (namespace epi): as a condition of
+// every launch the epilogue would cost the plain products registers.
+#ifndef FP4_EPILOGUE_FORM
+#define FP4_EPILOGUE_FORM 0
+#endif
+
+#if FP4_EPILOGUE_FORM
+#include "epilogue_device.hpp"
+#endif
 
 namespace fp4 {
-
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef float v16f __attribute__((ext_vector_type(16)));
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+#if FP4_EPILOGUE_FORM
+namespace epi {
+using GemmArgs = GemmEpiLaunch;
+using WoArgs = WoEpiLaunch;
+#else
+using GemmArgs = GemmLaunch;
+using WoArgs = WoGemmLaunch;
+#endif
 
 constexpr int kTile = 256;        // workgroup tile (rows of W) x (rows of A)
 constexpr int kGemmThreads = 256;
@@ -55,41 +69,63 @@ constexpr int kGemmThreads = 256;
 // epilogue: acc[i][j] holds D[n = 32 i + 8 q + 4 (l/32) + e][m = 32 j + l%32]
 // for register r = 4 q + e; scale by g and store as bf16 into C[m][n].
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void store_tile(const v16f (&acc)[4][4], float g, uint16_t* __restrict__ c, int64_t ldc,
-                                           int64_t m_base, int64_t n_base, int64_t M, int64_t N)
+#if FP4_EPILOGUE_FORM
+// C[m][n .. n + 3] = the epilogue of g v
+__device__ __forceinline__ void store_quad(const GemmArgs& p, int64_t m, int64_t n, bool, float g, float v0, float v1, float v2,
+                                           float v3)
 {
-    // 8-byte stores need 8-byte aligned rows; otherwise store element-wise
-    const bool vec = ((ldc & 3) == 0) && ((reinterpret_cast<uintptr_t>(c) & 7) == 0);
+    if (n >= p.n) return;
+    const float v[4] = {v0 * g, v1 * g, v2 * g, v3 * g};
+    float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (p.ep.bias)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < p.n) b[i] = epi_bias(p.ep, n + i);
+    epi_put<4>(p.ep, p.c, p.ldc, m, n, p.n, v, b);
+}
+#else
+// C[m][n .. n + 3] = bf16(g v).  8-byte stores need 8-byte aligned rows;
+// otherwise element-wise.
+__device__ __forceinline__ void store_quad(const GemmArgs& p, int64_t m, int64_t n, bool vec, float g, float v0, float v1,
+                                           float v2, float v3)
+{
+    uint16_t* const crow = p.c + m * p.ldc;
+    const uint32_t b0 = f32_to_bf16_rne(v0 * g), b1 = f32_to_bf16_rne(v1 * g);
+    const uint32_t b2 = f32_to_bf16_rne(v2 * g), b3 = f32_to_bf16_rne(v3 * g);
+    if (vec && n + 3 < p.n) {
+        *reinterpret_cast<uint2*>(crow + n) = uint2{b0 | (b1 << 16), b2 | (b3 << 16)};
+    } else {
+        if (n + 0 < p.n) crow[n + 0] = (uint16_t)b0;
+        if (n + 1 < p.n) crow[n + 1] = (uint16_t)b1;
+        if (n + 2 < p.n) crow[n + 2] = (uint16_t)b2;
+        if (n + 3 < p.n) crow[n + 3] = (uint16_t)b3;
+    }
+}
+#endif
+__device__ __forceinline__ bool quads(const GemmArgs& p)
+{
+    return ((p.ldc & 3) == 0) && ((reinterpret_cast<uintptr_t>(p.c) & 7) == 0);
+}
+
+#if !FP4_EPILOGUE_FORM
+__device__ __forceinline__ void store_tile(const GemmArgs& p, const v16f (&acc)[4][4], float g, int64_t m_base,
+                                           int64_t n_base)
+{
+    const bool vec = quads(p);
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int64_t m = m_base + 32 * j + (lane & 31);
-        if (m >= M) continue;
-        uint16_t* crow = c + m * ldc;
+        if (m >= p.m) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t n = n_base + 32 * i + 8 * q + 4 * (lane >> 5);
-                const uint32_t b0 = f32_to_bf16_rne(acc[i][j][4 * q + 0] * g);
-                const uint32_t b1 = f32_to_bf16_rne(acc[i][j][4 * q + 1] * g);
-                const uint32_t b2 = f32_to_bf16_rne(acc[i][j][4 * q + 2] * g);
-                const uint32_t b3 = f32_to_bf16_rne(acc[i][j][4 * q + 3] * g);
-                if (vec && n + 3 < N) {
-                    uint2 v;
-                    v.x = b0 | (b1 << 16);
-                    v.y = b2 | (b3 << 16);
-                    *reinterpret_cast<uint2*>(crow + n) = v;
-                } else {
-                    if (n + 0 < N) crow[n + 0] = (uint16_t)b0;
-                    if (n + 1 < N) crow[n + 1] = (uint16_t)b1;
-                    if (n + 2 < N) crow[n + 2] = (uint16_t)b2;
-                    if (n + 3 < N) crow[n + 3] = (uint16_t)b3;
-                }
-            }
-        }
+            for (int q = 0; q < 4; ++q)
+                store_quad(p, m, n_base + 32 * i + 8 * q + 4 * (lane >> 5), vec, g, acc[i][j][4 * q + 0],
+                           acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
     }
 }
+#endif
 
 // ---------------------------------------------------------------------------
 // MXFP4: native block-scaled FP4 matrix instruction
@@ -125,18 +161,6 @@ __device__ __forceinline__ void tile_coords(int tiles_n, int tiles_m, int* tn, i
 constexpr int kMx4Threads = 512;
 constexpr int kMx3BK = 128;                          // K elements per stage (f16 path)
 constexpr int kMx3RB = kMx3BK / 2;                   // 64 bytes of codes per row
-constexpr int kMx3Codes = kTile * kMx3RB;            // 16 KiB per operand per stage
-
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
-
-__device__ __forceinline__ void dma16(const void* g, uint8_t* lds)
-{
-    __builtin_amdgcn_global_load_lds(g, (lds_ptr_t)lds, 16, 0, 0);
-}
-__device__ __forceinline__ void dma4(const void* g, uint8_t* lds)
-{
-    __builtin_amdgcn_global_load_lds(g, (lds_ptr_t)lds, 4, 0, 0);
-}
 
 template <int BK>
 struct MxStage {
@@ -168,41 +192,60 @@ __device__ __forceinline__ int mx_swz(int r)
     return BK == 128 ? (((r >> 1) ^ (r >> 3)) & 3) : ((r >> 1) & 7);
 }
 
-__device__ __forceinline__ void store_tile_4x2(const v16f (&acc)[4][2], float g, uint16_t* __restrict__ c,
-                                               int64_t ldc, int64_t m_base, int64_t n_base, int64_t M, int64_t N)
+#if FP4_EPILOGUE_FORM
+// The image holds binary32, so half of the tile's rows at a time: the waves
+// that have them write g times their sums, then every thread takes pieces of
+// eight columns -- always the same eight, whose bias it reads once -- through
+// the epilogue, with multiplier, residual and outputs in whole 512-byte rows
+// of a half wave.  Everything between the sums and the one rounding of each
+// output stays in binary32, and the elementwise work is a rolled loop: the
+// tile's 128 sums a thread unrolled through five activations would not fit
+// the instruction cache.
+constexpr int kCTileRow = 4 * kTile + 16;           // bytes per LDS row of the image
+constexpr int kCTileBytes = kTile / 2 * kCTileRow;
+
+template <int NJ>
+__device__ __forceinline__ void store_tile_lds(const GemmArgs& p, const v16f (&acc)[4][NJ], float g,
+                                               uint8_t* __restrict__ img, int wm_off, int wn_off, int64_t m_base,
+                                               int64_t n_base)
 {
-    const bool vec = ((ldc & 3) == 0) && ((reinterpret_cast<uintptr_t>(c) & 7) == 0);
-    const int lane = threadIdx.x & 63;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int cb = tid % (kTile / 8);
+    const int64_t n = n_base + 8 * cb;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        __syncthreads();                             // every wave is done reading the stages, or the other half
+        if (wm_off / (kTile / 2) == half) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int64_t m = m_base + 32 * j + (lane & 31);
-        if (m >= M) continue;
-        uint16_t* crow = c + m * ldc;
+            for (int j = 0; j < NJ; ++j) {
+                uint8_t* const row = img + (wm_off % (kTile / 2) + 32 * j + (lane & 31)) * kCTileRow;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t n = n_base + 32 * i + 8 * q + 4 * (lane >> 5);
-                const uint32_t b0 = f32_to_bf16_rne(acc[i][j][4 * q + 0] * g);
-                const uint32_t b1 = f32_to_bf16_rne(acc[i][j][4 * q + 1] * g);
-                const uint32_t b2 = f32_to_bf16_rne(acc[i][j][4 * q + 2] * g);
-                const uint32_t b3 = f32_to_bf16_rne(acc[i][j][4 * q + 3] * g);
-                if (vec && n + 3 < N) {
-                    uint2 v;
-                    v.x = b0 | (b1 << 16);
-                    v.y = b2 | (b3 << 16);
-                    *reinterpret_cast<uint2*>(crow + n) = v;
-                } else {
-                    if (n + 0 < N) crow[n + 0] = (uint16_t)b0;
-                    if (n + 1 < N) crow[n + 1] = (uint16_t)b1;
-                    if (n + 2 < N) crow[n + 2] = (uint16_t)b2;
-                    if (n + 3 < N) crow[n + 3] = (uint16_t)b3;
-                }
+                    for (int q = 0; q < 4; ++q) {
+                        const int nl = wn_off + 32 * i + 8 * q + 4 * (lane >> 5);
+                        *reinterpret_cast<v4f*>(row + 4 * nl) =
+                            v4f{acc[i][j][4 * q + 0] * g, acc[i][j][4 * q + 1] * g, acc[i][j][4 * q + 2] * g,
+                                acc[i][j][4 * q + 3] * g};
+                    }
             }
+        }
+        __syncthreads();
+        if (n >= p.n) continue;
+        float bias[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bias[i] = p.ep.bias && n + i < p.n ? epi_bias(p.ep, n + i) : 0.0f;
+        for (int ml = tid / (kTile / 8); ml < kTile / 2; ml += (int)blockDim.x / (kTile / 8)) {
+            const int64_t m = m_base + half * (kTile / 2) + ml;
+            if (m >= p.m) break;
+            const v4f* const src = reinterpret_cast<const v4f*>(img + ml * kCTileRow + 32 * cb);
+            const v4f a = src[0], b = src[1];
+            const float sum[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+            epi_put<8>(p.ep, p.c, p.ldc, m, n, p.n, sum, bias);
         }
     }
 }
-
+#else
 // Epilogue of the 256 x 256 tiles through LDS (the stage buffers are free by
 // then).  Each wave writes its scaled bf16 sub-tile, whose lanes each hold
 // one column m and runs of four n, into a row-major image of the C tile
@@ -252,6 +295,7 @@ __device__ __forceinline__ void store_tile_lds(const v16f (&acc)[4][NJ], float g
         }
     }
 }
+#endif
 
 // The scaled matrix instruction taking byte SEL of each operand's scale
 // dword (the instruction's own byte select).
@@ -274,7 +318,7 @@ __device__ __forceinline__ v16f mfma_fp4_step(int ks, const v8i& w, const v8i& a
 }
 
 template <int BK, int NS>
-__global__ __launch_bounds__(kMx4Threads) void k_gemm_mx(GemmLaunch p)
+__global__ __launch_bounds__(kMx4Threads) void k_gemm_mx(GemmArgs p)
 {
     using L = MxStage<BK>;
     static_assert(NS >= 2 && (BK == 128 || BK == 256), "stage shape");
@@ -514,19 +558,15 @@ __global__ __launch_bounds__(kMx4Threads) void k_gemm_mx(GemmLaunch p)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     static_assert(NS * L::Bytes + (L::Grouped ? 2 * L::GroupBytes : 0) >= kCTileBytes, "the C image fits the LDS");
     const float g = p.ga[0] * p.gb[0];
+#if FP4_EPILOGUE_FORM
+    store_tile_lds<2>(p, acc, g, smem, wm * 64, wn * 128, m_base, n_base);
+#else
     store_tile_lds<2>(acc, g, smem, p.c, p.ldc, wm * 64, wn * 128, m_base, n_base, M, N);
-}
-
-// Kernels with more than 64 KiB of dynamic LDS must opt in once per device.
-template <typename K>
-static hipError_t allow_lds(K kernel, size_t bytes)
-{
-    return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)bytes);
+#endif
 }
 
 template <int BK, int NS>
-static hipError_t launch_mx(const GemmLaunch& p, hipStream_t s)
+static hipError_t launch_mx(const GemmArgs& p, hipStream_t s)
 {
     constexpr size_t sh = (size_t)NS * MxStage<BK>::Bytes + (MxStage<BK>::Grouped ? 2 * MxStage<BK>::GroupBytes : 0);
     static_assert(sh <= 160 * 1024, "LDS");
@@ -539,7 +579,7 @@ static hipError_t launch_mx(const GemmLaunch& p, hipStream_t s)
 
 // 256-element stages read whole 128-byte lines of every row (two stages fit
 // in LDS); K that is only a multiple of 128 takes four 128-element stages.
-hipError_t launch_gemm_mx(const GemmLaunch& p, hipStream_t s)
+hipError_t launch_gemm_mx(const GemmArgs& p, hipStream_t s)
 {
     if (p.k % 256 == 0 && p.k >= 512) return launch_mx<256, 2>(p, s);
     return launch_mx<128, 4>(p, s);
@@ -582,7 +622,7 @@ struct Mx16Shape {
 };
 
 
-__global__ __launch_bounds__(kMx4Threads) void k_gemm_mx16(GemmLaunch p)
+__global__ __launch_bounds__(kMx4Threads) void k_gemm_mx16(GemmArgs p)
 {
     using L = Mx16Shape;
     constexpr int NS = 2;
@@ -714,9 +754,14 @@ __global__ __launch_bounds__(kMx4Threads) void k_gemm_mx16(GemmLaunch p)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     static_assert(NS * L::Bytes + 2 * L::GroupBytes >= kCTileBytes, "the C image fits the LDS");
     const float gg = p.ga[0] * p.gb[0];
+#if FP4_EPILOGUE_FORM
+    store_tile_lds<2>(p, acc, gg, smem, wm * 64, wn * 128, m_base, n_base);
+#else
     store_tile_lds<2>(acc, gg, smem, p.c, p.ldc, wm * 64, wn * 128, m_base, n_base, M, N);
+#endif
 }
 
+#if !FP4_EPILOGUE_FORM
 // E2M1 with E8M0 scales at block 16 on both operands, whole 256-element
 // stages, at least 16 scale bytes per row and operands below 4 GiB.
 bool gemm_mx16_supported(const GemmLaunch& p)
@@ -725,8 +770,9 @@ bool gemm_mx16_supported(const GemmLaunch& p)
     if (p.m * (p.k / 2) >= (int64_t(1) << 32) || p.n * (p.k / 2) >= (int64_t(1) << 32)) return false;
     return p.k % 256 == 0 && p.k / 16 >= 16;
 }
+#endif
 
-hipError_t launch_gemm_mx16(const GemmLaunch& p, hipStream_t s)
+hipError_t launch_gemm_mx16(const GemmArgs& p, hipStream_t s)
 {
     using L = Mx16Shape;
     constexpr size_t sh = (size_t)2 * L::Bytes + 2 * L::GroupBytes;
@@ -748,14 +794,6 @@ struct DqSmem {
     uint8_t w[2][kTile * kDqRow];
     uint8_t a[2][kTile * kDqRow];
 };
-
-// Largest power of two not above a positive normal g (1 for anything else):
-// g / split_pow2(g) lies in [1, 2) and the division is exact.
-__device__ __forceinline__ float split_pow2(float g)
-{
-    const uint32_t e = __float_as_uint(g) & 0x7F800000u;
-    return (e == 0u || e == 0x7F800000u || g < 0.0f) ? 1.0f : __uint_as_float(e);
-}
 
 // Dequantize 32 E2M1 codes (16 bytes) with scale(s) into 32 16-bit values.
 // The product e2m1 * s is exact in binary32 and, for the chosen element type,
@@ -807,7 +845,6 @@ __device__ __forceinline__ void dequant32_split(const v4i& codes, float s0, floa
     }
 }
 
-typedef float v2f __attribute__((ext_vector_type(2)));
 
 // Dequantize 16 one-byte elements (FP8 E4M3 codes for ELEM 2, INT8 for
 // ELEM 3) with one scale into 16 16-bit values; out[j] holds elements 2j and
@@ -902,7 +939,7 @@ __device__ __forceinline__ void dequant32_w6(const uint64_t d[3], float s0, floa
 // products carry 4 + 4 bits, E3M2 3 + 5, INT6 5 + 3 in bf16 or 5 + 6 in
 // f16); the LDS tiles and the matrix loop are the same.
 template <bool F16, int BLOCK, int ELEM = 0>
-__global__ __launch_bounds__(kGemmThreads) void k_gemm_dq(GemmLaunch p)
+__global__ __launch_bounds__(kGemmThreads) void k_gemm_dq(GemmArgs p)
 {
     constexpr bool INT = ELEM == 1;
     constexpr bool W8 = ELEM == 2 || ELEM == 3;
@@ -1054,7 +1091,12 @@ __global__ __launch_bounds__(kGemmThreads) void k_gemm_dq(GemmLaunch p)
         if (kt + 1 < KT) sstore(buf ^ 1);
         __syncthreads();
     }
-    store_tile(acc, g, p.c, p.ldc, m_base + wm * 128, n_base + wn * 128, M, N);
+#if FP4_EPILOGUE_FORM
+    static_assert(sizeof(DqSmem) >= kCTileBytes, "the image fits the LDS");
+    store_tile_lds<4>(p, acc, g, smem_raw, wm * 128, wn * 128, m_base, n_base);
+#else
+    store_tile(p, acc, g, m_base + wm * 128, n_base + wn * 128);
+#endif
 }
 
 // ---------------------------------------------------------------------------
@@ -1178,7 +1220,7 @@ struct NvHalf {
 // read while half 1's products run.  The conversions of each 32x32x16 step
 // are interleaved with the previous step's products.
 template <int BLOCK, int NS, int CVT, int WM>
-__global__ __launch_bounds__(128 * WM) void k_gemm_nv(GemmLaunch p)
+__global__ __launch_bounds__(128 * WM) void k_gemm_nv(GemmArgs p)
 {
     constexpr bool FP8 = CVT == kNvFp8, INT8 = CVT == kNvInt8;
     constexpr bool W8 = FP8 || INT8;            // one byte per element
@@ -1414,17 +1456,16 @@ __global__ __launch_bounds__(128 * WM) void k_gemm_nv(GemmLaunch p)
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     static_assert(NS * L::kBytes >= kCTileBytes, "the C image fits the stage buffers");
     const float gg = BF16 ? (p.ga[0] / pa) * (p.gb[0] / pw) : p.ga[0] * p.gb[0];
+#if FP4_EPILOGUE_FORM
+    store_tile_lds<JA>(p, acc, gg, smem, wm * 32 * JA, wn * 128, m_base, n_base);
+#else
     store_tile_lds<JA>(acc, gg, smem, p.c, p.ldc, wm * 32 * JA, wn * 128, m_base, n_base, M, N);
+#endif
 }
 
 #ifndef FP4_NV_NS
 #define FP4_NV_NS 4
 #endif
-
-// Formats whose e2m1 * s products are exact in f16 (normal range) and those
-// exact in bf16 (at most 8 significant bits).
-static bool exact_in_f16(const ScaleFmtHost& f) { return !f.is_e8m0 && f.ebits <= 4 && (f.ebits + f.mbits == 7); }
-static bool exact_in_bf16(const ScaleFmtHost& f) { return f.is_e8m0 || f.mbits <= 5; }
 
 static bool is_e4m3(const ScaleFmtHost& f) { return !f.is_e8m0 && f.ebits == 4 && f.mbits == 3; }
 
@@ -1437,7 +1478,7 @@ static bool is_e4m3(const ScaleFmtHost& f) { return !f.is_e8m0 && f.ebits == 4 &
 // bf16 and 8-bit forms: four waves (one per SIMD); 8-bit rows (128 bytes
 // per stage) leave room for two stages.
 template <int BLOCK, int CVT>
-static hipError_t launch_nv(const GemmLaunch& p, hipStream_t s)
+static hipError_t launch_nv(const GemmArgs& p, hipStream_t s)
 {
     constexpr bool W8 = CVT == kNvFp8 || CVT == kNvInt8;
     constexpr int WM = CVT == kNvBf16 || W8 ? 2 : 4;
@@ -1482,10 +1523,12 @@ static hipError_t launch_nv(const GemmLaunch& p, hipStream_t s)
 // ---------------------------------------------------------------------------
 constexpr int kSmallWaves = 4;
 constexpr int kSmallAhead = 8;
+#if !FP4_EPILOGUE_FORM
 int64_t g_gemm_small_outputs = (int64_t)1 << 21;
+#endif
 
 template <int MODE, int BLOCK, bool KSPLIT>
-__global__ __launch_bounds__(64 * kSmallWaves) void k_gemm_small(GemmLaunch p)
+__global__ __launch_bounds__(64 * kSmallWaves) void k_gemm_small(GemmArgs p)
 {
     static_assert(MODE != 2 || BLOCK == 32, "MXFP4 scales cover 32 elements");
     static_assert(MODE != 4 || BLOCK == 16, "two runs per K-half for blocks of 16");
@@ -1646,23 +1689,11 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_gemm_small(GemmLaunch p)
     const int64_t m = m0 + r;
     if (m >= p.m) return;
     const float g = FOLD ? (p.ga[0] / pa) * (p.gb[0] / pw) : p.ga[0] * p.gb[0];
-    uint16_t* crow = p.c + m * p.ldc;
-    const bool vec = ((p.ldc & 3) == 0) && ((reinterpret_cast<uintptr_t>(p.c) & 7) == 0);
+    const bool vec = quads(p);
 #pragma unroll
-    for (int qi = 0; qi < NQS; ++qi) {
-        const int q = KSPLIT ? wave : qi;
-        const int64_t n = n0 + 8 * q + 4 * h;
-        const uint32_t b0 = f32_to_bf16_rne(v[4 * qi + 0] * g), b1 = f32_to_bf16_rne(v[4 * qi + 1] * g);
-        const uint32_t b2 = f32_to_bf16_rne(v[4 * qi + 2] * g), b3 = f32_to_bf16_rne(v[4 * qi + 3] * g);
-        if (vec && n + 3 < p.n) {
-            *reinterpret_cast<uint2*>(crow + n) = uint2{b0 | (b1 << 16), b2 | (b3 << 16)};
-        } else {
-            if (n + 0 < p.n) crow[n + 0] = (uint16_t)b0;
-            if (n + 1 < p.n) crow[n + 1] = (uint16_t)b1;
-            if (n + 2 < p.n) crow[n + 2] = (uint16_t)b2;
-            if (n + 3 < p.n) crow[n + 3] = (uint16_t)b3;
-        }
-    }
+    for (int qi = 0; qi < NQS; ++qi)
+        store_quad(p, m, n0 + 8 * (KSPLIT ? wave : qi) + 4 * h, vec, g, v[4 * qi + 0], v[4 * qi + 1], v[4 * qi + 2],
+                   v[4 * qi + 3]);
 }
 
 // The small path takes E2M1 operands with E8M0 scales (block 32 or 16), or with
@@ -1677,6 +1708,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void k_gemm_small(GemmLaunch p)
 // 91, 512 x 4096 68 against 89, 256 x 11008 111 against 92 (tiled), and
 // MXFP4 64 x 11008 37 against 31 (tiled); UE5M3 (bf16 form) 64 x 11008 63
 // against 156, 256 x 11008 126 against 160, 512 x 4096 90 against 159.
+#if !FP4_EPILOGUE_FORM
 bool gemm_small_supported(const GemmLaunch& p)
 {
     if ((p.m + 31) / 32 > 65535) return false;
@@ -1690,6 +1722,7 @@ bool gemm_small_supported(const GemmLaunch& p)
     if (exact_in_f16(p.fa) && exact_in_f16(p.fb)) return mn <= (double)bound;
     return exact_in_bf16(p.fa) && exact_in_bf16(p.fb) && mn <= 1.5 * (double)bound;
 }
+#endif
 
 // Fewer 32 x 32 output tiles than SIMDs: the four waves of a workgroup split
 // K of one tile (more waves in flight, each a quarter of the chunks);
@@ -1699,7 +1732,7 @@ bool gemm_small_supported(const GemmLaunch& p)
 // 9.5 -> 7.5 and MXFP4 6.8 -> 5.9; but NVFP4 512 x 4096 x 4096 (2048
 // tiles) 68 -> 85.
 template <int MODE, int BLOCK>
-static void launch_small_mode(const GemmLaunch& p, hipStream_t s)
+static void launch_small_mode(const GemmArgs& p, hipStream_t s)
 {
     const int64_t tm = (p.m + 31) / 32, tn = (p.n + 31) / 32;
     const dim3 t(64 * kSmallWaves);
@@ -1710,7 +1743,7 @@ static void launch_small_mode(const GemmLaunch& p, hipStream_t s)
                            (unsigned)tm), t, 0, s, p);
 }
 
-hipError_t launch_gemm_small(const GemmLaunch& p, hipStream_t s)
+hipError_t launch_gemm_small(const GemmArgs& p, hipStream_t s)
 {
     if (p.elem == 2) {
         if (p.block == 16) launch_small_mode<5, 16>(p, s);
@@ -1776,15 +1809,17 @@ static int dq_type(const ScaleFmtHost& fa, const ScaleFmtHost& fb, int elem)
     }
 }
 
+#if !FP4_EPILOGUE_FORM
 bool gemm_dq_supported(const ScaleFmtHost& fa, const ScaleFmtHost& fb, int elem)
 {
     return dq_type(fa, fb, elem) != 0;
 }
+#endif
 
 // Operands on the INT4 or an 8-bit grid: the exact dequantize path with the
 // grid's decode, in the 16-bit type dq_type picks.
 template <int BLOCK, int ELEM>
-static hipError_t launch_dq_elem(const GemmLaunch& p, bool f16, hipStream_t s)
+static hipError_t launch_dq_elem(const GemmArgs& p, bool f16, hipStream_t s)
 {
     dim3 grid((unsigned)((p.n + kTile - 1) / kTile), (unsigned)((p.m + kTile - 1) / kTile));
     const size_t sh = sizeof(DqSmem);
@@ -1803,12 +1838,12 @@ static hipError_t launch_dq_elem(const GemmLaunch& p, bool f16, hipStream_t s)
 }
 
 template <int ELEM>
-static hipError_t launch_dq_grid(const GemmLaunch& p, bool f16, hipStream_t s)
+static hipError_t launch_dq_grid(const GemmArgs& p, bool f16, hipStream_t s)
 {
     return p.block == 16 ? launch_dq_elem<16, ELEM>(p, f16, s) : launch_dq_elem<32, ELEM>(p, f16, s);
 }
 
-hipError_t launch_gemm_dq(const GemmLaunch& p, hipStream_t s)
+hipError_t launch_gemm_dq(const GemmArgs& p, hipStream_t s)
 {
     if (p.elem != 0) {
         const int t = dq_type(p.fa, p.fb, p.elem);
@@ -1890,162 +1925,11 @@ hipError_t launch_gemm_dq(const GemmLaunch& p, hipStream_t s)
 // free of bank conflicts.  The waves' partial tiles are summed in LDS in a
 // fixed order (deterministic).
 // ---------------------------------------------------------------------------
-typedef float v4f __attribute__((ext_vector_type(4)));
-
-// Exact bf16 dequantization of one dword of 8 E2M1 codes with scale s.  The
-// gfx950 converts apply only the exponent of their scale operand, so:
-//  POW2 (E8M0 scales): v_cvt_scalef32_pk_bf16_fp4 with s does everything;
-//  otherwise: convert with scale 1 to fp32, multiply by s (exact: at most
-//  9 significant bits), keep the top half (exact when the value fits bf16).
-// Elements 2b and 2b + 1 of a dword of codes as binary32: the hardware
-// E2M1 conversion (scale 1), or for INT4 the sign-extended nibbles.
-template <bool INT>
-__device__ __forceinline__ v2f elem_pair_f32(uint32_t w, int b)
-{
-    if (INT)
-        return v2f{(float)((int32_t)(w << (28 - 8 * b)) >> 28), (float)((int32_t)(w << (24 - 8 * b)) >> 28)};
-    return b == 0 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0)
-         : b == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1)
-         : b == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2)
-                  : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-}
-
-// Elements k and k + 1 (k even) of the codes dw of one chunk row piece (the
-// grid's packing: 4-bit nibbles, bytes, or the six-bit stream) as binary32:
-// E2M1 and FP8 E4M3 by the hardware conversions (scale 1, exact), INT4 /
-// INT8 / INT6 sign-extended, FP6 E2M3 / E3M2 through the FP8 E4M3 / E5M2
-// byte of the value times 2^-6 / 2^-12 (exact) and one multiply back.  k is
-// a compile-time constant after unrolling.
-template <int ELEM>
-__device__ __forceinline__ v2f elem_pair_any(const uint32_t* dw, int k)
-{
-    if constexpr (ELEM <= 1) {
-        return elem_pair_f32<ELEM == 1>(dw[k >> 3], (k & 7) >> 1);
-    } else if constexpr (ELEM == 2) {
-        return (k & 3) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)dw[k >> 2], true)
-                       : __builtin_amdgcn_cvt_pk_f32_fp8((int)dw[k >> 2], false);
-    } else if constexpr (ELEM == 3) {
-        const uint32_t w = dw[k >> 2] >> (8 * (k & 3));
-        return v2f{int8_value(w), int8_value(w >> 8)};
-    } else {
-        const int bit = 6 * k, i = bit >> 5, sh = bit & 31;
-        const uint32_t x = sh + 12 <= 32 ? dw[i] >> sh : __builtin_amdgcn_alignbit(dw[i + 1], dw[i], sh);
-        if constexpr (ELEM == 6) {
-            return v2f{(float)((int32_t)(x << 26) >> 26), (float)((int32_t)(x << 20) >> 26)};
-        } else {
-            // the two codes to one byte each, sign bit 5 -> 7: the FP8 byte
-            const uint32_t y = (x & 0x3Fu) | ((x << 2) & 0x3F00u);
-            const uint32_t w = (y & 0x1F1Fu) | ((y & 0x2020u) << 2);
-            const v2f e = ELEM == 4 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false)
-                                    : __builtin_amdgcn_cvt_pk_f32_bf8((int)w, false);
-            constexpr float kFold = ELEM == 4 ? 64.0f : 4096.0f;
-            return v2f{e[0] * kFold, e[1] * kFold};
-        }
-    }
-}
-
-// Elements 8t .. 8t + 7 of dw times s as bf16 pairs: hi the truncation of
-// each binary32 product (exact when it fits bf16), with SPLIT lo the exact
-// remainder (products of up to 16 significant bits).
-template <int ELEM, bool SPLIT>
-__device__ __forceinline__ void dq8_any(const uint32_t* dw, int t, float s, v4i& hi, v4i& lo)
-{
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const v2f f = elem_pair_any<ELEM>(dw, 8 * t + 2 * b);
-        const float v0 = f[0] * s, v1 = f[1] * s;
-        if (SPLIT) {
-            const uint32_t h0 = __float_as_uint(v0) & 0xFFFF0000u, h1 = __float_as_uint(v1) & 0xFFFF0000u;
-            const float l0 = v0 - __uint_as_float(h0), l1 = v1 - __uint_as_float(h1);
-            hi[b] = (int)((h0 >> 16) | h1);
-            lo[b] = (int)((__float_as_uint(l0) >> 16) | (__float_as_uint(l1) & 0xFFFF0000u));
-        } else {
-            hi[b] = (int)__builtin_amdgcn_perm(__float_as_uint(v1), __float_as_uint(v0), 0x07060302u);
-        }
-    }
-}
-
-// INT: INT4 elements (never POW2: the multiply by s is exact for E8M0 too).
-template <bool POW2, bool INT = false>
-__device__ __forceinline__ v4i dq8_bf16(uint32_t w, float s)
-{
-    v4i r;
-    if (POW2 && !INT) {
-        r[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
-        r[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
-        r[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
-        r[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
-    } else {
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const v2f f = elem_pair_f32<INT>(w, b);
-            const uint32_t lo = __float_as_uint(f[0] * s), hi = __float_as_uint(f[1] * s);
-            r[b] = (int)__builtin_amdgcn_perm(hi, lo, 0x07060302u);     // {hi[31:16], lo[31:16]}
-        }
-    }
-    return r;
-}
-
-// Products wider than bf16 (E1M6 with E2M1: 9 significant bits; INT4 with
-// 5- or 6-bit mantissas: up to 10): split v = hi + lo, both exact bf16.
-template <bool INT = false>
-__device__ __forceinline__ void dq8_bf16_split(uint32_t w, float s, v4i& hi, v4i& lo)
-{
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const v2f f = elem_pair_f32<INT>(w, b);
-        const float v0 = f[0] * s, v1 = f[1] * s;
-        const uint32_t h0 = __float_as_uint(v0) & 0xFFFF0000u, h1 = __float_as_uint(v1) & 0xFFFF0000u;
-        const float l0 = v0 - __uint_as_float(h0), l1 = v1 - __uint_as_float(h1);
-        hi[b] = (int)((h0 >> 16) | h1);
-        lo[b] = (int)((__float_as_uint(l0) >> 16) | (__float_as_uint(l1) & 0xFFFF0000u));
-    }
-}
-
-// One ring slot of the weight-only GEMM (byte offsets).  A chunk is SUB
-// runs of 128 K-elements.  XQ = 0: M == 1, the single X row arrives by
-// 4-byte loads (SUB of them); else XQ * SUB loads of four 256-byte X row
-// pieces each.  WP: LDS pitch of a W chunk row (64 bytes, or 128 for the
-// wider rows); SCB: scale bytes of a row per chunk.
-template <int RG, int XQ, int WP, int SUB, int SCB>
-struct WoSlot {
-    static constexpr int WD = WP / 64;                 // W loads per 16-row group
-    static constexpr int W = 0;                        // row r of group g at 16 WP g + WP r
-    static constexpr int SC = RG * 16 * WP;            // row r of the slot's 16 RG rows at SC + SCB r
-    static constexpr int SCBytes = (RG * 16 * SCB + 255) / 256 * 256;
-    static constexpr int NSC = (RG * 16 * SCB / 4 + 63) / 64;      // 4-byte scale loads (64 lanes each)
-    static constexpr int X = SC + SCBytes;             // piece h of row m at X + 1024 (SUB (m / 4) + h) + 256 (m % 4)
-    static constexpr int XRows = XQ == 0 ? 1 : 4 * XQ;
-    static constexpr int Bytes = X + 256 * SUB * XRows;
-    static constexpr int Loads = RG * WD + NSC + SUB * (XQ == 0 ? 1 : XQ);   // direct-to-LDS loads per chunk
-};
-
-// 16-byte piece c of row r sits at c ^ swz(r): 64-byte rows (r >> 1) & 3,
-// 128-byte rows (r >> 1) & 7 (16 consecutive rows, one piece each, on
-// distinct banks)
-__device__ __forceinline__ int wo_swz(int r) { return (r >> 1) & 3; }
-__device__ __forceinline__ int wo_swz8(int r) { return (r >> 1) & 7; }
-
-template <int N>
-__device__ __forceinline__ void wait_vmcnt()
-{
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-// Code bytes of a W row per 128 K-elements and the LDS pitch of a chunk row.
-template <int ELEM, int SUB>
-struct WoRow {
-    static constexpr int Bytes128 = ELEM <= 1 ? 64 : ELEM <= 3 ? 128 : 96;
-    static constexpr int WB = SUB * Bytes128;
-    static constexpr int WP = WB <= 64 ? 64 : 128;
-};
-
 // AD: the rows' adapters in the epilogue.  A form of its own: as a condition of
 // every launch it took a quarter of the plain product's waves by its registers
 // (18944 x 3584, 8 rows 15.8 us against 15.5, 16 rows 18.1 against 17.9).
 template <int NW, int D, int RG, int XQ, int BLOCK, bool SPLIT, bool POW2, int ELEM, int SUB, bool AD>
-__global__ __launch_bounds__(64 * NW) void k_wo_gemm(WoGemmLaunch p)
+__global__ __launch_bounds__(64 * NW) void k_wo_gemm(WoArgs p)
 {
     constexpr bool WIDE = ELEM >= 2;
     static_assert(SUB == 1 || (SUB == 2 && !WIDE), "two runs per chunk for the 4-bit grids");
@@ -2302,7 +2186,12 @@ __global__ __launch_bounds__(64 * NW) void k_wo_gemm(WoGemmLaunch p)
                     v += p.ad.scale[sl] * dot;
                 }
             }
+#if FP4_EPILOGUE_FORM
+            const float one[1] = {v}, bias[1] = {p.ep.bias ? epi_bias(p.ep, nn) : 0.0f};
+            epi_put<1>(p.ep, p.y, p.ldy, m, nn, N, one, bias);
+#else
             p.y[m * p.ldy + nn] = (uint16_t)f32_to_bf16_rne(v);
+#endif
         }
     }
 }
@@ -2311,7 +2200,7 @@ template <int RG, int XQ, int ELEM, int SUB, int BLOCK>
 using WoSlotOf = WoSlot<RG, XQ, WoRow<ELEM, SUB>::WP, SUB, 128 * SUB / BLOCK>;
 
 template <int NW, int D, int RG, int XQ, int BLOCK, bool SPLIT, bool POW2, int ELEM, int SUB, bool AD>
-static hipError_t launch_wo_a(const WoGemmLaunch& p, hipStream_t s)
+static hipError_t launch_wo_a(const WoArgs& p, hipStream_t s)
 {
     // the ring, later the partial tiles and, with adapters, their T (16 rows of up to 128)
     constexpr size_t ring = (size_t)NW * D * WoSlotOf<RG, XQ, ELEM, SUB, BLOCK>::Bytes;
@@ -2331,33 +2220,24 @@ static hipError_t launch_wo_a(const WoGemmLaunch& p, hipStream_t s)
 // table, else four waves x two slots: the same with adapters as without, so
 // that a row that has none keeps the plain product's bits.
 template <int NW, int D, int RG, int XQ, int BLOCK, bool SPLIT, bool POW2, int ELEM, int SUB>
-static hipError_t launch_wo_k(const WoGemmLaunch& p, hipStream_t s)
+static hipError_t launch_wo_k(const WoArgs& p, hipStream_t s)
 {
     constexpr size_t ring = (size_t)NW * D * WoSlotOf<RG, XQ, ELEM, SUB, BLOCK>::Bytes;
     if constexpr (ring + sizeof(float) * 256 > 160 * 1024) {
         static_assert(NW != 4 || D != 2, "the smallest ring fits");
         return launch_wo_k<4, 2, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB>(p, s);
     } else {
+#if !FP4_EPILOGUE_FORM
         if (p.ad.t) return launch_wo_a<NW, D, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB, true>(p, s);
+#endif
         return launch_wo_a<NW, D, RG, XQ, BLOCK, SPLIT, POW2, ELEM, SUB, false>(p, s);
     }
-}
-
-// Significant bits of the largest element of each grid (E2M1 2, INT4 3,
-// FP8 E4M3 4, INT8 7, FP6 E2M3 4, FP6 E3M2 3, INT6 5) plus those of the
-// scale: products with at most 8 are exact in bf16, the others (at most 14)
-// take the hi + lo split.
-static bool wo_exact_in_bf16(int elem, const ScaleFmtHost& f)
-{
-    static const int ebits[7] = {2, 3, 4, 7, 4, 3, 5};
-    const int sbits = f.is_e8m0 ? 1 : f.mbits + 1;
-    return ebits[elem] + sbits <= 8;
 }
 
 // SUB: 128-element runs per chunk of the 4-bit grids (the wider grids
 // take one).
 template <int NW, int D, int RG, int XQ, int ELEM, int SUB>
-static hipError_t launch_wo_w(const WoGemmLaunch& p, hipStream_t s)
+static hipError_t launch_wo_w(const WoArgs& p, hipStream_t s)
 {
     constexpr int U = ELEM >= 2 ? 1 : SUB;
     const bool split = !wo_exact_in_bf16(ELEM, p.fw);
@@ -2370,7 +2250,7 @@ static hipError_t launch_wo_w(const WoGemmLaunch& p, hipStream_t s)
 }
 
 template <int NW, int D, int RG, int XQ, int SUB>
-static hipError_t launch_wo_x(const WoGemmLaunch& p, hipStream_t s)
+static hipError_t launch_wo_x(const WoArgs& p, hipStream_t s)
 {
     switch (p.elem) {
     case 1: return launch_wo_w<NW, D, RG, XQ, 1, SUB>(p, s);
@@ -2396,6 +2276,7 @@ static hipError_t launch_wo_x(const WoGemmLaunch& p, hipStream_t s)
 
 constexpr int64_t kWoManyGroups = 512;   // 16-row groups that fill the device on their own
 
+#if !FP4_EPILOGUE_FORM
 // Zero fill of a bf16 matrix with row stride ld, one 2-byte store per
 // element (a kernel rather than a memset, so graph capture records a kernel
 // node).
@@ -2416,6 +2297,7 @@ hipError_t launch_fill_zero_bf16(uint16_t* c, int64_t ld, int64_t rows, int64_t 
     hipLaunchKernelGGL(k_fill_zero_bf16, dim3(blocks), dim3(256), 0, s, c, ld, rows, cols);
     return hipGetLastError();
 }
+#endif
 
 // Per problem class (measured on the Qwen-2.5 7B MLP decode shapes):
 //  M = 1: four waves with four slots each; with fewer than 512 row groups
@@ -2432,7 +2314,7 @@ hipError_t launch_fill_zero_bf16(uint16_t* c, int64_t ld, int64_t rows, int64_t 
 //   slower, and at M = 1 the single run per chunk is faster).
 //  Each grid takes the ring asked for when its slot fits the LDS, else
 //  four waves x two slots.
-hipError_t launch_wo_gemm(const WoGemmLaunch& p, hipStream_t s)
+hipError_t launch_wo_gemm(const WoArgs& p, hipStream_t s)
 {
     const bool many = (p.n + 15) / 16 >= kWoManyGroups;
     if (p.m == 1) return many ? launch_wo_x<4, 4, 1, 0, 1>(p, s) : launch_wo_x<8, 4, 1, 0, 1>(p, s);
@@ -2441,4 +2323,7 @@ hipError_t launch_wo_gemm(const WoGemmLaunch& p, hipStream_t s)
     return many ? launch_wo_x<4, 2, 2, 4, 1>(p, s) : launch_wo_x<4, 4, 1, 4, 2>(p, s);
 }
 
+#if FP4_EPILOGUE_FORM
+}  // namespace epi
+#endif
 }  // namespace fp4

@@ -548,6 +548,182 @@ FP4_API fp4_status fp4_residual_norm_backward(const fp4_norm* args, const float*
                                               int64_t ld_dres, float* dw_pre, float* dw_post, float* dgate,
                                               void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Products with an epilogue (ue5m3-fp4-pretraining "Что сделали": all suitable
+ * linear layers run in FP4; the pages give no formula for what follows a
+ * product, reading):
+ *   v = A W^T + bias,  y = bf16_RNE(residual + mul act(v)),  pre = bf16_RNE(v)
+ * everything between the product's sums and the roundings in binary32.  With
+ * s(x) = 1 / (1 + e^-x) and Phi the normal distribution, act(v) is
+ *   none v; relu max(v, 0); silu v s(v); gelu v Phi(v);
+ *   gelu_tanh v s(2 u), u = sqrt(2 / pi) (v + 0.044715 v^3)
+ * so that a gated layer is two products: the up projection's output is the
+ * gate projection's mul.  bias: [n] in bias_dtype (f32 or bf16); mul, residual
+ * and pre: bf16 [m, n], element aligned, row strides >= n; each may be null.
+ * y may be mul or residual (same row stride), pre none of them.  Rows of
+ * whole 16-byte vectors (every stride % 8 == 0, every pointer 16-byte
+ * aligned) are read and written as vectors. */
+typedef enum fp4_act {
+    FP4_ACT_NONE = 0,
+    FP4_ACT_RELU = 1,
+    FP4_ACT_SILU = 2,
+    FP4_ACT_GELU = 3,
+    FP4_ACT_GELU_TANH = 4
+} fp4_act;
+
+typedef struct fp4_epilogue {
+    const void* bias;
+    int32_t bias_dtype;
+    int32_t act;
+    const uint16_t* mul; int64_t ld_mul;
+    const uint16_t* residual; int64_t ld_residual;
+    uint16_t* pre; int64_t ld_pre;
+} fp4_epilogue;
+
+/*
+ * fp4_gemm_epilogue -- fp4_gemm followed by the epilogue.  Requirements,
+ * paths and errors as fp4_gemm (K may not be 0 here); the product's error
+ * bound is that of fp4_gemm before any rounding.
+ */
+FP4_API fp4_status fp4_gemm_epilogue(const fp4_tensor* a, const fp4_tensor* b, const fp4_epilogue* e, uint16_t* y,
+                                     int64_t ldy, void* stream);
+
+/*
+ * fp4_wo_gemm_epilogue -- fp4_wo_gemm followed by the epilogue, for serving
+ * (pre is UNSUPPORTED).  Requirements and errors as fp4_wo_gemm (neither N nor
+ * K may be 0 here).
+ */
+FP4_API fp4_status fp4_wo_gemm_epilogue(const uint16_t* x, int64_t ldx, int64_t m, const fp4_tensor* w,
+                                        const fp4_epilogue* e, uint16_t* y, int64_t ldy, void* stream);
+
+/*
+ * fp4_epilogue_backward -- the epilogue's gradients for dy [rows, cols], at
+ * the saved pre (bf16):
+ *   dpre = bf16_RNE(dy mul act'(pre)),  dmul = bf16_RNE(dy act(pre)),
+ *   dbias = sum over the rows of dy mul act'(pre), binary32, unrounded terms
+ * (relu'(0) = 0; the residual's gradient is dy).  All bf16 with row strides
+ * >= cols, element aligned.  mul null: 1, and no dmul.  dbias null: not
+ * computed.  With act none and mul null dpre is dy itself: pre is not read
+ * and dpre may be null.  dpre and dmul may be dy, pre or mul (same row
+ * stride), but not each other.  The sums over the rows are taken in a fixed
+ * order: the same inputs give the same bits.  cols at most 2^24.  workspace
+ * (only with dbias): as above, fp4_epilogue_workspace bytes.
+ */
+FP4_API int64_t fp4_epilogue_workspace(int64_t rows, int64_t cols);
+FP4_API fp4_status fp4_epilogue_backward(const uint16_t* dy, int64_t ld_dy, const uint16_t* pre, int64_t ld_pre,
+                                         const uint16_t* mul, int64_t ld_mul, int64_t rows, int64_t cols, int32_t act,
+                                         uint16_t* dpre, int64_t ld_dpre, uint16_t* dmul, int64_t ld_dmul, float* dbias,
+                                         void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * fp4_moe_route -- a router's choice: for every row of logits [rows, experts]
+ * (f32 or bf16, any row stride ld >= experts, element aligned)
+ *   s = softmax(logits) or, each alone, 1 / (1 + e^-logits)
+ *   ids [rows, top] = the `top` largest of s + bias (bias [experts] binary32,
+ *     null for none: it takes part in the choice alone), largest first, equal
+ *     ones by the lower index; without a bias by the logits themselves
+ *   weights [rows, top] = scale s[ids], with renormalize divided by the chosen
+ *     ones' sum (0 where that is 0)
+ * in binary64, rounded once.  An expert whose logit is -inf is never chosen:
+ * a row with fewer than `top` others ends in id -1 and weight 0.  NaN sorts
+ * above everything.  top 1 .. 16 and at most experts, which are at most 1024;
+ * fewer than 2^22 rows.
+ */
+typedef enum fp4_route_score {
+    FP4_ROUTE_SOFTMAX = 0,
+    FP4_ROUTE_SIGMOID = 1
+} fp4_route_score;
+
+FP4_API fp4_status fp4_moe_route(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t experts, int32_t top,
+                                 int32_t score, const float* bias, int32_t renormalize, float scale, int32_t* ids,
+                                 float* weights, void* stream);
+
+/* The experts of a layer: gate_up [experts * 2 ffn, hidden], each expert's ffn
+ * gate rows before its ffn up rows, and down [experts * hidden, ffn], quantized
+ * along their columns on any element grid (they may differ); up_scale and
+ * down_scale [experts] in binary32 (null: 1) multiply an expert's products, for
+ * experts that were quantized each with a tensor scale of its own. */
+typedef struct fp4_moe_bank {
+    const fp4_tensor* gate_up;
+    const fp4_tensor* down;
+    const float* up_scale;
+    const float* down_scale;
+    int64_t experts;
+} fp4_moe_bank;
+
+/*
+ * fp4_moe -- a whole mixture-of-experts layer for 1 .. 16 tokens (the
+ * weight-only product's rows; quant_prune_distill/574 "Эксперименты"):
+ *   y_i = bf16_RNE(residual_i + sum_k w_ik D_e (act(G_e x_i) (U_e x_i))),
+ *   e = ids_ik
+ * with bf16 x, ids (int32) and weights (binary32) [m, top] dense, top 1 .. 16.
+ * Weights enter the matrix instruction exactly as in fp4_wo_gemm, sums are
+ * binary32, and what act gives reaches the down projection with 16 bits (an
+ * infinity there stays one).  An id outside 0 .. experts - 1 (-1 by
+ * convention) is no expert; an id that a token names twice has both weights.
+ * A token without experts gets residual (null: zero).  Nothing of one token
+ * or expert reaches the results of a token that did not choose it.  The sums
+ * are taken in a fixed order.
+ * hidden % 128 == 0, ffn % 128 == 0; x 16-byte aligned with ldx % 8 == 0;
+ * codes 16-byte and scales 4-byte aligned, no transform, one expert's codes
+ * below 4 GiB, at most 65535 experts; y and residual element aligned, y may be
+ * residual (same row stride) or x.  workspace: as above, fp4_moe_workspace
+ * bytes.
+ */
+FP4_API int64_t fp4_moe_workspace(int64_t m, int32_t top, int64_t ffn);
+FP4_API fp4_status fp4_moe(const uint16_t* x, int64_t ldx, int64_t m, const fp4_moe_bank* bank, const int32_t* ids,
+                           const float* weights, int32_t top, int32_t act, const uint16_t* residual, int64_t ld_residual,
+                           uint16_t* y, int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * fp4_distill_loss -- the loss of a student's logits z [rows, vocab] (f32 or
+ * bf16, any row stride ld >= vocab, element aligned) against a teacher's top
+ * log probabilities, for instance those of fp4_token_logprobs (the pages
+ * train models with FP4 linear layers; the loss is a reading).  With q =
+ * softmax(z / temperature), p_j = exp(top_logprobs_j), P = sum p_j and R the
+ * student's probability of the tokens that are not listed:
+ *   bucket       loss = sum p_j (log p_j - log q_j)
+ *                       + (1 - P) (log(1 - P) - log R)
+ *   renormalize  loss = the first sum with p_j / P in the place of p_j
+ * top_ids (int32) and top_logprobs [rows, top] dense, top 1 .. 128.  An id
+ * outside the vocabulary (-1 by convention) is no entry; a row without
+ * entries, or whose entries have no probability, has loss 0 and no gradient.
+ * A token that is listed twice has the sum of both probabilities, and both
+ * terms.  In the bucket's form a P of 1 or more, by rounding, leaves nothing
+ * for the other tokens, and a student that gives them nothing (all listed, or
+ * -inf) has no such term.  A student's -inf at a token with p > 0 makes the
+ * loss inf (its gradient stays finite); a row of only -inf has loss inf and
+ * gradient 0; a NaN or +inf logit makes its row's loss NaN.
+ * stats [rows, 7]: for the backward call.  temperature > 0, and 2 /
+ * temperature is finite.  Fewer than 2^22 rows, at most 2^24 tokens.
+ * workspace: as above, fp4_distill_workspace bytes.
+ */
+typedef enum fp4_distill_rest {
+    FP4_DISTILL_BUCKET = 0,
+    FP4_DISTILL_RENORMALIZE = 1
+} fp4_distill_rest;
+
+FP4_API int64_t fp4_distill_workspace(int64_t rows, int64_t vocab);
+FP4_API fp4_status fp4_distill_loss(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
+                                    const int32_t* top_ids, const float* top_logprobs, int32_t top, float temperature,
+                                    int32_t rest, float* loss, float* stats, void* workspace, int64_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * fp4_distill_loss_backward -- dlogits [rows, vocab] (the logits' type, row
+ * stride ld_d; it may be the logits themselves) for grad_loss [rows]:
+ *   dz_v = grad_loss (q_v - p_v) / temperature           (bucket: listed v)
+ *   dz_v = grad_loss q_v (1 - (1 - P) / R) / temperature (bucket: others)
+ * with p_v / P, and 0 for the others, in the renormalized form.  Without the
+ * bucket's second term (above) q_v comes with the factor P.  The arguments are
+ * the forward call's; the teacher has no gradient.  A row whose grad_loss is 0
+ * gets zeros whatever its logits hold.
+ */
+FP4_API fp4_status fp4_distill_loss_backward(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
+                                             const int32_t* top_ids, const float* top_logprobs, int32_t top,
+                                             float temperature, int32_t rest, const float* stats, const float* grad_loss,
+                                             void* dlogits, int64_t ld_d, void* stream);
+
 /* Static description of a status code. */
 FP4_API const char* fp4_status_string(fp4_status status);
 
