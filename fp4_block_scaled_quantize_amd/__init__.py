@@ -70,10 +70,16 @@ class Fp4EpilogueC(ctypes.Structure):
 
 
 class Fp4MoeBankC(ctypes.Structure):
-    _fields_ = [("gate_up", ctypes.POINTER(Fp4TensorC)), ("down", ctypes.POINTER(Fp4TensorC)),
-                ("up_scale", ctypes.c_void_p), ("down_scale", ctypes.c_void_p), ("experts", ctypes.c_int64)]
+    _fields_ = [("gate_up", Fp4TensorC), ("down", Fp4TensorC), ("up_scale", ctypes.c_void_p),
+                ("down_scale", ctypes.c_void_p), ("experts", ctypes.c_int64)]
 
 
+# These structures' layouts; packing one costs a fraction of filling a ctypes.Structure.
+_TENSOR_ARGS = struct.Struct("@PPPqqiiiiiIi4x")
+_EPILOGUE_ARGS = struct.Struct("@PiiPqPqPq")
+_MOE_ARGS = struct.Struct("@PPq")
+assert _TENSOR_ARGS.size == ctypes.sizeof(Fp4TensorC) and _EPILOGUE_ARGS.size == ctypes.sizeof(Fp4EpilogueC)
+assert 2 * _TENSOR_ARGS.size + _MOE_ARGS.size == ctypes.sizeof(Fp4MoeBankC)
 # Fp4NormC's layout; packing it costs a third of filling a ctypes.Structure.
 _NORM_ARGS = struct.Struct("@PqPqqqPPPffiii4x")
 assert _NORM_ARGS.size == ctypes.sizeof(Fp4NormC)
@@ -99,7 +105,6 @@ def lib():
     vp, i32, i64, u64, u32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_uint32
     f32 = ctypes.c_float
     T, LB = ctypes.POINTER(Fp4TensorC), ctypes.POINTER(Fp4LoraBankC)
-    EP, MB = ctypes.POINTER(Fp4EpilogueC), ctypes.POINTER(Fp4MoeBankC)
     sig = {
         "fp4_version": (i32, []),
         "fp4_status_string": (ctypes.c_char_p, [i32]),
@@ -127,13 +132,14 @@ def lib():
         "fp4_residual_norm": (i32, [vp, vp, i64, vp, i64, vp, vp]),
         "fp4_residual_norm_workspace": (i64, [i64, i64, i32]),
         "fp4_residual_norm_backward": (i32, [vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp]),
-        "fp4_gemm_epilogue": (i32, [T, T, EP, vp, i64, vp]),
-        "fp4_wo_gemm_epilogue": (i32, [vp, i64, i64, T, EP, vp, i64, vp]),
+        "fp4_gemm_epilogue_workspace": (i64, [vp, vp]),
+        "fp4_gemm_epilogue": (i32, [vp, vp, vp, vp, i64, vp, i64, vp]),
+        "fp4_wo_gemm_epilogue": (i32, [vp, i64, i64, vp, vp, vp, i64, vp]),
         "fp4_epilogue_workspace": (i64, [i64, i64]),
         "fp4_epilogue_backward": (i32, [vp, i64, vp, i64, vp, i64, i64, i64, i32, vp, i64, vp, i64, vp, vp, i64, vp]),
         "fp4_moe_route": (i32, [vp, i32, i64, i64, i64, i32, i32, vp, i32, f32, vp, vp, vp]),
         "fp4_moe_workspace": (i64, [i64, i32, i64]),
-        "fp4_moe": (i32, [vp, i64, i64, MB, vp, vp, i32, i32, vp, i64, vp, i64, vp, i64, vp]),
+        "fp4_moe": (i32, [vp, i64, i64, vp, vp, vp, i32, i32, vp, i64, vp, i64, vp, i64, vp]),
         "fp4_distill_workspace": (i64, [i64, i64]),
         "fp4_distill_loss": (i32, [vp, i32, i64, i64, i64, vp, vp, i32, f32, i32, vp, vp, vp, i64, vp]),
         "fp4_distill_loss_backward": (i32, [vp, i32, i64, i64, i64, vp, vp, i32, f32, i32, vp, vp, vp, i64, vp]),
@@ -220,7 +226,7 @@ class QTensor:
         ts = torch.empty(2, dtype=torch.float32, device=device)
         return cls(q, s, ts, rows, cols, block, scale, rounding, amax, transform, rht_signs, element)
 
-    def c(self) -> Fp4TensorC:
+    def _fits(self):
         # the library reads or writes rows * cols * bits / 8 code bytes and
         # rows * cols / block scale bytes through these pointers, densely
         qb = self.rows * (self.cols * ELEMENT_BITS[self.element] // 8)
@@ -231,6 +237,17 @@ class QTensor:
                 self.tensor_scale.numel() < 2:
             raise ValueError(f"QTensor buffers are smaller than a [{self.rows}, {self.cols}] tensor on the "
                              f"{self.element} grid needs")
+
+    def packed(self) -> bytes:
+        """The C structure as bytes."""
+        self._fits()
+        return _TENSOR_ARGS.pack(self.q.data_ptr(), self.scales.data_ptr(), self.tensor_scale.data_ptr(), self.rows,
+                                 self.cols, self.block, SCALE_FORMATS[self.scale], ROUNDING[self.rounding],
+                                 AMAX[self.amax], TRANSFORM[self.transform], self.rht_signs & 0xFFFFFFFF,
+                                 ELEMENT[self.element])
+
+    def c(self) -> Fp4TensorC:
+        self._fits()
         fmt = Fp4Format(self.block, SCALE_FORMATS[self.scale], ROUNDING[self.rounding], AMAX[self.amax],
                         TRANSFORM[self.transform], self.rht_signs & 0xFFFFFFFF, ELEMENT[self.element])
         return Fp4TensorC(self.q.data_ptr(), self.scales.data_ptr(), self.tensor_scale.data_ptr(),
@@ -808,21 +825,32 @@ def _one_of(what: str, name: str, value, table: dict) -> int:
     return table[value]
 
 
-def _bf16_rows(what: str, name: str, t: torch.Tensor, rows: int, cols: int):
-    if t.dtype != torch.bfloat16 or not _is_rows(t, cols, rows):
-        raise ValueError(f"{what}: {name} must be bf16 [{rows}, {cols}] with unit column stride")
+def _bf16_rows(what: str, name: str, t: torch.Tensor, rows: int, cols: int) -> int:
+    """The row stride of a bf16 [rows, cols] tensor whose rows are dense."""
+    if t.dtype == torch.bfloat16 and t.shape == (rows, cols):
+        ld, step = t.stride()
+        if step == 1 or cols < 2 or rows == 0:
+            return ld if rows > 1 else max(cols, 1)
+    raise ValueError(f"{what}: {name} must be bf16 [{rows}, {cols}] with unit column stride")
 
 
-def _epilogue(what: str, m: int, n: int, bias, act, mul, residual, pre=None) -> Fp4EpilogueC:
+def _epilogue(what: str, m: int, n: int, bias, act, mul, residual) -> list:
+    """The fields of the C structure, without pre."""
     a = _one_of(what, "act", act, ACT)
-    if bias is not None and (bias.dtype not in DTYPE or not _is_vector(bias, n, bias.dtype)):
-        raise ValueError(f"{what}: bias must be a dense float32 or bfloat16 [{n}]")
-    for t, name in ((mul, "mul"), (residual, "residual")):
-        if t is not None:
-            _bf16_rows(what, name, t, m, n)
-    return Fp4EpilogueC(_ptr(bias), 0 if bias is None else DTYPE[bias.dtype], a, _ptr(mul), 0 if mul is None else _ld(mul),
-                        _ptr(residual), 0 if residual is None else _ld(residual), _ptr(pre),
-                        0 if pre is None else _ld(pre))
+    args = [0, 0, a, 0, 0, 0, 0]
+    if bias is not None:
+        if bias.dtype not in DTYPE or not _is_vector(bias, n, bias.dtype):
+            raise ValueError(f"{what}: bias must be a dense float32 or bfloat16 [{n}]")
+        args[0], args[1] = bias.data_ptr(), DTYPE[bias.dtype]
+    if mul is not None:
+        args[4], args[3] = _bf16_rows(what, "mul", mul, m, n), mul.data_ptr()
+    if residual is not None:
+        args[6], args[5] = _bf16_rows(what, "residual", residual, m, n), residual.data_ptr()
+    return args
+
+
+def _given(*tensors) -> list:
+    return [t for t in tensors if t is not None]
 
 
 def fp4_gemm_epilogue(a: QTensor, b: QTensor, bias: torch.Tensor | None = None, act: str = "none",
@@ -835,19 +863,18 @@ def fp4_gemm_epilogue(a: QTensor, b: QTensor, bias: torch.Tensor | None = None, 
     what = "fp4_gemm_epilogue"
     m, n = a.rows, b.rows
     args = _epilogue(what, m, n, bias, act, mul, residual)
-    dev = _on_device(what, a.q, a.scales, a.tensor_scale, b.q, b.scales, b.tensor_scale,
-                     *(t for t in (bias, mul, residual, out) if t is not None))
-    ta, tb = a.c(), b.c()
+    ld = None if out is None else _bf16_rows(what, "out", out, m, n)
+    dev = _on_device(what, a.q, a.scales, a.tensor_scale, b.q, b.scales, b.tensor_scale, *_given(bias, mul, residual, out))
+    ta, tb, L = a.packed(), b.packed(), lib()
     with _allocating(stream, dev):
         if out is None:
-            out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
-        else:
-            _check_dense_out(out, (m, n), (torch.bfloat16,), what)
+            out, ld = torch.empty((m, n), dtype=torch.bfloat16, device=dev), max(n, 1)
         pre = torch.empty((m, n), dtype=torch.bfloat16, device=dev) if save_pre else None
-        if pre is not None:
-            args.pre, args.ld_pre = _ptr(pre), _ld(pre)
-        st = lib().fp4_gemm_epilogue(ctypes.byref(ta), ctypes.byref(tb), ctypes.byref(args), out.data_ptr(), _ld(out),
-                                     _stream(stream, dev))
+        if m == 0 or n == 0:
+            return out, pre
+        ws = _space(L.fp4_gemm_epilogue_workspace(ta, tb), dev, what)
+        st = L.fp4_gemm_epilogue(ta, tb, _EPILOGUE_ARGS.pack(*args, 0 if pre is None else pre.data_ptr(), n),
+                                 out.data_ptr(), ld, _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream, dev))
     _check(st, what)
     return out, pre
 
@@ -858,19 +885,16 @@ def fp4_wo_gemm_epilogue(x: torch.Tensor, w: QTensor, bias: torch.Tensor | None 
     """fp4_wo_gemm followed by the epilogue of fp4_gemm_epilogue: residual +
     mul act(X W^T + bias) for at most 16 rows."""
     what = "fp4_wo_gemm_epilogue"
-    if x.dtype != torch.bfloat16 or not _is_rows(x, w.cols):
-        raise ValueError(f"{what}: x must be bf16 [rows, {w.cols}] with unit column stride")
     m, n = x.shape[0], w.rows
-    args = _epilogue(what, m, n, bias, act, mul, residual)
-    dev = _on_device(what, x, w.q, w.scales, w.tensor_scale, *(t for t in (bias, mul, residual, out) if t is not None))
-    tw = w.c()
+    ldx = _bf16_rows(what, "x", x, m, w.cols)
+    args = _EPILOGUE_ARGS.pack(*_epilogue(what, m, n, bias, act, mul, residual), 0, 0)
+    ld = max(n, 1) if out is None else _bf16_rows(what, "out", out, m, n)
+    dev = _on_device(what, x, w.q, w.scales, w.tensor_scale, *_given(bias, mul, residual, out))
+    tw = w.packed()
     with _allocating(stream, dev):
         if out is None:
             out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
-        else:
-            _check_dense_out(out, (m, n), (torch.bfloat16,), what)
-        st = lib().fp4_wo_gemm_epilogue(x.data_ptr(), _ld(x), m, ctypes.byref(tw), ctypes.byref(args), out.data_ptr(),
-                                        _ld(out), _stream(stream, dev))
+        st = lib().fp4_wo_gemm_epilogue(x.data_ptr(), ldx, m, tw, args, out.data_ptr(), ld, _stream(stream, dev))
     _check(st, what)
     return out
 
@@ -897,10 +921,9 @@ def fp4_epilogue_backward(dy: torch.Tensor, pre: torch.Tensor | None, act: str =
     reads = a != 0 or mul is not None
     if reads and pre is None:
         raise ValueError(f"{what}: pre is needed with an activation or mul")
-    for t, name in ((pre if reads else None, "pre"), (mul, "mul")):
-        if t is not None:
-            _bf16_rows(what, name, t, m, n)
-    dev = _on_device(what, dy, *(t for t in (pre if reads else None, mul) if t is not None))
+    ld_pre = _bf16_rows(what, "pre", pre, m, n) if reads else 0
+    ld_mul = 0 if mul is None else _bf16_rows(what, "mul", mul, m, n)
+    dev = _on_device(what, dy, *_given(pre if reads else None, mul))
     if n == 0:
         return EpilogueGrads(_empty_as(dy), torch.empty(0, dtype=torch.float32, device=dev) if bias else None,
                              None if mul is None else _empty_as(mul))
@@ -910,9 +933,8 @@ def fp4_epilogue_backward(dy: torch.Tensor, pre: torch.Tensor | None, act: str =
         dmul = _empty_as(mul) if mul is not None else None
         dbias = torch.empty(n, dtype=torch.float32, device=dev) if bias else None
         ws = _space(L.fp4_epilogue_workspace(m, n), dev, what) if bias else None
-        st = L.fp4_epilogue_backward(dy.data_ptr(), _ld(dy), _ptr(pre) if reads else None, _ld(pre) if reads else 0, _ptr(mul),
-                                     0 if mul is None else _ld(mul), m, n, a, _ptr(dpre), n, _ptr(dmul), n, _ptr(dbias),
-                                     _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream, dev))
+        st = L.fp4_epilogue_backward(dy.data_ptr(), _ld(dy), _ptr(pre) if reads else None, ld_pre, _ptr(mul), ld_mul, m, n, a, _ptr(dpre),
+                                     n, _ptr(dmul), n, _ptr(dbias), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream, dev))
     _check(st, what)
     return EpilogueGrads(dy if dpre is None else dpre, dbias, dmul)
 
@@ -959,15 +981,16 @@ class MoeBank:
              self.down.tensor_scale]
         return t + [s for s in (self.up_scale, self.down_scale) if s is not None]
 
-    def c(self) -> Fp4MoeBankC:
+    def packed(self) -> bytes:
+        """The C structure as bytes."""
         e, h, f = self.experts, self.gate_up.cols, self.down.cols
         if e < 1 or self.gate_up.rows != e * 2 * f or self.down.rows != e * h:
             raise ValueError("MoeBank: gate_up is [experts * 2 F, H], down is [experts * H, F]")
         for s in (self.up_scale, self.down_scale):
             if s is not None and not _is_vector(s, e, torch.float32):
                 raise ValueError(f"MoeBank: scales must be float32 [{e}]")
-        return Fp4MoeBankC(ctypes.pointer(self.gate_up.c()), ctypes.pointer(self.down.c()), _ptr(self.up_scale),
-                           _ptr(self.down_scale), e)
+        return self.gate_up.packed() + self.down.packed() + _MOE_ARGS.pack(_ptr(self.up_scale) or 0,
+                                                                           _ptr(self.down_scale) or 0, e)
 
 
 def fp4_moe(x: torch.Tensor, bank: MoeBank, ids: torch.Tensor, weights: torch.Tensor, act: str = "silu",
@@ -978,27 +1001,22 @@ def fp4_moe(x: torch.Tensor, bank: MoeBank, ids: torch.Tensor, weights: torch.Te
     bank: none).  out may be residual or x."""
     what = "fp4_moe"
     a = _one_of(what, "act", act, ACT)
-    tb = bank.c()
-    h, f = bank.gate_up.cols, bank.down.cols
-    if x.dtype != torch.bfloat16 or not _is_rows(x, h):
-        raise ValueError(f"{what}: x must be bf16 [tokens, {h}] with unit column stride")
-    m = x.shape[0]
+    tb = bank.packed()
+    h, f, m = bank.gate_up.cols, bank.down.cols, x.shape[0]
+    ldx = _bf16_rows(what, "x", x, m, h)
     if ids.dim() != 2 or ids.dtype != torch.int32 or ids.shape[0] != m or not ids.is_contiguous() \
             or weights.dtype != torch.float32 or weights.shape != ids.shape or not weights.is_contiguous():
         raise ValueError(f"{what}: ids must be int32 and weights float32, both dense [{m}, top]")
-    if residual is not None:
-        _bf16_rows(what, "residual", residual, m, h)
-    dev = _on_device(what, x, ids, weights, *bank.tensors(), *(t for t in (residual, out) if t is not None))
+    ld_res = 0 if residual is None else _bf16_rows(what, "residual", residual, m, h)
+    ld = h if out is None else _bf16_rows(what, "out", out, m, h)
+    dev = _on_device(what, x, ids, weights, *bank.tensors(), *_given(residual, out))
     top, L = ids.shape[1], lib()
     with _allocating(stream, dev):
         if out is None:
             out = torch.empty((m, h), dtype=torch.bfloat16, device=dev)
-        else:
-            _check_dense_out(out, (m, h), (torch.bfloat16,), what)
         ws = _space(L.fp4_moe_workspace(m, top, f), dev, what)
-        st = L.fp4_moe(x.data_ptr(), _ld(x), m, ctypes.byref(tb), ids.data_ptr(), weights.data_ptr(), top, a,
-                       _ptr(residual), 0 if residual is None else _ld(residual), out.data_ptr(), _ld(out), _ptr(ws),
-                       0 if ws is None else ws.numel(), _stream(stream, dev))
+        st = L.fp4_moe(x.data_ptr(), ldx, m, tb, ids.data_ptr(), weights.data_ptr(), top, a, _ptr(residual), ld_res,
+                       out.data_ptr(), ld, _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream, dev))
     _check(st, what)
     return out
 

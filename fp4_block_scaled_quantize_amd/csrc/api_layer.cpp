@@ -14,15 +14,13 @@ using namespace fp4;
 
 namespace {
 
-// Rows [m, cols] of bf16 at any element; *vec: whether they are 16-byte vectors too.
-fp4_status check_plain_rows(const void* p, int64_t ld, int64_t m, int64_t cols, int32_t* vec)
+// Rows [m, cols] of bf16 at any element.
+fp4_status check_plain_rows(const void* p, int64_t ld, int64_t m, int64_t cols)
 {
     if (!p) return m && cols ? FP4_ERR_INVALID_ARG : FP4_OK;
     if (ld < cols) return FP4_ERR_SHAPE;
     if (ld > kMaxElems / (m ? m : 1)) return FP4_ERR_UNSUPPORTED;
-    if (!aligned(p, 2)) return FP4_ERR_ALIGN;
-    if (!aligned(p, 16) || (m > 1 && ld % 8)) *vec = 0;
-    return FP4_OK;
+    return aligned(p, 2) ? FP4_OK : FP4_ERR_ALIGN;
 }
 
 bool act_ok(int32_t a) { return a >= FP4_ACT_NONE && a <= FP4_ACT_GELU_TANH; }
@@ -32,12 +30,11 @@ fp4_status check_epilogue(const fp4_epilogue* e, const uint16_t* y, int64_t ldy,
     if (!e || !act_ok(e->act)) return FP4_ERR_INVALID_ARG;
     if (e->bias && !dtype_ok(e->bias_dtype)) return FP4_ERR_INVALID_ARG;
     if (e->pre && (e->pre == y || e->pre == e->mul || e->pre == e->residual)) return FP4_ERR_INVALID_ARG;
-    int32_t vec = 1;
-    fp4_status st = check_plain_rows(y, ldy, m, n, &vec);
+    fp4_status st = check_plain_rows(y, ldy, m, n);
     if (st != FP4_OK) return st;
-    if (e->mul && (st = check_plain_rows(e->mul, e->ld_mul, m, n, &vec)) != FP4_OK) return st;
-    if (e->residual && (st = check_plain_rows(e->residual, e->ld_residual, m, n, &vec)) != FP4_OK) return st;
-    if (e->pre && (st = check_plain_rows(e->pre, e->ld_pre, m, n, &vec)) != FP4_OK) return st;
+    if (e->mul && (st = check_plain_rows(e->mul, e->ld_mul, m, n)) != FP4_OK) return st;
+    if (e->residual && (st = check_plain_rows(e->residual, e->ld_residual, m, n)) != FP4_OK) return st;
+    if (e->pre && (st = check_plain_rows(e->pre, e->ld_pre, m, n)) != FP4_OK) return st;
     // in place means the same rows: another stride would let one row's output
     // overwrite another's input
     if ((e->mul == y && e->ld_mul != ldy) || (e->residual == y && e->ld_residual != ldy)) return FP4_ERR_SHAPE;
@@ -48,7 +45,6 @@ fp4_status check_epilogue(const fp4_epilogue* e, const uint16_t* y, int64_t ldy,
     out->mul = e->mul; out->ld_mul = e->ld_mul;
     out->res = e->residual; out->ld_res = e->ld_residual;
     out->pre = e->pre; out->ld_pre = e->ld_pre;
-    out->vec = vec;
     return FP4_OK;
 }
 
@@ -90,8 +86,18 @@ fp4_status check_distill(const void* z, int32_t dtype, int64_t ld, int64_t rows,
 
 extern "C" {
 
+int64_t fp4_gemm_epilogue_workspace(const fp4_tensor* a, const fp4_tensor* b)
+{
+    GemmEpiLaunch p{};
+    uint16_t* const any = reinterpret_cast<uint16_t*>(uintptr_t(16));     // y takes no part in it
+    const fp4_status st = check_gemm(a, b, any, b ? b->rows : 0, &p);
+    if (st != FP4_OK) return st;
+    if (a->rows == 0 || b->rows == 0 || a->cols == 0) return 0;
+    return epi::gemm_split(&p);
+}
+
 fp4_status fp4_gemm_epilogue(const fp4_tensor* a, const fp4_tensor* b, const fp4_epilogue* e, uint16_t* y, int64_t ldy,
-                             void* stream)
+                             void* workspace, int64_t workspace_bytes, void* stream)
 {
     GemmEpiLaunch p{};
     fp4_status st = check_gemm(a, b, y, ldy, &p);
@@ -99,12 +105,15 @@ fp4_status fp4_gemm_epilogue(const fp4_tensor* a, const fp4_tensor* b, const fp4
     if (a->cols == 0) return FP4_ERR_SHAPE;
     if ((st = check_epilogue(e, y, ldy, a->rows, b->rows, &p.ep)) != FP4_OK) return st;
     if (a->rows == 0 || b->rows == 0) return FP4_OK;
+    const bool mx = gemm_is_mx(p), mx16 = !mx && gemm_mx16_supported(p);
+    if (!mx && !mx16 && !gemm_dq_supported(p.fa, p.fb, p.elem)) return FP4_ERR_UNSUPPORTED;
+    if ((st = check_space(workspace, workspace_bytes, epi::gemm_split(&p))) != FP4_OK) return st;
+    p.part = (float*)workspace;
     hipStream_t s = (hipStream_t)stream;
     if (gemm_small_supported(p)) return hip_status(epi::launch_gemm_small(p, s));
-    if (gemm_is_mx(p)) return hip_status(epi::launch_gemm_mx(p, s));
-    if (gemm_mx16_supported(p)) return hip_status(epi::launch_gemm_mx16(p, s));
-    if (!gemm_dq_supported(p.fa, p.fb, p.elem)) return FP4_ERR_UNSUPPORTED;
-    return hip_status(epi::launch_gemm_dq(p, s));
+    st = hip_status(mx ? epi::launch_gemm_mx(p, s) : mx16 ? epi::launch_gemm_mx16(p, s) : epi::launch_gemm_dq(p, s));
+    if (st != FP4_OK || p.splits == 1) return st;
+    return hip_status(launch_epilogue_join(p, s));
 }
 
 fp4_status fp4_wo_gemm_epilogue(const uint16_t* x, int64_t ldx, int64_t m, const fp4_tensor* w, const fp4_epilogue* e,
@@ -134,17 +143,16 @@ fp4_status fp4_epilogue_backward(const uint16_t* dy, int64_t ld_dy, const uint16
     if (!act_ok(act)) return FP4_ERR_INVALID_ARG;
     const int64_t need = fp4_epilogue_workspace(rows, cols);
     if (need < 0) return (fp4_status)need;
-    int32_t vec = 1;
-    fp4_status st = check_plain_rows(dy, ld_dy, rows, cols, &vec);
+    fp4_status st = check_plain_rows(dy, ld_dy, rows, cols);
     if (st != FP4_OK) return st;
     const bool reads = act != FP4_ACT_NONE || mul;
     // without either the gradient of v is dy itself, and only the bias's sum is left to do
     if (rows && reads && (!dpre || !pre)) return FP4_ERR_INVALID_ARG;
     if (rows && mul && !dmul) return FP4_ERR_INVALID_ARG;
-    if (reads && (st = check_plain_rows(pre, ld_pre, rows, cols, &vec)) != FP4_OK) return st;
-    if (mul && (st = check_plain_rows(mul, ld_mul, rows, cols, &vec)) != FP4_OK) return st;
-    if (dpre && (st = check_plain_rows(dpre, ld_dpre, rows, cols, &vec)) != FP4_OK) return st;
-    if (mul && (st = check_plain_rows(dmul, ld_dmul, rows, cols, &vec)) != FP4_OK) return st;
+    if (reads && (st = check_plain_rows(pre, ld_pre, rows, cols)) != FP4_OK) return st;
+    if (mul && (st = check_plain_rows(mul, ld_mul, rows, cols)) != FP4_OK) return st;
+    if (dpre && (st = check_plain_rows(dpre, ld_dpre, rows, cols)) != FP4_OK) return st;
+    if (mul && (st = check_plain_rows(dmul, ld_dmul, rows, cols)) != FP4_OK) return st;
     if (rows && mul && dpre == dmul) return FP4_ERR_INVALID_ARG;
     const struct { const uint16_t* p; int64_t ld; } in[3] = {{dy, ld_dy}, {reads ? pre : nullptr, ld_pre}, {mul, ld_mul}};
     for (const auto& i : in)
@@ -154,7 +162,7 @@ fp4_status fp4_epilogue_backward(const uint16_t* dy, int64_t ld_dy, const uint16
     if (!dbias && (rows == 0 || (!dpre && !mul))) return FP4_OK;
     EpiGradLaunch p{};
     p.dy = dy; p.lddy = ld_dy; p.pre = pre; p.ldpre = ld_pre; p.mul = mul; p.ldmul = ld_mul;
-    p.rows = rows; p.cols = cols; p.act = act; p.vec = vec;
+    p.rows = rows; p.cols = cols; p.act = act;
     p.dpre = dpre; p.lddpre = ld_dpre; p.dmul = mul ? dmul : nullptr; p.lddmul = ld_dmul;
     p.dbias = dbias;
     p.part = (float*)workspace;
@@ -198,15 +206,15 @@ fp4_status fp4_moe(const uint16_t* x, int64_t ldx, int64_t m, const fp4_moe_bank
 {
     MoeLaunch p{};
     if (!bank) return FP4_ERR_INVALID_ARG;
-    fp4_status st = check_tensor(bank->gate_up, &p.up.fmt);
+    fp4_status st = check_tensor(&bank->gate_up, &p.up.fmt);
     if (st != FP4_OK) return st;
-    if ((st = check_tensor(bank->down, &p.down.fmt)) != FP4_OK) return st;
+    if ((st = check_tensor(&bank->down, &p.down.fmt)) != FP4_OK) return st;
     if (!act_ok(act) || !x || !y || !ids || !weights) return FP4_ERR_INVALID_ARG;
     if (m < 1 || m > kMoeMaxTokens || top > kMoeMaxTop || bank->experts > kMaxExperts) return FP4_ERR_UNSUPPORTED;
-    const int64_t hidden = bank->gate_up->cols, ffn = bank->down->cols, experts = bank->experts;
+    const int64_t hidden = bank->gate_up.cols, ffn = bank->down.cols, experts = bank->experts;
     if (top < 1 || experts < 1 || hidden < 1 || ffn < 1) return FP4_ERR_SHAPE;
-    if ((st = check_experts(bank->gate_up, bank->up_scale, experts, 2 * ffn, &p.up)) != FP4_OK) return st;
-    if ((st = check_experts(bank->down, bank->down_scale, experts, hidden, &p.down)) != FP4_OK) return st;
+    if ((st = check_experts(&bank->gate_up, bank->up_scale, experts, 2 * ffn, &p.up)) != FP4_OK) return st;
+    if ((st = check_experts(&bank->down, bank->down_scale, experts, hidden, &p.down)) != FP4_OK) return st;
     if (ldx < hidden || ldy < hidden || (residual && ld_residual < hidden)) return FP4_ERR_SHAPE;
     if (ldx > kMaxElems / m || ldy > kMaxElems / m || (residual && ld_residual > kMaxElems / m)) return FP4_ERR_UNSUPPORTED;
     if (residual == y && ld_residual != ldy) return FP4_ERR_SHAPE;

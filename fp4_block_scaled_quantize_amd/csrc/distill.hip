@@ -26,7 +26,6 @@ namespace fp4 {
 
 constexpr double kLn2d = 0.693147180559945309417;
 constexpr int kDsThreads = 256;
-constexpr int kDsPiece = 16384;        // elements of a backward piece at most
 
 // Tokens of the list inside the vocabulary; a token listed again keeps both
 // probabilities and counts once among the student's.
@@ -302,9 +301,8 @@ __global__ __launch_bounds__(kDsThreads) void k_distill_backward(DistillGradLaun
     using L = Logit<BF16>;
     using T = typename L::Raw;
     constexpr int VN = L::N;
-    __shared__ uint32_t bits[kDsPiece / 32 + 1];          // a vector's bits may end in the next word
     __shared__ int32_t ids[kDistillMaxTop];
-    __shared__ float prob[kDistillMaxTop];
+    __shared__ float prob[kDistillMaxTop], share[kDistillMaxTop];
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     const T* const z = (const T*)p.logits + row * p.ld;
@@ -319,88 +317,85 @@ __global__ __launch_bounds__(kDsThreads) void k_distill_backward(DistillGradLaun
     // large coefficient would make visible.
     const float k = 0.5f * c * kLog2e;
     const float ml = st[0], mu = st[2], gl = g * cl * st[1], gu = g * cu * st[3];
-    auto grad = [&](float x, bool listed, float p) {
-        const float h = __builtin_amdgcn_exp2f((x - (listed ? ml : mu)) * k);
-        return c * __builtin_fmaf(h, h * (listed ? gl : gu), -p);     // c last: it must not overflow against q = 0
+    auto other = [&](float x) {
+        const float h = __builtin_amdgcn_exp2f((x - mu) * k);
+        return c * (h * (h * gu));                        // c last: it must not overflow against q = 0
     };
     // elements that are vectors of both rows
     const int64_t head = (int64_t)((16 - ((uintptr_t)(z + b) & 15)) & 15) / (int64_t)sizeof(T);
     const bool same = (((uintptr_t)(z + b) ^ (uintptr_t)(dz + b)) & 15) == 0;
     const int64_t vb = !same ? e : b + head < e ? b + head : e;
     const int64_t nvec = (e - vb) / VN, ve = vb + nvec * VN;
-    if (!none) {
-        for (int j = tid; j < p.top; j += kDsThreads) {
-            const int32_t id = p.ids[row * p.top + j];
-            ids[j] = id;
-            prob[j] = g * (float)exp((double)p.logprobs[row * p.top + j] - (double)logmass);
-        }
-        mark_listed(bits, (int)((e - b + 31) / 32), p.ids + row * p.top, p.top, b, e, tid, kDsThreads);
-    }
-    // p of the VN elements from `from` on, those that the list names
-    auto listed_probs = [&](int64_t from, auto& p_of) {
-        constexpr int N = sizeof(p_of) / sizeof(float);
-#pragma unroll
-        for (int j = 0; j < N; ++j) p_of[j] = 0.0f;
-        for (int i = 0; i < p.top; ++i) {
-            const int64_t at = (int64_t)ids[i] - from;
-            const float one = prob[i];
-#pragma unroll
-            for (int j = 0; j < N; ++j) p_of[j] += at == j ? one : 0.0f;
-        }
-    };
-    auto put = [&](int64_t i) {
-        float d = 0.0f;
-        if (!none) {
-            const bool listed = bits[(i - b) >> 5] >> ((i - b) & 31) & 1u;
-            float one[1] = {0.0f};
-            if (listed) listed_probs(i, one);
-            d = grad(L::one(z + i), listed, one[0]);
-        }
-        if constexpr (BF16) dz[i] = (uint16_t)f32_to_bf16_rne(d);
-        else dz[i] = d;
-    };
     const v4i* const zv = reinterpret_cast<const v4i*>(z + vb);
     v4i* const dv = reinterpret_cast<v4i*>(dz + vb);
-    const int sh = (int)(vb - b) & 31, word0 = (int)(vb - b) >> 5;   // the vectors' first bit
-    for (int64_t r0 = 0; r0 < nvec; r0 += kDsThreads * kLpVec) {
-        v4i raw[kLpVec];
+    v4i raw[kLpVec];
+    auto fetch = [&](int64_t r0) {
 #pragma unroll
         for (int u = 0; u < kLpVec; ++u) {
             const int64_t i = r0 + kDsThreads * u + tid;
             if (i < nvec && !none) raw[u] = zv[i];
         }
+    };
+    fetch(0);
+    // The listed tokens of this piece, whose logits are read before anything
+    // is written: every element is first written as one of the others, and
+    // theirs once more at the end, a token a thread.  (Looking for them among
+    // the elements instead cost a third of the kernel's time: with 32 of 32000
+    // listed every other wave's vectors hold one.)
+    int32_t mine = -1;
+    if (!none && tid < p.top) {
+        const int32_t id = p.ids[row * p.top + tid];
+        const bool in = id >= b && id < e;
+        mine = in ? id : -1;
+        ids[tid] = mine;
+        if (in) {
+            const float h = __builtin_amdgcn_exp2f((L::one(z + id) - ml) * k);
+            share[tid] = h * (h * gl);
+            prob[tid] = g * (float)exp((double)p.logprobs[row * p.top + tid] - (double)logmass);
+        }
+    }
+    __syncthreads();
+    auto put = [&](int64_t i) {
+        const float d = none ? 0.0f : other(L::one(z + i));
+        if constexpr (BF16) dz[i] = (uint16_t)f32_to_bf16_rne(d);
+        else dz[i] = d;
+    };
+    for (int64_t r0 = 0; r0 < nvec; r0 += kDsThreads * kLpVec) {
+        v4i out[kLpVec];
+#pragma unroll
+        for (int u = 0; u < kLpVec; ++u) {
+            if (none) {
+                out[u] = v4i{0, 0, 0, 0};
+                continue;
+            }
+            float f[VN];
+            L::unpack(raw[u], f);
+#pragma unroll
+            for (int j = 0; j < VN; ++j) f[j] = other(f[j]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (BF16) out[u][q] = (int)pack_bf16(f[2 * q], f[2 * q + 1]);
+                else out[u][q] = (int)f_bits(f[q]);
+            }
+        }
+        fetch(r0 + kDsThreads * kLpVec);
 #pragma unroll
         for (int u = 0; u < kLpVec; ++u) {
             const int64_t i = r0 + kDsThreads * u + tid;
-            if (i >= nvec) continue;
-            v4i out{0, 0, 0, 0};
-            if (!none) {
-                float f[VN];
-                L::unpack(raw[u], f);
-                // the vector's VN bits, which may cross a word
-                const int at = sh + (int)i * VN, w = word0 + (at >> 5);
-                const uint64_t two = (uint64_t)bits[w] | ((uint64_t)bits[w + 1] << 32);
-                const uint32_t mark = (uint32_t)(two >> (at & 31)) & ((1u << VN) - 1);
-                if (mark == 0) {
-#pragma unroll
-                    for (int j = 0; j < VN; ++j) f[j] = grad(f[j], false, 0.0f);
-                } else {
-                    float p_of[VN];
-                    listed_probs(vb + i * VN, p_of);
-#pragma unroll
-                    for (int j = 0; j < VN; ++j) f[j] = grad(f[j], mark >> j & 1u, p_of[j]);
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if constexpr (BF16) out[q] = (int)pack_bf16(f[2 * q], f[2 * q + 1]);
-                    else out[q] = (int)f_bits(f[q]);
-                }
-            }
-            __builtin_nontemporal_store(out, dv + i);     // read next long after it has left the caches
+            if (i < nvec) __builtin_nontemporal_store(out[u], dv + i);   // read next long after it has left the caches
         }
     }
     for (int64_t i = b + tid; i < vb; i += kDsThreads) put(i);
     for (int64_t i = ve + tid; i < e; i += kDsThreads) put(i);
+    // every thread's stores have arrived before one of them is written again
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (mine < 0) return;
+    float pm = 0.0f;                                       // a token may be listed twice
+    for (int i = 0; i < p.top; ++i) pm += ids[i] == mine ? prob[i] : 0.0f;
+    const float d = c * (share[tid] - pm);
+    if constexpr (BF16) dz[mine] = (uint16_t)f32_to_bf16_rne(d);
+    else dz[mine] = d;
 }
 
 // ---------------------------------------------------------------------------
@@ -442,7 +437,7 @@ hipError_t launch_distill_backward(const DistillGradLaunch& in, hipStream_t s)
     DistillGradLaunch p = in;
     // two rounds of a workgroup's threads: 16384 bf16 or 8192 binary32 elements
     p.piece = 2 * kDsThreads * kLpVec * (p.bf16 ? 8 : 4);
-    static_assert(2 * kDsThreads * kLpVec * 8 <= kDsPiece, "the piece's bitmap");
+    static_assert(kDistillMaxTop <= kDsThreads, "a thread for each listed token");
     const dim3 grid((unsigned)p.rows, (unsigned)cdiv(p.vocab, p.piece));
     if (p.bf16) hipLaunchKernelGGL((k_distill_backward<true>), grid, dim3(kDsThreads), 0, s, p);
     else hipLaunchKernelGGL((k_distill_backward<false>), grid, dim3(kDsThreads), 0, s, p);

@@ -17,53 +17,54 @@
 
 namespace fp4 {
 
-constexpr int kEgThreads = 256;
-constexpr int kEgCols = 256;           // columns of a workgroup: 32 threads of eight
-constexpr int kEgRows = kEgThreads / (kEgCols / 8);
-
-template <int ACT>
-__global__ __launch_bounds__(kEgThreads) void k_epilogue_backward(EpiGradLaunch p, int64_t step)
+// COLS columns of a workgroup, eight a thread.
+template <int ACT, int COLS, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_epilogue_backward(EpiGradLaunch p, int64_t step)
 {
-    __shared__ float sums[kEgRows][kEgCols];
-    const int tid = threadIdx.x, cb = tid % (kEgCols / 8), r0 = tid / (kEgCols / 8);
-    const int64_t n = (int64_t)blockIdx.x * kEgCols + 8 * cb;
+    constexpr int CB = COLS / 8, ROWS = THREADS / CB;
+    __shared__ float sums[ROWS][COLS + 1];
+    const int tid = threadIdx.x, cb = tid % CB, r0 = tid / CB;
+    const int64_t n = (int64_t)blockIdx.x * COLS + 8 * cb;
     const int64_t b = (int64_t)blockIdx.y * step, e = b + step < p.rows ? b + step : p.rows;
-    const bool full = p.vec && n + 8 <= p.cols;
     const int have = n >= p.cols ? 0 : p.cols - n < 8 ? (int)(p.cols - n) : 8;
     float total[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) total[i] = 0.0f;
     if (have) {
 #pragma unroll 2
-        for (int64_t m = b + r0; m < e; m += kEgRows) {
+        for (int64_t m = b + r0; m < e; m += ROWS) {
             float dy[8], v[8], mul[8], d[8];
-            bf16_load<8>(p.dy + m * p.lddy + n, full, have, dy);
-            if (ACT != kActNone || p.mul) bf16_load<8>(p.pre + m * p.ldpre + n, full, have, v);
-            if (p.mul) bf16_load<8>(p.mul + m * p.ldmul + n, full, have, mul);
+            bf16_load<8>(p.dy + m * p.lddy + n, have, dy);
+            if (ACT != kActNone || p.mul) bf16_load<8>(p.pre + m * p.ldpre + n, have, v);
+            if (p.mul) bf16_load<8>(p.mul + m * p.ldmul + n, have, mul);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 d[i] = dy[i];
                 if (p.mul) d[i] *= mul[i];
                 if (ACT != kActNone) d[i] *= act_slope<ACT>(v[i]);
-                if (i < have) total[i] += d[i];
+                total[i] += d[i];                          // elements past the last are zeros
             }
             if (p.mul) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = dy[i] * act_value<ACT>(v[i]);
-                bf16_store<8>(p.dmul + m * p.lddmul + n, full, have, v);
+                bf16_store<8>(p.dmul + m * p.lddmul + n, have, v);
             }
-            if (p.dpre) bf16_store<8>(p.dpre + m * p.lddpre + n, full, have, d);
+            if (p.dpre) bf16_store<8>(p.dpre + m * p.lddpre + n, have, d);
         }
     }
     if (!p.dbias) return;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sums[r0][8 * cb + i] = total[i];
     __syncthreads();
-    const int64_t col = (int64_t)blockIdx.x * kEgCols + tid;
-    if (col >= p.cols) return;
-    float s = 0.0f;
+    // rows in halves: always the same order
 #pragma unroll
-    for (int r = 0; r < kEgRows; ++r) s += sums[r][tid];
+    for (int h = ROWS / 2; h >= 4; h /= 2) {
+        for (int i = tid; i < h * COLS; i += THREADS) sums[i / COLS][i % COLS] += sums[i / COLS + h][i % COLS];
+        __syncthreads();
+    }
+    const int64_t col = (int64_t)blockIdx.x * COLS + tid;
+    if (tid >= COLS || col >= p.cols) return;
+    const float s = (sums[0][tid] + sums[1][tid]) + (sums[2][tid] + sums[3][tid]);
     (gridDim.y == 1 ? p.dbias : p.part + (int64_t)blockIdx.y * p.cols)[col] = s;
 }
 
@@ -78,22 +79,58 @@ __global__ __launch_bounds__(256) void k_epilogue_join(const float* __restrict__
     out[col] = s;
 }
 
+// The K ranges' partial sums of a product, joined in order, then its epilogue.
+__global__ __launch_bounds__(256) void k_epilogue_product(GemmEpiLaunch p)
+{
+    const int64_t eights = p.ldp / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= p.m * eights) return;
+    const int64_t m = i / eights, n = 8 * (i % eights);
+    const int64_t from = m * p.ldp + n, step = p.m * p.ldp;
+    float sum[8], bias[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        sum[j] = 0.0f;
+        bias[j] = p.ep.bias && n + j < p.n ? epi_bias(p.ep, n + j) : 0.0f;
+    }
+#pragma unroll 4
+    for (int64_t s = 0; s < p.splits; ++s) {
+        const float4* const q = reinterpret_cast<const float4*>(p.part + s * step + from);
+        const float4 a = q[0], b = q[1];
+        sum[0] += a.x; sum[1] += a.y; sum[2] += a.z; sum[3] += a.w;
+        sum[4] += b.x; sum[5] += b.y; sum[6] += b.z; sum[7] += b.w;
+    }
+    epi_put<8>(p.ep, p.c, p.ldc, m, n, p.n, sum, bias);
+}
+
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Row ranges: about 2048 workgroups, none with fewer than 32 rows.
+hipError_t launch_epilogue_join(const GemmEpiLaunch& p, hipStream_t s)
+{
+    hipLaunchKernelGGL(k_epilogue_product, dim3((unsigned)cdiv(p.m * (p.ldp / 8), 256)), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+// Few rows take one launch, with workgroups of 64 columns over all of them;
+// more are cut into ranges, about 2048 workgroups of 256 columns, whose sums a
+// second launch joins.
+constexpr int64_t kEgFewRows = 1024;
+constexpr int kEgCols = 256, kEgFewCols = 64;
 int64_t epilogue_groups(int64_t rows, int64_t cols)
 {
-    const int64_t blocks = cdiv(cols, kEgCols);
-    int64_t g = cdiv(2048, blocks), most = cdiv(rows, 32);
-    g = g < most ? g : most;
-    return g < 1 ? 1 : g;
+    if (rows <= kEgFewRows) return 1;
+    const int64_t g = cdiv(2048, cdiv(cols, kEgCols)), most = cdiv(rows, 32);
+    return g < most ? g : most;
 }
 
 template <int ACT>
 static void run(const EpiGradLaunch& p, int64_t step, hipStream_t s)
 {
-    const dim3 grid((unsigned)cdiv(p.cols, kEgCols), (unsigned)p.groups);
-    hipLaunchKernelGGL((k_epilogue_backward<ACT>), grid, dim3(kEgThreads), 0, s, p, step);
+    if (p.rows <= kEgFewRows)
+        hipLaunchKernelGGL((k_epilogue_backward<ACT, kEgFewCols, 1024>), dim3((unsigned)cdiv(p.cols, kEgFewCols)), dim3(1024), 0, s,
+                           p, step);
+    else
+        hipLaunchKernelGGL((k_epilogue_backward<ACT, kEgCols, 256>), dim3((unsigned)cdiv(p.cols, kEgCols), (unsigned)p.groups),
+                           dim3(256), 0, s, p, step);
 }
 
 hipError_t launch_epilogue_backward(const EpiGradLaunch& in, hipStream_t s)

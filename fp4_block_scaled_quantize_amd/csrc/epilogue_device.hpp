@@ -80,36 +80,34 @@ __device__ __forceinline__ void with_act(int act, F f)
     }
 }
 
-// W (1, 4 or 8) neighbouring bf16 elements, `full` as one load or store, else
-// the first `n`.
+// W (1, 4 or 8) neighbouring bf16 elements: all of them in one load or store
+// at whatever element they start (global memory takes wide accesses at any
+// alignment here, at no cost to aligned ones), or the first n.
+typedef uint32_t u4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
 template <int W>
-__device__ __forceinline__ void bf16_load(const uint16_t* p, bool full, int n, float (&o)[W])
+using epi_vec = typename std::conditional<W == 8, u4_any, u2_any>::type;
+
+template <int W>
+__device__ __forceinline__ void bf16_load(const uint16_t* p, int n, float (&o)[W])
 {
-    if (W > 1 && full) {
-        uint32_t d[W / 2 ? W / 2 : 1];
-        if constexpr (W == 8) {
-            const uint4 v = *reinterpret_cast<const uint4*>(p);
-            d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
-        } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(p);
-            d[0] = v.x; d[1] = v.y;
-        }
+    if (W > 1 && n >= W) {
+        const epi_vec<W> v = *reinterpret_cast<const epi_vec<W>*>(p);
 #pragma unroll
-        for (int i = 0; i < W / 2; ++i) { o[2 * i] = bf16_lo(d[i]); o[2 * i + 1] = bf16_hi(d[i]); }
+        for (int i = 0; i < W / 2; ++i) { o[2 * i] = bf16_lo(v[i]); o[2 * i + 1] = bf16_hi(v[i]); }
     } else {
 #pragma unroll
         for (int i = 0; i < W; ++i) o[i] = i < n ? bf16_lo(p[i]) : 0.0f;
     }
 }
 template <int W>
-__device__ __forceinline__ void bf16_store(uint16_t* p, bool full, int n, const float (&v)[W])
+__device__ __forceinline__ void bf16_store(uint16_t* p, int n, const float (&v)[W])
 {
-    if (W > 1 && full) {
-        if constexpr (W == 8)
-            *reinterpret_cast<uint4*>(p) = uint4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                                 pack_bf16(v[6], v[7])};
-        else
-            *reinterpret_cast<uint2*>(p) = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    if (W > 1 && n >= W) {
+        epi_vec<W> o;
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<epi_vec<W>*>(p) = o;
     } else {
 #pragma unroll
         for (int i = 0; i < W; ++i)
@@ -128,14 +126,13 @@ template <int W>
 __device__ __forceinline__ void epi_put(const Epilogue& e, uint16_t* c, int64_t ldc, int64_t m, int64_t n, int64_t N,
                                         const float (&sum)[W], const float (&bias)[W])
 {
-    const bool full = e.vec && n + W <= N;
     const int have = N - n < W ? (int)(N - n) : W;
     float v[W], mul[W], res[W];
-    if (e.mul) bf16_load<W>(e.mul + m * e.ld_mul + n, full, have, mul);
-    if (e.res) bf16_load<W>(e.res + m * e.ld_res + n, full, have, res);
+    if (e.mul) bf16_load<W>(e.mul + m * e.ld_mul + n, have, mul);
+    if (e.res) bf16_load<W>(e.res + m * e.ld_res + n, have, res);
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = sum[i] + bias[i];
-    if (e.pre) bf16_store<W>(e.pre + m * e.ld_pre + n, full, have, v);
+    if (e.pre) bf16_store<W>(e.pre + m * e.ld_pre + n, have, v);
     with_act(e.act, [&](auto act) {
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] = act_value<decltype(act)::value>(v[i]);
@@ -146,7 +143,7 @@ __device__ __forceinline__ void epi_put(const Epilogue& e, uint16_t* c, int64_t 
     if (e.res)
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] += res[i];
-    bf16_store<W>(c + m * ldc + n, full, have, v);
+    bf16_store<W>(c + m * ldc + n, have, v);
 }
 
 }  // namespace fp4

@@ -153,11 +153,19 @@ struct Epilogue {
     const uint16_t* mul; int64_t ld_mul;
     const uint16_t* res; int64_t ld_res;
     uint16_t* pre; int64_t ld_pre;                        // out: v
-    int32_t vec;               // rows of y, mul, res and pre are 16-byte aligned
 };
-struct GemmEpiLaunch : GemmLaunch { Epilogue ep; };
+// K in `splits` ranges of kstep; more than one: their products as partial sums
+// [splits, m, ldp] in binary32, joined before the epilogue
+struct GemmEpiLaunch : GemmLaunch {
+    Epilogue ep;
+    int64_t splits, kstep, ldp;
+    float* part;
+};
 struct WoEpiLaunch : WoGemmLaunch { Epilogue ep; };
+hipError_t launch_epilogue_join(const GemmEpiLaunch& p, hipStream_t s);
 namespace epi {
+// Fills in splits, kstep and ldp; returns the bytes of the partial sums.
+int64_t gemm_split(GemmEpiLaunch* p);
 hipError_t launch_gemm_mx(const GemmEpiLaunch& p, hipStream_t s);
 hipError_t launch_gemm_mx16(const GemmEpiLaunch& p, hipStream_t s);
 hipError_t launch_gemm_dq(const GemmEpiLaunch& p, hipStream_t s);
@@ -170,7 +178,7 @@ struct EpiGradLaunch {
     const uint16_t* pre; int64_t ldpre;
     const uint16_t* mul; int64_t ldmul;
     int64_t rows, cols;
-    int32_t act, vec;
+    int32_t act;
     uint16_t* dpre; int64_t lddpre;                       // null: not written
     uint16_t* dmul; int64_t lddmul;
     float* dbias;              // [cols], null: none

@@ -62,6 +62,35 @@ using GemmArgs = GemmLaunch;
 using WoArgs = WoGemmLaunch;
 #endif
 
+// The part of K that a workgroup multiplies: its elements, and those from its
+// first to the row's end.
+struct KRange { int64_t len, left; };
+#if FP4_EPILOGUE_FORM
+// The operands' pointers move to its first element.
+template <int BITS, int BLOCK>
+__device__ __forceinline__ KRange k_range(GemmArgs& p)
+{
+    const int64_t from = (int64_t)blockIdx.z * p.kstep, left = p.k - from;
+    p.qa += from * BITS / 8; p.qb += from * BITS / 8;
+    p.sa += from / BLOCK; p.sb += from / BLOCK;
+    return KRange{left < p.kstep ? left : p.kstep, left};
+}
+#define FP4_K_RANGE(BITS, BLOCK) k_range<BITS, BLOCK>(p)
+#else
+#define FP4_K_RANGE(BITS, BLOCK) KRange{K, K}
+#endif
+
+// K ranges of a launch, a workgroup each.
+inline unsigned k_ranges(const GemmArgs& p)
+{
+#if FP4_EPILOGUE_FORM
+    return (unsigned)p.splits;
+#else
+    (void)p;
+    return 1;
+#endif
+}
+
 constexpr int kTile = 256;        // workgroup tile (rows of W) x (rows of A)
 constexpr int kGemmThreads = 256;
 
@@ -234,12 +263,18 @@ __device__ __forceinline__ void store_tile_lds(const GemmArgs& p, const v16f (&a
         if (n >= p.n) continue;
         float bias[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) bias[i] = p.ep.bias && n + i < p.n ? epi_bias(p.ep, n + i) : 0.0f;
+        for (int i = 0; i < 8; ++i) bias[i] = p.ep.bias && gridDim.z == 1 && n + i < p.n ? epi_bias(p.ep, n + i) : 0.0f;
         for (int ml = tid / (kTile / 8); ml < kTile / 2; ml += (int)blockDim.x / (kTile / 8)) {
             const int64_t m = m_base + half * (kTile / 2) + ml;
             if (m >= p.m) break;
             const v4f* const src = reinterpret_cast<const v4f*>(img + ml * kCTileRow + 32 * cb);
             const v4f a = src[0], b = src[1];
+            if (gridDim.z > 1) {                           // rows of whole eights
+                v4f* const out = reinterpret_cast<v4f*>(p.part + ((int64_t)blockIdx.z * p.m + m) * p.ldp + n);
+                out[0] = a;
+                out[1] = b;
+                continue;
+            }
             const float sum[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
             epi_put<8>(p.ep, p.c, p.ldc, m, n, p.n, sum, bias);
         }
@@ -330,7 +365,9 @@ __global__ __launch_bounds__(kMx4Threads) void k_gemm_mx(GemmArgs p)
     tile_coords((int)((N + kTile - 1) / kTile), (int)((M + kTile - 1) / kTile), &tn, &tm);
     const int64_t n_base = (int64_t)tn * kTile, m_base = (int64_t)tm * kTile;
     const int64_t rowb = K / 2, rows = K / 32;
-    const int KT = (int)(K / BK);
+    const KRange kr = FP4_K_RANGE(4, 32);
+    const int64_t rows_left = kr.left / 32;
+    const int KT = (int)(kr.len / BK);
     auto row_w = [&](int r) { return n_base + r < N ? n_base + r : N - 1; };   // rows past the matrix
     auto row_a = [&](int r) { return m_base + r < M ? m_base + r : M - 1; };   // re-read the last one
 
@@ -393,7 +430,7 @@ __global__ __launch_bounds__(kMx4Threads) void k_gemm_mx(GemmArgs p)
         } else if (kt % L::GroupStages == 0 && kt < KT) {
             // group kt / 4 (stages kt .. kt + 3) with the codes of its first stage
             const int64_t off = (int64_t)(kt / L::GroupStages) * L::GroupRow + 16 * ghalf;
-            const int64_t o = off + 16 <= rows ? off : rows - 16;
+            const int64_t o = off + 16 <= rows_left ? off : rows_left - 16;
             uint8_t* const gb = gbuf + ((kt / L::GroupStages) & 1) * L::GroupBytes;
 #pragma unroll
             for (int j = 0; j < 2; ++j) dma16(gsrc[j] + o, gb + j * (L::GroupBytes / 2) + 1024 * wave);
@@ -419,7 +456,7 @@ __global__ __launch_bounds__(kMx4Threads) void k_gemm_mx(GemmArgs p)
         }
         if (part == 0 && kt % L::GroupStages == 0 && kt < KT) {
             const int64_t off = (int64_t)(kt / L::GroupStages) * L::GroupRow + 16 * ghalf;
-            const int64_t o = off + 16 <= rows ? off : rows - 16;
+            const int64_t o = off + 16 <= rows_left ? off : rows_left - 16;
             uint8_t* const gb = gbuf + ((kt / L::GroupStages) & 1) * L::GroupBytes;
 #pragma unroll
             for (int j = 0; j < 2; ++j) dma16(gsrc[j] + o, gb + j * (L::GroupBytes / 2) + 1024 * wave);
@@ -573,7 +610,7 @@ static hipError_t launch_mx(const GemmArgs& p, hipStream_t s)
     hipError_t e = allow_lds(k_gemm_mx<BK, NS>, sh);
     if (e != hipSuccess) return e;
     const unsigned tiles = (unsigned)(((p.n + kTile - 1) / kTile) * ((p.m + kTile - 1) / kTile));
-    hipLaunchKernelGGL((k_gemm_mx<BK, NS>), dim3(tiles), dim3(kMx4Threads), sh, s, p);
+    hipLaunchKernelGGL((k_gemm_mx<BK, NS>), dim3(tiles, 1, k_ranges(p)), dim3(kMx4Threads), sh, s, p);
     return hipGetLastError();
 }
 
@@ -634,7 +671,9 @@ __global__ __launch_bounds__(kMx4Threads) void k_gemm_mx16(GemmArgs p)
     tile_coords((int)((N + kTile - 1) / kTile), (int)((M + kTile - 1) / kTile), &tn, &tm);
     const int64_t n_base = (int64_t)tn * kTile, m_base = (int64_t)tm * kTile;
     const int64_t rowb = K / 2, rows = K / 16;
-    const int KT = (int)(K / L::EPS);
+    const KRange kr = FP4_K_RANGE(4, 16);
+    const int64_t rows_left = kr.left / 16;
+    const int KT = (int)(kr.len / L::EPS);
     auto row_w = [&](int r) { return n_base + r < N ? n_base + r : N - 1; };
     auto row_a = [&](int r) { return m_base + r < M ? m_base + r : M - 1; };
 
@@ -668,7 +707,7 @@ __global__ __launch_bounds__(kMx4Threads) void k_gemm_mx16(GemmArgs p)
         }
         if (part == 0 && kt % L::GS == 0 && kt < KT) {
             const int64_t off = (int64_t)(kt / L::GS) * 32 + 16 * ghalf;
-            const uint32_t o = (uint32_t)(off + 16 <= rows ? off : rows - 16);
+            const uint32_t o = (uint32_t)(off + 16 <= rows_left ? off : rows_left - 16);
             uint8_t* const gb = gbuf + ((kt / L::GS) & 1) * L::GroupBytes;
             dma16(p.sb + (goff[0] + o), gb + 1024 * wave);
             dma16(p.sa + (goff[1] + o), gb + L::GroupBytes / 2 + 1024 * wave);
@@ -693,7 +732,7 @@ __global__ __launch_bounds__(kMx4Threads) void k_gemm_mx16(GemmArgs p)
         __builtin_amdgcn_s_barrier();
         const uint8_t* st = smem + (kt % NS) * L::Bytes;
         // this stage's 16 scale bytes of each fragment row: half h of its
-        // group, which starts at min(32 g + 16 h, rows - 16) of the row
+        // group, which starts at min(32 g + 16 h, rows_left - 16) of the row
         const int g = kt / L::GS, h = kt % L::GS;
         const uint8_t* gb = gbuf + (g & 1) * L::GroupBytes;
         uint32_t swg[4][2], sag[2][2];
@@ -780,7 +819,7 @@ hipError_t launch_gemm_mx16(const GemmArgs& p, hipStream_t s)
     hipError_t e = allow_lds(k_gemm_mx16, sh);
     if (e != hipSuccess) return e;
     const unsigned tiles = (unsigned)(((p.n + kTile - 1) / kTile) * ((p.m + kTile - 1) / kTile));
-    hipLaunchKernelGGL(k_gemm_mx16, dim3(tiles), dim3(kMx4Threads), sh, s, p);
+    hipLaunchKernelGGL(k_gemm_mx16, dim3(tiles, 1, k_ranges(p)), dim3(kMx4Threads), sh, s, p);
     return hipGetLastError();
 }
 
@@ -952,7 +991,7 @@ __global__ __launch_bounds__(kGemmThreads) void k_gemm_dq(GemmArgs p)
     const int64_t m_base = (int64_t)blockIdx.y * kTile;
     const int64_t M = p.m, N = p.n, K = p.k;
     const int64_t rowb = W8 ? K : W6 ? K / 4 * 3 : K / 2, rows = K / BLOCK;
-    const int KT = (int)(K / kDqBK);
+    const int KT = (int)((FP4_K_RANGE((W8 ? 8 : W6 ? 6 : 4), BLOCK)).len / kDqBK);
     const ScaleFmt fw{p.fb.ebits, p.fb.mbits, p.fb.bias, p.fb.maxcode, p.fb.smax, p.fb.is_e8m0};
     const ScaleFmt fa{p.fa.ebits, p.fa.mbits, p.fa.bias, p.fa.maxcode, p.fa.smax, p.fa.is_e8m0};
     // bf16 spans the binary32 range, so the power-of-two part of each tensor
@@ -1243,7 +1282,7 @@ __global__ __launch_bounds__(128 * WM) void k_gemm_nv(GemmArgs p)
     tile_coords((int)((N + kTile - 1) / kTile), (int)((M + kTile - 1) / kTile), &tn, &tm);
     const int64_t n_base = (int64_t)tn * kTile, m_base = (int64_t)tm * kTile;
     const int64_t rowb = W8 ? K : K / 2, rows = K / BLOCK;
-    const int KT = (int)(K / kMx3BK);
+    const int KT = (int)((FP4_K_RANGE((W8 ? 8 : 4), BLOCK)).len / kMx3BK);
     // 16-byte chunk c of row r sits at c ^ swz(r) (64- or 128-byte rows)
     auto swz = [&](int r) { return W8 ? mx_swz<256>(r) : mx_swz<128>(r); };
 
@@ -1489,7 +1528,7 @@ static hipError_t launch_nv(const GemmArgs& p, hipStream_t s)
     hipError_t e = allow_lds(k_gemm_nv<BLOCK, NS, CVT, WM>, sh);
     if (e != hipSuccess) return e;
     const unsigned tiles = (unsigned)(((p.n + kTile - 1) / kTile) * ((p.m + kTile - 1) / kTile));
-    hipLaunchKernelGGL((k_gemm_nv<BLOCK, NS, CVT, WM>), dim3(tiles), dim3(128 * WM), sh, s, p);
+    hipLaunchKernelGGL((k_gemm_nv<BLOCK, NS, CVT, WM>), dim3(tiles, 1, k_ranges(p)), dim3(128 * WM), sh, s, p);
     return hipGetLastError();
 }
 
@@ -1821,7 +1860,7 @@ bool gemm_dq_supported(const ScaleFmtHost& fa, const ScaleFmtHost& fb, int elem)
 template <int BLOCK, int ELEM>
 static hipError_t launch_dq_elem(const GemmArgs& p, bool f16, hipStream_t s)
 {
-    dim3 grid((unsigned)((p.n + kTile - 1) / kTile), (unsigned)((p.m + kTile - 1) / kTile));
+    dim3 grid((unsigned)((p.n + kTile - 1) / kTile), (unsigned)((p.m + kTile - 1) / kTile), k_ranges(p));
     const size_t sh = sizeof(DqSmem);
     if constexpr (ELEM != 2 && ELEM != 4 && ELEM != 5) {      // FP8 / FP6 elements have no f16 variant
         if (f16) {
@@ -1877,7 +1916,7 @@ hipError_t launch_gemm_dq(const GemmArgs& p, hipStream_t s)
     // products are bf16 subnormals) keeps the LDS dequantize path
     if (!p.fa.is_e8m0 && !p.fb.is_e8m0)
         return p.block == 16 ? launch_nv<16, kNvBf16>(p, s) : launch_nv<32, kNvBf16>(p, s);
-    dim3 grid((unsigned)((p.n + kTile - 1) / kTile), (unsigned)((p.m + kTile - 1) / kTile));
+    dim3 grid((unsigned)((p.n + kTile - 1) / kTile), (unsigned)((p.m + kTile - 1) / kTile), k_ranges(p));
     const size_t sh = sizeof(DqSmem);
     hipError_t e = hipSuccess;
     if (f16) e = p.block == 16 ? allow_lds(k_gemm_dq<true, 16>, sh) : allow_lds(k_gemm_dq<true, 32>, sh);
@@ -2324,6 +2363,43 @@ hipError_t launch_wo_gemm(const WoArgs& p, hipStream_t s)
 }
 
 #if FP4_EPILOGUE_FORM
+// Microseconds that a 256 x 256 tile takes for 128 elements of K, and the
+// elements that a K range must be a multiple of (what a kernel's scale loads
+// cover at once).
+struct TileCost { double us; int64_t step; };
+static TileCost tile_cost(const GemmLaunch& p)
+{
+    if (p.elem == 0 && p.fa.is_e8m0 && p.fb.is_e8m0) return TileCost{1.2, 1024};
+    if (p.elem == 0 && exact_in_f16(p.fa) && exact_in_f16(p.fb)) return TileCost{2.8, 128};
+    return TileCost{4.5, 128};
+}
+
+// K in ranges where whole products are too few tiles for 256 CUs: the
+// workgroups run in rounds of 256, each as long as a range, and the partial
+// sums are written and read once more at about 4 TB/s, in a launch of its own.
+int64_t gemm_split(GemmEpiLaunch* p)
+{
+    const int64_t tiles = ((p->n + kTile - 1) / kTile) * ((p->m + kTile - 1) / kTile);
+    const TileCost c = tile_cost(*p);
+    const int64_t units = (p->k + c.step - 1) / c.step;
+    p->ldp = (p->n + 7) / 8 * 8;
+    p->splits = 1;
+    p->kstep = p->k;
+    if (gemm_small_supported(*p)) return 0;
+    double best = 0.0;
+    for (int64_t s = 1; s <= 16 && s <= units; ++s) {
+        const int64_t per = (units + s - 1) / s, used = (units + per - 1) / per;
+        if (used != s) continue;
+        const double us = (double)((tiles * s + 255) / 256) * (double)(per * c.step / 128) * c.us +
+                          (s > 1 ? 4.0 + 8.0 * (double)s * (double)p->m * (double)p->ldp / 4e6 : 0.0);
+        if (s == 1 || us < 0.9 * best) {
+            best = us;
+            p->splits = s;
+            p->kstep = s == 1 ? p->k : per * c.step;
+        }
+    }
+    return p->splits == 1 ? 0 : 4 * p->splits * p->m * p->ldp;
+}
 }  // namespace epi
 #endif
 }  // namespace fp4

@@ -560,9 +560,7 @@ FP4_API fp4_status fp4_residual_norm_backward(const fp4_norm* args, const float*
  * so that a gated layer is two products: the up projection's output is the
  * gate projection's mul.  bias: [n] in bias_dtype (f32 or bf16); mul, residual
  * and pre: bf16 [m, n], element aligned, row strides >= n; each may be null.
- * y may be mul or residual (same row stride), pre none of them.  Rows of
- * whole 16-byte vectors (every stride % 8 == 0, every pointer 16-byte
- * aligned) are read and written as vectors. */
+ * y may be mul or residual (same row stride), pre none of them. */
 typedef enum fp4_act {
     FP4_ACT_NONE = 0,
     FP4_ACT_RELU = 1,
@@ -583,10 +581,14 @@ typedef struct fp4_epilogue {
 /*
  * fp4_gemm_epilogue -- fp4_gemm followed by the epilogue.  Requirements,
  * paths and errors as fp4_gemm (K may not be 0 here); the product's error
- * bound is that of fp4_gemm before any rounding.
+ * bound is that of fp4_gemm before any rounding.  A product of few tiles is
+ * taken in ranges of K, whose sums are joined in a fixed order.  workspace: as
+ * above, fp4_gemm_epilogue_workspace bytes for these operands (it depends on
+ * their shapes and formats, and on fp4_set_gemm_small_outputs).
  */
+FP4_API int64_t fp4_gemm_epilogue_workspace(const fp4_tensor* a, const fp4_tensor* b);
 FP4_API fp4_status fp4_gemm_epilogue(const fp4_tensor* a, const fp4_tensor* b, const fp4_epilogue* e, uint16_t* y,
-                                     int64_t ldy, void* stream);
+                                     int64_t ldy, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * fp4_wo_gemm_epilogue -- fp4_wo_gemm followed by the epilogue, for serving
@@ -644,8 +646,7 @@ FP4_API fp4_status fp4_moe_route(const void* logits, int32_t dtype, int64_t ld, 
  * down_scale [experts] in binary32 (null: 1) multiply an expert's products, for
  * experts that were quantized each with a tensor scale of its own. */
 typedef struct fp4_moe_bank {
-    const fp4_tensor* gate_up;
-    const fp4_tensor* down;
+    fp4_tensor gate_up, down;
     const float* up_scale;
     const float* down_scale;
     int64_t experts;

@@ -116,6 +116,26 @@ def test_product_epilogue_sizes(m, n, k, scale, block):
             fq.set_gemm_small_outputs(was)
 
 
+@pytest.mark.parametrize("block,scale,element,k", [(32, "e8m0", "e2m1", 2304), (32, "e8m0", "e2m1", 4096), (32, "e8m0", "e2m1", 2176),
+                                                   *((b, s, e, 1408 if b == 32 or s != "e8m0" else 2304)
+                                                     for b, s, e, _, small in PATHS if not small and (b, s, e) != (32, "e8m0", "e2m1"))])
+def test_product_epilogue_in_k_ranges(block, scale, element, k):
+    """Few tiles of a long K: ranges of it, the last one short, joined before the epilogue."""
+    m, n = 260, 301
+    a, b = quantized(m, k, 61, block, scale, element, 1.0), quantized(n, k, 62, block, scale, element, 0.1)
+    v, e = product64(a, b)
+    was = fq.set_gemm_small_outputs(0)
+    try:
+        assert fq.lib().fp4_gemm_epilogue_workspace(a.packed(), b.packed()) >= 2 * 4 * m * 304
+        bias, mul, res = tensors(m, n, 63, BF, True, True)
+        y, pre = fq.fp4_gemm_epilogue(a, b, bias=bias, act="silu", mul=mul, residual=res, save_pre=True)
+        check(y, pre, v, e, "silu", bias, mul, res)
+        for _ in range(3):
+            assert torch.equal(fq.fp4_gemm_epilogue(a, b, bias=bias, act="silu", mul=mul, residual=res)[0], y)
+    finally:
+        fq.set_gemm_small_outputs(was)
+
+
 @pytest.mark.parametrize("small", [0, 1 << 21])
 def test_product_epilogue_strided_rows_stay_inside(small):
     """Padded rows of every operand, and y in the place of the residual; what lies behind the rows stays."""

@@ -32,7 +32,7 @@ Y = FAKE + 1024
                                            (dict(pre=FAKE), -1)])
 def test_gemm_epilogue_rejects_before_launch(kw, want):
     a, b, e = _q(5, 256), _q(64, 256), _epi(**kw)
-    assert fq.lib().fp4_gemm_epilogue(ctypes.byref(a), ctypes.byref(b), ctypes.byref(e), Y, 64, None) == want
+    assert fq.lib().fp4_gemm_epilogue(ctypes.byref(a), ctypes.byref(b), ctypes.byref(e), Y, 64, FAKE, ROOM, None) == want
 
 
 @pytest.mark.parametrize("kw,want", EPI + [(dict(pre=FAKE + 512), -2)])
@@ -44,8 +44,8 @@ def test_wo_gemm_epilogue_rejects_before_launch(kw, want):
 def test_products_epilogues_refuse_what_the_products_refuse():
     L, e = fq.lib(), _epi()
 
-    def gemm(a, b, y=Y, ldy=64, e=e):
-        return L.fp4_gemm_epilogue(ctypes.byref(a), ctypes.byref(b), None if e is None else ctypes.byref(e), y, ldy, None)
+    def gemm(a, b, y=Y, ldy=64, e=e, ws=FAKE, room=ROOM):
+        return L.fp4_gemm_epilogue(ctypes.byref(a), ctypes.byref(b), None if e is None else ctypes.byref(e), y, ldy, ws, room, None)
 
     def wo(w, m=4, x=FAKE, ldx=256, y=Y, ldy=64, e=e):
         return L.fp4_wo_gemm_epilogue(x, ldx, m, ctypes.byref(w), None if e is None else ctypes.byref(e), y, ldy, None)
@@ -55,6 +55,14 @@ def test_products_epilogues_refuse_what_the_products_refuse():
     assert gemm(_q(5, 128), ok) == -3 and gemm(_q(5, 0), _q(64, 0)) == -3 and gemm(_q(5, 256, 32, 4), ok) == -2
     assert gemm(_q(5, 256, q=FAKE + 4), ok) == -4 and gemm(_q(5, 256, transform=1), ok) == -2
     assert gemm(_q(5, 256, 16, 4, 3), _q(64, 256, 16, 2, 3)) == -2                 # a pairing without an exact type
+    a, b = _q(3000, 4096), _q(800, 4096)                  # K in ranges
+    need = L.fp4_gemm_epilogue_workspace(ctypes.byref(a), ctypes.byref(b))
+    e2 = _epi(mul=None, res=None)
+    assert need > 0 and need % (4 * 3000 * 800) == 0
+    assert gemm(a, b, ldy=800, e=e2, ws=None) == -1 and gemm(a, b, ldy=800, e=e2, room=need - 1) == -1
+    assert gemm(a, b, ldy=800, e=e2, ws=FAKE + 8) == -4
+    assert L.fp4_gemm_epilogue_workspace(ctypes.byref(_q(5, 256)), ctypes.byref(ok)) == 0
+    assert L.fp4_gemm_epilogue_workspace(None, ctypes.byref(ok)) == -1 and L.fp4_gemm_epilogue_workspace(ctypes.byref(ok), None) == -1
     assert wo(ok, m=0) == -2 and wo(ok, m=17) == -2 and wo(ok, x=None) == -1 and wo(ok, ldx=260) == -4
     assert wo(_q(64, 0)) == -3 and wo(_q(0, 256), ldy=0) == -3 and wo(_q(64, 256, transform=1)) == -2
 
@@ -91,7 +99,7 @@ def _moe(m=4, top=2, hidden=256, ffn=128, experts=3, x=FAKE, ldx=256, up=None, d
          res=None, ldr=256, y=Y, ldy=256, ws=FAKE, room=ROOM, bank=True):
     up = up or _q(experts * 2 * ffn, hidden)
     down = down or _q(experts * hidden, ffn)
-    b = fq.Fp4MoeBankC(ctypes.pointer(up), ctypes.pointer(down), us, ds, experts)
+    b = fq.Fp4MoeBankC(up, down, us, ds, experts)
     return fq.lib().fp4_moe(x, ldx, m, ctypes.byref(b) if bank else None, ids, w, top, act, res, ldr, y, ldy, ws, room, None)
 
 
