@@ -32,90 +32,8 @@
 
 namespace fp4 {
 
-constexpr int kMoePairs = kMoeMaxTokens * kMoeMaxTop;      // 256
+constexpr int kMoePairs = kMoeMaxTokens * kMoeMaxTop;      // 256: a pair's index is a byte
 constexpr int kNoExpert = 0x7FFFFFFF;
-
-// The pairs sorted by expert; experts without a token have no entry.
-struct MoeTable {
-    int32_t active;                       // experts with tokens
-    int32_t expert[kMoePairs];
-    uint16_t start[kMoePairs + 1];        // of the active expert's pairs
-    uint16_t row[kMoePairs];              // token * top + choice
-    uint8_t tok[kMoePairs];
-    float w[kMoePairs];
-};
-struct MoeScratch {
-    int32_t raw[kMoePairs], key[kMoePairs], sorted[kMoePairs];
-    int32_t waves[kMoePairs / 64];
-};
-
-// Called by all threads (at least 256); scratch may be the ring.  An id that a
-// token names again adds its weight to the first; one outside the experts is
-// dropped.
-__device__ __forceinline__ void moe_table(const MoeLaunch& p, MoeTable& t, MoeScratch& s, int tid)
-{
-    const int pairs = p.m * p.top;
-    const bool in = tid < pairs;
-    const int tok = in ? tid / p.top : 0, k = tid - tok * p.top;
-    float w = 0.0f;
-    if (in) {
-        s.raw[tid] = p.ids[tid];
-        w = p.weights[tid];
-    }
-    __syncthreads();
-    int key = kNoExpert;
-    if (in) {
-        const int id = s.raw[tid];
-        bool again = false;
-        for (int j = 0; j < k; ++j) again |= s.raw[tok * p.top + j] == id;
-        if (id >= 0 && id < p.experts && !again) {
-            key = id;
-            for (int j = k + 1; j < p.top; ++j)
-                if (s.raw[tok * p.top + j] == id) w += p.weights[tok * p.top + j];
-        }
-        s.key[tid] = key;
-    }
-    __syncthreads();
-    if (in && key != kNoExpert) {
-        int at = 0;
-        for (int q = 0; q < pairs; ++q) {
-            const int o = s.key[q];
-            at += o < key || (o == key && q < tid);
-        }
-        s.sorted[at] = key;
-        t.tok[at] = (uint8_t)tok;
-        t.row[at] = (uint16_t)tid;
-        t.w[at] = w;
-    }
-    // pairs that have an expert
-    const int mine = __builtin_popcountll(__builtin_amdgcn_ballot_w64(in && key != kNoExpert));
-    if ((tid & 63) == 0 && tid < kMoePairs) s.waves[tid >> 6] = mine;
-    __syncthreads();
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < kMoePairs / 64; ++i) n += s.waves[i];
-    const bool first = tid < n && (tid == 0 || s.sorted[tid] != s.sorted[tid - 1]);
-    const uint64_t lanes = __builtin_amdgcn_ballot_w64(first);
-    __syncthreads();
-    if ((tid & 63) == 0 && tid < kMoePairs) s.waves[tid >> 6] = __builtin_popcountll(lanes);
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int i = 0; i < kMoePairs / 64; ++i) {
-        before += i < (tid >> 6) ? s.waves[i] : 0;
-        all += s.waves[i];
-    }
-    if (first) {
-        const int a = before + __builtin_popcountll(lanes & ((1ull << (tid & 63)) - 1));
-        t.expert[a] = s.sorted[tid];
-        t.start[a] = (uint16_t)tid;
-    }
-    if (tid == 0) {
-        t.active = all;
-        t.start[all] = (uint16_t)n;
-    }
-    __syncthreads();
-}
 
 // One side's weights as a wave streams them: RG groups of 16 rows of an
 // expert's matrix, K elements each.
@@ -128,52 +46,69 @@ struct MoeSide {
     int64_t ldx, plane;                   // plane: from its first bf16 term to its second
 };
 
-// The ring of one wave for XQ (0: one token, else up to 4 XQ), XP terms of x.
-template <int RG, int XQ, int XP, int ELEM, int BLOCK>
-struct MoeRing {
-    static constexpr int WP = WoRow<ELEM, 1>::WP, SCB = 128 / BLOCK;
-    using S = WoSlot<RG, XQ, WP, 1, SCB>;
-    static constexpr int XBytes = 256 * S::XRows;
-    static constexpr int Bytes = S::X + XP * XBytes;
-    static constexpr int Loads = RG * S::WD + S::NSC + XP * (XQ == 0 ? 1 : XQ);
+// A slot of a wave's ring: a chunk of SUB runs of 128 elements of K for 16 RG
+// rows of W (as in the weight-only product's slot), their scales, and XR rows of
+// XP terms of x, whose pieces of 256 bytes lie term by term, row by row, run by
+// run, four to a load.
+template <int RG, int XR, int XP, int ELEM, int BLOCK, int SUB>
+struct MoeSlot {
+    static constexpr int K = 128 * SUB;
+    static constexpr int WP = WoRow<ELEM, SUB>::WP, WB = WoRow<ELEM, SUB>::WB, WD = WP / 64;
+    static constexpr int SCB = K / BLOCK, SDW = SCB / 4;
+    static constexpr int NSC = (RG * 16 * SDW + 63) / 64;
+    static constexpr int W = 0, SC = RG * 16 * WP;
+    static constexpr int X = SC + RG * 16 * SCB;
+    static constexpr int Pieces = XR * XP * SUB, XL = (Pieces + 3) / 4;
+    static constexpr int Bytes = X + 256 * Pieces;
+    static constexpr int Loads = RG * WD + NSC + XL;
 };
 
 // Slots of a wave and waves that stream, within `budget` bytes of LDS for NW
-// waves: up to four slots each, and where two do not fit, fewer waves.
-template <typename R, int NW>
+// waves: up to eight slots each, and where two do not fit, fewer waves.
+template <typename S, int NW, int BUDGET>
 struct MoeShape {
-    static constexpr int fit(int budget) { return budget / (NW * R::Bytes); }
-    static constexpr int slots(int budget)
+    static constexpr int Fit = BUDGET / (NW * S::Bytes);
+    static constexpr int slots()
     {
-        int d = fit(budget) > 4 ? 4 : fit(budget) < 2 ? 2 : fit(budget);
-        while ((d - 1) * R::Loads >= 64) --d;
+        int d = Fit > 8 ? 8 : Fit < 2 ? 2 : Fit;
+        while ((d - 1) * S::Loads >= 64) --d;
         return d;
     }
-    static constexpr int waves(int budget) { return fit(budget) >= 2 ? NW : budget / (2 * R::Bytes); }
+    static constexpr int D = slots();
+    static constexpr int Waves = Fit >= 2 ? NW : BUDGET / (2 * S::Bytes);
+    static constexpr int Bytes = Waves * D * S::Bytes;
 };
 
-// fold(a, acc): the sums of active expert a over this wave's chunks of it;
-// acc[g][r] is row 4 (lane / 16) + r of the expert's tokens, column lane % 16 of group g.
-template <int NW, int BUDGET, int RG, int XQ, int XP, int ELEM, int BLOCK, bool SPLIT, bool POW2, typename F>
-__device__ __forceinline__ void moe_stream(uint8_t* lds, const MoeSide& s, const MoeTable& t, const uint16_t* xrow_of_pair,
-                                           const float* sdec, int a0, int experts, int wave, int lane, F fold)
+// `behind` whole slots of LOADS loads each may still be under way.
+template <int LOADS, int MOST>
+__device__ __forceinline__ void wait_slots(int behind)
+{
+    if constexpr (MOST == 0) {
+        wait_vmcnt<0>();
+    } else {
+        if (behind >= MOST) wait_vmcnt<MOST * LOADS>();
+        else wait_slots<LOADS, MOST - 1>(behind);
+    }
+}
+
+// Streams items first .. first + mine - 1 of a list of (expert, chunk) pairs,
+// K / (128 SUB) chunks to an expert.  expert(a) says who the a-th is:
+// {id, tokens, their rows of x}.  fold(a, acc) takes the sums over this call's
+// chunks of it: acc[g][r] is row 4 (lane / 16) + r of the expert's tokens, column
+// lane % 16 of group g.
+struct MoeExpert { int id, tokens; const uint8_t* rows; };
+
+template <int D, int RG, int XR, int XP, int ELEM, int BLOCK, int SUB, bool SPLIT, bool POW2, typename E, typename F>
+__device__ __forceinline__ void moe_stream(uint8_t* ring, const MoeSide& s, const float* sdec, int first, int mine, int lane,
+                                           E expert, F fold)
 {
     constexpr bool WIDE = ELEM >= 2;
-    using R = MoeRing<RG, XQ, XP, ELEM, BLOCK>;
-    using S = typename R::S;
-    using Shape = MoeShape<R, NW>;
-    constexpr int D = Shape::slots(BUDGET), NA = Shape::waves(BUDGET);
-    constexpr int WP = R::WP, WB = WoRow<ELEM, 1>::WB, SCB = R::SCB, SDW = SCB / 4;
-    static_assert(D >= 2 && NA >= 1 && (D - 1) * R::Loads < 64, "ring");
-    static_assert(NA * D * R::Bytes <= BUDGET, "LDS");
-    const int r16 = lane & 15, grp = lane >> 4;
-    const int nch = s.k / 128;
-    // this wave's part of the (expert, chunk) list
-    const int items = experts * nch;
-    if (wave >= NA) return;
-    const int first = (int)((int64_t)items * wave / NA), mine = (int)((int64_t)items * (wave + 1) / NA) - first;
+    using S = MoeSlot<RG, XR, XP, ELEM, BLOCK, SUB>;
+    static_assert(SUB == 1 || !WIDE, "two runs a chunk for the 4-bit grids");
+    static_assert(D >= 2 && (D - 1) * S::Loads < 64, "ring");
     if (mine <= 0) return;
-    uint8_t* const ring = lds + wave * (D * R::Bytes);
+    const int r16 = lane & 15, grp = lane >> 4;
+    const int nch = s.k / S::K;
     const uint32_t rowb = (uint32_t)((int64_t)s.k * (ELEM <= 1 ? 4 : ELEM <= 3 ? 8 : 6) / 8);
     const uint32_t srow = (uint32_t)(s.k / BLOCK);
 
@@ -182,9 +117,9 @@ __device__ __forceinline__ void moe_stream(uint8_t* lds, const MoeSide& s, const
     bool wact[S::WD];
 #pragma unroll
     for (int k = 0; k < S::WD; ++k) {
-        const int r = WP == 128 ? 8 * k + (lane >> 3) : lane >> 2;
-        const int pc = WP == 128 ? (lane & 7) ^ wo_swz8(r) : (lane & 3) ^ wo_swz(r);
-        wact[k] = 16 * pc < WB;
+        const int r = S::WP == 128 ? 8 * k + (lane >> 3) : lane >> 2;
+        const int pc = S::WP == 128 ? (lane & 7) ^ wo_swz8(r) : (lane & 3) ^ wo_swz(r);
+        wact[k] = 16 * pc < S::WB;
 #pragma unroll
         for (int g = 0; g < RG; ++g) wsrc[g][k] = ((g ? s.row1 : s.row0) + (uint32_t)r) * rowb + 16u * (uint32_t)pc;
     }
@@ -192,117 +127,112 @@ __device__ __forceinline__ void moe_stream(uint8_t* lds, const MoeSide& s, const
     bool sact[S::NSC];
 #pragma unroll
     for (int j = 0; j < S::NSC; ++j) {
-        const int f = 64 * j + lane, rr = f / SDW;
+        const int f = 64 * j + lane, rr = f / S::SDW;
         sact[j] = rr < 16 * RG;
         const int r = sact[j] ? rr : 16 * RG - 1;
-        ssrc[j] = ((r < 16 ? s.row0 : s.row1) + (uint32_t)(r & 15)) * srow + 4u * (uint32_t)(f % SDW);
+        ssrc[j] = ((r < 16 ? s.row0 : s.row1) + (uint32_t)(r & 15)) * srow + 4u * (uint32_t)(f % S::SDW);
     }
-    constexpr int XL = XQ == 0 ? 1 : XQ;
-    const uint16_t* xsrc[XL];
+    // x: load q, lane l takes 16 bytes of piece 4 q + l / 16: run piece % SUB of
+    // row piece / SUB, which is token row % XR (past the expert's last: the last
+    // again), term row / XR
+    const uint16_t* xsrc[S::XL];
     const uint8_t* qe = nullptr;
     const uint8_t* se = nullptr;
-    // the next chunk to load
-    int ia = first / nch, ik = first - ia * nch;
+    int ia = first / nch, ik = first - ia * nch;           // the next chunk to load
     auto enter = [&](int a) {
-        const int e = __builtin_amdgcn_readfirstlane(t.expert[a0 + a]);
+        const MoeExpert w = expert(a);
+        const int e = __builtin_amdgcn_readfirstlane(w.id), n = __builtin_amdgcn_readfirstlane(w.tokens);
         qe = s.q + (int64_t)e * s.expert_q;
         se = s.s + (int64_t)e * s.expert_s;
-        const int b = __builtin_amdgcn_readfirstlane((int)t.start[a0 + a]);
-        const int n = __builtin_amdgcn_readfirstlane((int)t.start[a0 + a + 1]) - b;
 #pragma unroll
-        for (int q = 0; q < XL; ++q) {
-            if (XQ == 0) {
-                xsrc[0] = s.x + (int64_t)xrow_of_pair[b] * s.ldx + 2 * lane;
-            } else {
-                const int m = 4 * q + grp;
-                xsrc[q] = s.x + (int64_t)xrow_of_pair[b + (m < n ? m : n - 1)] * s.ldx + 8 * (r16 ^ (m & 7));
-            }
+        for (int q = 0; q < S::XL; ++q) {
+            const int piece = 4 * q + grp, row = piece / SUB, m = row % XR, h = row / XR;
+            xsrc[q] = s.x + (int64_t)w.rows[m < n ? m : n - 1] * s.ldx + (XP > 1 && h == 1 ? s.plane : 0) +
+                      128 * (piece % SUB) + 8 * (r16 ^ (m & 7));
         }
     };
     enter(ia);
     auto issue = [&](int d) {
-        uint8_t* const sl = ring + d * R::Bytes;
+        uint8_t* const sl = ring + d * S::Bytes;
 #pragma unroll
         for (int g = 0; g < RG; ++g)
 #pragma unroll
             for (int k = 0; k < S::WD; ++k)
-                if (ELEM < 4 || wact[k]) dma16(qe + wsrc[g][k] + (uint32_t)ik * (uint32_t)WB, sl + S::W + 16 * WP * g + 1024 * k);
+                if (ELEM < 4 || wact[k])
+                    dma16(qe + wsrc[g][k] + (uint32_t)ik * (uint32_t)S::WB, sl + S::W + 16 * S::WP * g + 1024 * k);
 #pragma unroll
         for (int j = 0; j < S::NSC; ++j)
-            if (sact[j]) dma4(se + ssrc[j] + (uint32_t)ik * (uint32_t)SCB, sl + S::SC + 256 * j);
+            if (sact[j]) dma4(se + ssrc[j] + (uint32_t)ik * (uint32_t)S::SCB, sl + S::SC + 256 * j);
 #pragma unroll
-        for (int h = 0; h < XP; ++h) {
-            const int64_t off = h * s.plane + (int64_t)ik * 128;
-            if (XQ == 0) {
-                dma4(xsrc[0] + off, sl + S::X + h * R::XBytes);
-            } else {
-#pragma unroll
-                for (int q = 0; q < XL; ++q) dma16(xsrc[q] + off, sl + S::X + h * R::XBytes + 1024 * q);
-            }
-        }
-        if (++ik == nch) ik = 0, ++ia;
+        for (int q = 0; q < S::XL; ++q)
+            if (S::Pieces % 4 == 0 || 4 * q + grp < S::Pieces) dma16(xsrc[q] + (int64_t)ik * S::K, sl + S::X + 1024 * q);
     };
-    v4f acc[RG];
+    // a chain of sums for each term: a matrix instruction waits for the one before it
+    v4f acc[RG][XP];
     auto clear = [&] {
 #pragma unroll
-        for (int g = 0; g < RG; ++g) acc[g] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int g = 0; g < RG; ++g)
+#pragma unroll
+            for (int h = 0; h < XP; ++h) acc[g][h] = v4f{0.f, 0.f, 0.f, 0.f};
     };
     clear();
-    const int mr = r16 < S::XRows ? r16 : S::XRows - 1;
-    auto xoff = [&](int h, int tt) {
-        return S::X + h * R::XBytes + (XQ == 0 ? 16 * (4 * grp + tt)
-                                               : 1024 * (mr >> 2) + 256 * (mr & 3) + 16 * ((4 * grp + tt) ^ (mr & 7)));
+    const int mr = r16 < XR ? r16 : XR - 1;
+    auto xoff = [&](int h, int u, int tt) {
+        return S::X + 256 * ((h * XR + mr) * SUB + u) + 16 * ((4 * grp + tt) ^ (mr & 7));
     };
-    auto woff = [&](int j) {
-        if (WP == 64) return S::W + 64 * r16 + 16 * (grp ^ wo_swz(r16));
-        const int byte = ELEM >= 4 ? 24 * grp + 8 * j : ELEM >= 2 ? 32 * grp + 16 * j : 16 * grp;
-        return S::W + WP * r16 + 16 * ((byte >> 4) ^ wo_swz8(r16)) + (byte & 15);
+    auto woff = [&](int u, int j) {
+        if (S::WP == 64) return S::W + 64 * r16 + 16 * (grp ^ wo_swz(r16));
+        const int byte = ELEM >= 4 ? 24 * grp + 8 * j : ELEM >= 2 ? 32 * grp + 16 * j : 64 * u + 16 * grp;
+        return S::W + S::WP * r16 + 16 * ((byte >> 4) ^ wo_swz8(r16)) + (byte & 15);
     };
-    const int soff = S::SC + SCB * r16 + (BLOCK == 16 ? 2 * grp : grp);
+    auto soff = [&](int u) { return S::SC + S::SCB * r16 + (BLOCK == 16 ? 8 * u + 2 * grp : 4 * u + grp); };
     auto consume = [&](int d) {
-        const uint8_t* const sl = ring + d * R::Bytes;
-        v4i xf[XP][4];
+        const uint8_t* const sl = ring + d * S::Bytes;
 #pragma unroll
-        for (int h = 0; h < XP; ++h)
+        for (int u = 0; u < SUB; ++u) {
+            v4i xf[XP][4];
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) xf[h][tt] = *reinterpret_cast<const v4i*>(sl + xoff(h, tt));
+            for (int h = 0; h < XP; ++h)
 #pragma unroll
-        for (int g = 0; g < RG; ++g) {
-            v4i wv;
-            uint32_t dw[8];
-            if constexpr (!WIDE) {
-                wv = *reinterpret_cast<const v4i*>(sl + woff(0) + 16 * WP * g);
-            } else if constexpr (ELEM <= 3) {
-                const v4i w0 = *reinterpret_cast<const v4i*>(sl + woff(0) + 16 * WP * g);
-                const v4i w1 = *reinterpret_cast<const v4i*>(sl + woff(1) + 16 * WP * g);
+                for (int tt = 0; tt < 4; ++tt) xf[h][tt] = *reinterpret_cast<const v4i*>(sl + xoff(h, u, tt));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) { dw[i] = (uint32_t)w0[i]; dw[4 + i] = (uint32_t)w1[i]; }
-            } else {
+            for (int g = 0; g < RG; ++g) {
+                v4i wv;
+                uint32_t dw[8];
+                if constexpr (!WIDE) {
+                    wv = *reinterpret_cast<const v4i*>(sl + woff(u, 0) + 16 * S::WP * g);
+                } else if constexpr (ELEM <= 3) {
+                    const v4i w0 = *reinterpret_cast<const v4i*>(sl + woff(u, 0) + 16 * S::WP * g);
+                    const v4i w1 = *reinterpret_cast<const v4i*>(sl + woff(u, 1) + 16 * S::WP * g);
 #pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    const uint64_t v = *reinterpret_cast<const uint64_t*>(sl + woff(j) + 16 * WP * g);
-                    dw[2 * j] = (uint32_t)v;
-                    dw[2 * j + 1] = (uint32_t)(v >> 32);
+                    for (int i = 0; i < 4; ++i) { dw[i] = (uint32_t)w0[i]; dw[4 + i] = (uint32_t)w1[i]; }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) {
+                        const uint64_t v = *reinterpret_cast<const uint64_t*>(sl + woff(u, j) + 16 * S::WP * g);
+                        dw[2 * j] = (uint32_t)v;
+                        dw[2 * j + 1] = (uint32_t)(v >> 32);
+                    }
+                    dw[6] = dw[7] = 0u;
                 }
-                dw[6] = dw[7] = 0u;
-            }
-            const uint32_t sc = BLOCK == 16 ? (uint32_t)*reinterpret_cast<const uint16_t*>(sl + soff + 16 * SCB * g)
-                                            : (uint32_t)sl[soff + 16 * SCB * g];
-            const float s0 = sdec[sc & 0xFFu], s1 = BLOCK == 16 ? sdec[(sc >> 8) & 0xFFu] : s0;
+                const uint32_t sc = BLOCK == 16 ? (uint32_t)*reinterpret_cast<const uint16_t*>(sl + soff(u) + 16 * S::SCB * g)
+                                                : (uint32_t)sl[soff(u) + 16 * S::SCB * g];
+                const float s0 = sdec[sc & 0xFFu], s1 = BLOCK == 16 ? sdec[(sc >> 8) & 0xFFu] : s0;
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-                const float st = tt < 2 ? s0 : s1;                  // elements 0..15: the first block
-                v4i hi, lo;
-                if constexpr (WIDE) dq8_any<ELEM, SPLIT>(dw, tt, st, hi, lo);
-                else if constexpr (SPLIT) dq8_bf16_split<ELEM == 1>((uint32_t)wv[tt], st, hi, lo);
-                else hi = dq8_bf16<POW2, ELEM == 1>((uint32_t)wv[tt], st);
+                for (int tt = 0; tt < 4; ++tt) {
+                    const float st = tt < 2 ? s0 : s1;                  // elements 0..15: the first block
+                    v4i hi, lo;
+                    if constexpr (WIDE) dq8_any<ELEM, SPLIT>(dw, tt, st, hi, lo);
+                    else if constexpr (SPLIT) dq8_bf16_split<ELEM == 1>((uint32_t)wv[tt], st, hi, lo);
+                    else hi = dq8_bf16<POW2, ELEM == 1>((uint32_t)wv[tt], st);
 #pragma unroll
-                for (int h = 0; h < XP; ++h) {
-                    acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xf[h][tt]),
-                                                                     __builtin_bit_cast(v8bf, hi), acc[g], 0, 0, 0);
-                    if (SPLIT)
-                        acc[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xf[h][tt]),
-                                                                         __builtin_bit_cast(v8bf, lo), acc[g], 0, 0, 0);
+                    for (int h = 0; h < XP; ++h) {
+                        acc[g][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xf[h][tt]),
+                                                                            __builtin_bit_cast(v8bf, hi), acc[g][h], 0, 0, 0);
+                        if (SPLIT)
+                            acc[g][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xf[h][tt]),
+                                                                                __builtin_bit_cast(v8bf, lo), acc[g][h], 0, 0, 0);
+                    }
                 }
             }
         }
@@ -310,34 +240,35 @@ __device__ __forceinline__ void moe_stream(uint8_t* lds, const MoeSide& s, const
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     };
 
-    int issued = 0, at = 0;               // at: the slot of chunk i; chunk i + D takes it next
+    int issued = 0, to = 0;               // to: the slot of the next load
     auto advance = [&] {
-        const int was = ia;
-        issue(issued % D);
+        issue(to);
+        to = to + 1 == D ? 0 : to + 1;
         ++issued;
-        if (ia != was && issued < mine) enter(ia);
+        if (++ik == nch) {
+            ik = 0;
+            ++ia;
+            if (issued < mine) enter(ia);
+        }
     };
     while (issued < D && issued < mine) advance();
-    int ca = first / nch, ck = first - ca * nch;
+    int at = 0, ca = first / nch, ck = first - ca * nch;
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
-        // loads of later chunks that are still under way
-        const int behind = mine - 1 - i < D - 1 ? mine - 1 - i : D - 1;
-        if (behind >= 3) wait_vmcnt<(D > 3 ? 3 * R::Loads : 0)>();
-        else if (behind == 2) wait_vmcnt<(D > 2 ? 2 * R::Loads : 0)>();
-        else if (behind == 1) wait_vmcnt<R::Loads>();
-        else wait_vmcnt<0>();
+        wait_slots<S::Loads, D - 1>(mine - 1 - i);         // loads of later chunks that are still under way
         consume(at);
         at = at + 1 == D ? 0 : at + 1;
         if (issued < mine) advance();
         if (++ck == nch || i + 1 == mine) {
-            fold(ca, acc);
+            v4f sum[RG];
+#pragma unroll
+            for (int g = 0; g < RG; ++g) sum[g] = XP == 1 ? acc[g][0] : acc[g][0] + acc[g][XP - 1];
+            fold(ca, sum);
             clear();
             ck = 0;
             ++ca;
         }
     }
-    wait_vmcnt<0>();
 }
 
 __device__ __forceinline__ ScaleFmt device_fmt(const ScaleFmtHost& f)
@@ -345,38 +276,102 @@ __device__ __forceinline__ ScaleFmt device_fmt(const ScaleFmtHost& f)
     return ScaleFmt{f.ebits, f.mbits, f.bias, f.maxcode, f.smax, f.is_e8m0};
 }
 
-// f(std::integral_constant<int, XQ>) for an expert's number of tokens, at most
-// the launch's
-template <int MAXQ, typename F>
-__device__ __forceinline__ void moe_class(int tokens, F f)
+// f(std::integral_constant<int, XR>) for an expert's number of tokens, XR at
+// most the launch's MAXR
+template <int MAXR, typename F>
+__device__ __forceinline__ void moe_rows(int tokens, F f)
 {
-    if (MAXQ == 0 || tokens <= 1) f(std::integral_constant<int, 0>{});
-    else if (MAXQ == 1 || tokens <= 4) f(std::integral_constant<int, MAXQ >= 1 ? 1 : 0>{});
-    else if (MAXQ == 2 || tokens <= 8) f(std::integral_constant<int, MAXQ >= 2 ? 2 : 0>{});
-    else f(std::integral_constant<int, MAXQ >= 4 ? 4 : 0>{});
+    if (MAXR == 1 || tokens <= 1) f(std::integral_constant<int, 1>{});
+    else if (tokens <= 2) f(std::integral_constant<int, MAXR >= 2 ? 2 : 1>{});
+    else if (MAXR == 4 || tokens <= 4) f(std::integral_constant<int, MAXR >= 4 ? 4 : 1>{});
+    else if (tokens <= 8) f(std::integral_constant<int, MAXR >= 8 ? 8 : 1>{});
+    else f(std::integral_constant<int, MAXR >= 16 ? 16 : 1>{});
 }
 
-constexpr int kMoeUpWaves = 4, kMoeUpBudget = 60 * 1024;
-constexpr int kMoeDownWaves = 8, kMoeDownBudget = 144 * 1024;
+// Bits from .. to - 1 of 256.
+__device__ __forceinline__ bool any_bit(const uint64_t (&m)[kMoePairs / 64], int from, int to)
+{
+    uint64_t got = 0;
+#pragma unroll
+    for (int w = 0; w < kMoePairs / 64; ++w) {
+        const int lo = from - 64 * w, hi = to - 64 * w;
+        const uint64_t above = lo <= 0 ? ~0ull : lo >= 64 ? 0ull : ~0ull << lo;
+        const uint64_t below = hi <= 0 ? 0ull : hi >= 64 ? ~0ull : ~(~0ull << hi);
+        got |= m[w] & above & below;
+    }
+    return got != 0;
+}
 
-template <int ELEM, int BLOCK, bool SPLIT, bool POW2, int MAXQ>
+constexpr int kMoeUpWaves = 4, kMoeUpBudget = 40 * 1024;
+constexpr int kMoeDownWaves = 16;
+
+// ---------------------------------------------------------------------------
+// The gate and up projections: a workgroup for 16 columns of one expert, its
+// four waves sharing K.  blockIdx.y is a (token, choice) pair, of which the
+// first that names its expert does the work, or an expert where those are
+// fewer; the others leave.  (A wave for each 16 columns with all of K, whose
+// gate and up meet in registers, is slower: 4096 x 11008, 5 experts met 75 us
+// against 61, 4096 x 1536, 37 met 83 against 79: fewer, longer workgroups end
+// less evenly.)
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void put_hidden(const MoeLaunch& p, float gate, float up, float f, int pair, int64_t n)
+{
+    float h = gate * f;
+    with_act(p.act, [&](auto act) { h = act_value<decltype(act)::value>(h); });
+    h *= up * f;
+    // h as the sum of two bf16: its first eight bits, and what they leave, rounded
+    const uint32_t hi = f_bits(h) & 0xFFFF0000u;
+    const float left = h - bits_f(hi);
+    const int64_t to = (int64_t)pair * p.ffn + n;
+    p.h[to] = (uint16_t)(hi >> 16) | (h != h ? 0x40u : 0u);
+    p.h[to + (int64_t)p.m * p.top * p.ffn] = left == left ? (uint16_t)f32_to_bf16_rne(left) : (uint16_t)0;
+}
+
+template <int ELEM, int BLOCK, int SUB, bool SPLIT, bool POW2, int MAXR>
 __global__ __launch_bounds__(64 * kMoeUpWaves) void k_moe_up(MoeLaunch p)
 {
     constexpr int NW = kMoeUpWaves;
+    static_assert(64 * NW >= kMoePairs, "a thread for each pair");
     extern __shared__ __align__(16) uint8_t lds[];
-    __shared__ MoeTable t;
     __shared__ float sdec[256];
-    __shared__ uint16_t xrow[kMoePairs];
+    __shared__ uint64_t found[2][kMoePairs / 64];
+    __shared__ uint8_t pair[kMoeMaxTokens], token[kMoeMaxTokens];
     __shared__ float part[NW][2][256];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int pairs = p.m * p.top, y = blockIdx.y;
+    const bool by_pair = pairs <= p.experts;
+    const int e = by_pair ? p.ids[y] : y;
+    if (e < 0 || e >= p.experts) return;                   // the whole workgroup, here and below
+    const bool match = tid < pairs && p.ids[tid] == e;
     const float g = p.up.g[0], pw = split_pow2(g), gres = g / pw;
+    const float f = gres * (p.up.scale ? p.up.scale[e] : 1.0f);
     const ScaleFmt fw = device_fmt(p.up.fmt);
-    moe_table(p, t, *reinterpret_cast<MoeScratch*>(lds), tid);
-    const int a = blockIdx.y;
-    if (a >= t.active) return;            // the whole workgroup
     for (int c = tid; c < 256; c += 64 * NW) sdec[c] = scale_decode_any((uint32_t)c, fw) * pw;
-    if (tid < kMoePairs) xrow[tid] = t.tok[tid];
-    const int e = t.expert[a], b = t.start[a], cnt = t.start[a + 1] - b;
+    const uint64_t here = __builtin_amdgcn_ballot_w64(match);
+    if (lane == 0) found[0][wave] = here;
+    __syncthreads();
+    uint64_t all[kMoePairs / 64];
+#pragma unroll
+    for (int w = 0; w < kMoePairs / 64; ++w) all[w] = found[0][w];
+    if (by_pair ? any_bit(all, 0, y) : !any_bit(all, 0, kMoePairs)) return;
+    // a token that names the expert again has it once
+    const int tok = tid / p.top;
+    const bool keep = match && !any_bit(all, tok * p.top, tid);
+    const uint64_t kept = __builtin_amdgcn_ballot_w64(keep);
+    if (lane == 0) found[1][wave] = kept;
+    __syncthreads();
+    int before = __builtin_popcountll(kept & ((1ull << lane) - 1)), cnt = 0;
+#pragma unroll
+    for (int w = 0; w < kMoePairs / 64; ++w) {
+        const int n = __builtin_popcountll(found[1][w]);
+        before += w < wave ? n : 0;
+        cnt += n;
+    }
+    if (keep) {
+        pair[before] = (uint8_t)tid;
+        token[before] = (uint8_t)tok;
+    }
+    cnt = __builtin_amdgcn_readfirstlane(cnt);
     __syncthreads();
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     MoeSide s;
@@ -387,53 +382,149 @@ __global__ __launch_bounds__(64 * kMoeUpWaves) void k_moe_up(MoeLaunch p)
     s.x = p.x; s.ldx = p.ldx; s.plane = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) part[wave][i >> 2][4 * lane + (i & 3)] = 0.0f;
-    moe_class<MAXQ>(cnt, [&](auto q) {
-        moe_stream<NW, kMoeUpBudget, 2, decltype(q)::value, 1, ELEM, BLOCK, SPLIT, POW2>(
-            lds, s, t, xrow, sdec, a, 1, wave, lane, [&](int, const v4f (&acc)[2]) {
+    moe_rows<MAXR>(cnt, [&](auto rows) {
+        constexpr int XR = decltype(rows)::value;
+        using S = MoeSlot<2, XR, 1, ELEM, BLOCK, SUB>;
+        using Shape = MoeShape<S, NW, kMoeUpBudget>;
+        constexpr int NA = Shape::Waves;
+        const int nch = s.k / S::K, first = nch * wave / NA;
+        if (wave < NA)
+            moe_stream<Shape::D, 2, XR, 1, ELEM, BLOCK, SUB, SPLIT, POW2>(
+                lds + wave * (Shape::D * S::Bytes), s, sdec, first, nch * (wave + 1) / NA - first, lane,
+                [&](int) { return MoeExpert{e, cnt, token}; }, [&](int, const v4f (&acc)[2]) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) { part[wave][0][4 * lane + r] = acc[0][r]; part[wave][1][4 * lane + r] = acc[1][r]; }
-            });
+                    for (int r = 0; r < 4; ++r) {
+                        part[wave][0][4 * lane + r] = acc[0][r];
+                        part[wave][1][4 * lane + r] = acc[1][r];
+                    }
+                });
     });
     __syncthreads();
-    const float f = gres * (p.up.scale ? p.up.scale[e] : 1.0f);
     const int j = tid >> 4, n = tid & 15;
     if (j >= cnt) return;
     const int at = 4 * (16 * (j >> 2) + n) + (j & 3);
     float gate = 0.0f, up = 0.0f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) { gate += part[w][0][at]; up += part[w][1][at]; }
-    float h = gate * f;
-    with_act(p.act, [&](auto act) { h = act_value<decltype(act)::value>(h); });
-    h *= up * f;
-    // h as the sum of two bf16: its first eight bits, and what they leave, rounded
-    const uint32_t hi = f_bits(h) & 0xFFFF0000u;
-    const float left = h - bits_f(hi);
-    const int64_t to = (int64_t)t.row[b + j] * p.ffn + n0 + n;
-    p.h[to] = (uint16_t)(hi >> 16) | (h != h ? 0x40u : 0u);
-    p.h[to + (int64_t)p.m * p.top * p.ffn] = left == left ? (uint16_t)f32_to_bf16_rne(left) : (uint16_t)0;
+    put_hidden(p, gate, up, f, pair[j], n0 + n);
 }
 
-template <int ELEM, int BLOCK, bool SPLIT, bool POW2, int MAXQ>
+// ---------------------------------------------------------------------------
+// The down projection.  The table of all pairs by expert, built by each
+// workgroup: the active experts in order of their number of tokens' class (at
+// most 2, 4, 8, 16: each class has rings of its own depth, since a slot holds the
+// rows of its tokens), in a class by their first pair.
+// ---------------------------------------------------------------------------
+constexpr int kMoeClasses = 4;
+struct MoeTable {
+    int32_t count[kMoeClasses];           // active experts of a class
+    int32_t expert[kMoePairs];
+    uint8_t tokens[kMoePairs];
+    uint8_t pair[kMoePairs][kMoeMaxTokens];
+    uint8_t tok[kMoePairs];               // of a pair
+    float w[kMoePairs];                   // of a pair: the router's weight times the expert's scale
+};
+struct MoeScratch {
+    int32_t id[kMoePairs];
+    int32_t place[kMoePairs];             // of the active expert that a first pair stands for
+    int32_t waves[kMoePairs / 64][kMoeClasses];
+};
+
+// Called by all threads (at least 256); scratch may be the ring.  An id that a
+// token names again adds its weight to the first; one outside the experts is
+// dropped.
+__device__ __forceinline__ void moe_table(const MoeLaunch& p, MoeTable& t, MoeScratch& s, int tid, float gres)
+{
+    const int pairs = p.m * p.top;
+    const bool in = tid < pairs;
+    const int tok = in ? tid / p.top : 0, k = tid - tok * p.top;
+    float w = in ? p.weights[tid] : 0.0f;
+    int id = in ? p.ids[tid] : -1;
+    if (tid < kMoePairs) s.id[tid] = id;
+    __syncthreads();
+    bool again = false;
+    if (in) {
+        for (int j = 0; j < k; ++j) again |= s.id[tok * p.top + j] == id;
+        if (!again)
+            for (int j = k + 1; j < p.top; ++j)
+                if (s.id[tok * p.top + j] == id) w += p.weights[tok * p.top + j];
+    }
+    __syncthreads();
+    if (again || id < 0 || id >= p.experts) id = kNoExpert;
+    if (in) {
+        s.id[tid] = id;
+        t.w[tid] = w * (p.down.scale && id != kNoExpert ? gres * p.down.scale[id] : gres);
+        t.tok[tid] = (uint8_t)tok;
+    } else if (tid < kMoePairs) {
+        s.id[tid] = -1;
+    }
+    __syncthreads();
+    // of the same expert: all, those before this pair, the first
+    int n = 0, before = 0, first = kMoePairs;
+    if (in && id != kNoExpert) {
+        for (int q = 0; q < pairs; q += 4) {               // past the pairs: -1
+            const int4 o = *reinterpret_cast<const int4*>(&s.id[q]);
+            const int v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool same = v[i] == id;
+                n += same;
+                before += same && q + i < tid;
+                first = same && q + i < first ? q + i : first;
+            }
+        }
+    }
+    const bool lead = n > 0 && before == 0;
+    const int cls = n <= 2 ? 0 : n <= 4 ? 1 : n <= 8 ? 2 : 3;
+    int rank = 0;
+#pragma unroll
+    for (int c = 0; c < kMoeClasses; ++c) {
+        const uint64_t b = __builtin_amdgcn_ballot_w64(lead && cls == c);
+        if (cls == c) rank = __builtin_popcountll(b & ((1ull << (tid & 63)) - 1));
+        if ((tid & 63) == 0 && tid < kMoePairs) s.waves[tid >> 6][c] = __builtin_popcountll(b);
+    }
+    __syncthreads();
+    int base = 0;
+#pragma unroll
+    for (int c = 0; c < kMoeClasses; ++c) {
+        int all = 0;
+#pragma unroll
+        for (int u = 0; u < kMoePairs / 64; ++u) {
+            const int v = s.waves[u][c];
+            if (c == cls && u < (tid >> 6)) rank += v;
+            all += v;
+        }
+        if (c < cls) base += all;
+        if (tid == 0) t.count[c] = all;
+    }
+    if (lead) {
+        s.place[tid] = base + rank;
+        t.expert[base + rank] = id;
+        t.tokens[base + rank] = (uint8_t)n;
+    }
+    __syncthreads();
+    if (n > 0) t.pair[s.place[first]][before] = (uint8_t)tid;
+    __syncthreads();
+}
+
+// What the LDS has left for the rings beside the table, the scales and the sums.
+template <int MAXR>
+constexpr int kMoeDownBudget = 160 * 1024 - (int)sizeof(MoeTable) - 4 * 256 - 4 * 16 * MAXR * kMoeDownWaves - 64;
+
+template <int ELEM, int BLOCK, int SUB, bool SPLIT, bool POW2, int MAXR>
 __global__ __launch_bounds__(64 * kMoeDownWaves) void k_moe_down(MoeLaunch p)
 {
     constexpr int NW = kMoeDownWaves;
     extern __shared__ __align__(16) uint8_t lds[];
     __shared__ MoeTable t;
     __shared__ float sdec[256];
-    __shared__ float tot[NW][16][16];     // a wave's sums: token, column
+    __shared__ float tot[NW][MAXR][16];   // a wave's sums: token, column
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const float g = p.down.g[0], pw = split_pow2(g), gres = g / pw;
     const ScaleFmt fw = device_fmt(p.down.fmt);
-    moe_table(p, t, *reinterpret_cast<MoeScratch*>(lds), tid);
+    moe_table(p, t, *reinterpret_cast<MoeScratch*>(lds), tid, gres);
     for (int c = tid; c < 256; c += 64 * NW) sdec[c] = scale_decode_any((uint32_t)c, fw) * pw;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) (&tot[wave][0][0])[64 * i + lane] = 0.0f;
-    int most = 0;
-    for (int a = 0; a < t.active; ++a) {
-        const int n = t.start[a + 1] - t.start[a];
-        most = n > most ? n : most;
-    }
-    most = __builtin_amdgcn_readfirstlane(most);
+    for (int i = lane; i < 16 * MAXR; i += 64) (&tot[wave][0][0])[i] = 0.0f;
     __syncthreads();
     const int64_t n0 = (int64_t)blockIdx.x * 16;
     MoeSide s;
@@ -442,21 +533,53 @@ __global__ __launch_bounds__(64 * kMoeDownWaves) void k_moe_down(MoeLaunch p)
     s.row0 = s.row1 = (uint32_t)n0;
     s.k = (int32_t)p.ffn;
     s.x = p.h; s.ldx = p.ffn; s.plane = (int64_t)p.m * p.top * p.ffn;
-    moe_class<MAXQ>(most, [&](auto q) {
-        moe_stream<NW, kMoeDownBudget, 1, decltype(q)::value, 2, ELEM, BLOCK, SPLIT, POW2>(
-            lds, s, t, t.row, sdec, 0, t.active, wave, lane, [&](int a, const v4f (&acc)[1]) {
-                const int b = t.start[a], n = t.start[a + 1] - b;
-                const float f = gres * (p.down.scale ? p.down.scale[t.expert[a]] : 1.0f);
+    const int nch = s.k / (128 * SUB);
+    int base = 0;
+    auto run = [&](auto rows, int count) {
+        constexpr int XR = decltype(rows)::value;
+        using S = MoeSlot<1, XR, 2, ELEM, BLOCK, SUB>;
+        using Shape = MoeShape<S, NW, kMoeDownBudget<MAXR>>;
+        constexpr int NA = Shape::Waves;
+        const int a0 = base;
+        base += count;
+        if (count == 0 || wave >= NA) return;
+        // this wave's part of the class's (expert, chunk) list
+        const int items = count * nch, first = (int)((int64_t)items * wave / NA);
+        moe_stream<Shape::D, 1, XR, 2, ELEM, BLOCK, SUB, SPLIT, POW2>(
+            lds + wave * (Shape::D * S::Bytes), s, sdec, first, (int)((int64_t)items * (wave + 1) / NA) - first, lane,
+            [&](int a) { return MoeExpert{t.expert[a0 + a], t.tokens[a0 + a], t.pair[a0 + a]}; },
+            [&](int a, const v4f (&acc)[1]) {
+                const int n = t.tokens[a0 + a];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int j = 4 * (lane >> 4) + r;
                     if (j < n) {
-                        float& to = tot[wave][t.tok[b + j]][lane & 15];
-                        to = __builtin_fmaf(t.w[b + j] * f, acc[0][r], to);
+                        const int q = t.pair[a0 + a][j];
+                        float& to = tot[wave][t.tok[q]][lane & 15];
+                        to = __builtin_fmaf(t.w[q], acc[0][r], to);
                     }
                 }
             });
-    });
+    };
+    // a class's rings lie where another's did: a wave's own loads have landed and
+    // been read by then, but the classes cut the LDS differently
+    run(std::integral_constant<int, MAXR == 1 ? 1 : 2>{}, t.count[0]);
+    if constexpr (MAXR >= 4) {
+        if (t.count[1]) {
+            __syncthreads();
+            run(std::integral_constant<int, 4>{}, t.count[1]);
+        }
+    }
+    if constexpr (MAXR >= 16) {
+        if (t.count[2]) {
+            __syncthreads();
+            run(std::integral_constant<int, 8>{}, t.count[2]);
+        }
+        if (t.count[3]) {
+            __syncthreads();
+            run(std::integral_constant<int, 16>{}, t.count[3]);
+        }
+    }
     __syncthreads();
     if (tid >= 256) return;
     const int m = tid >> 4;
@@ -472,64 +595,71 @@ __global__ __launch_bounds__(64 * kMoeDownWaves) void k_moe_down(MoeLaunch p)
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-template <int NW, int BUDGET, int RG, int XP, int ELEM, int BLOCK, int XQ>
+// the largest of the rings that a launch may take
+template <int NW, int BUDGET, int RG, int XP, int ELEM, int BLOCK, int SUB, int MAXR>
 constexpr size_t ring_bytes()
 {
-    using R = MoeRing<RG, XQ, XP, ELEM, BLOCK>;
-    using Shape = MoeShape<R, NW>;
-    return (size_t)Shape::waves(BUDGET) * Shape::slots(BUDGET) * R::Bytes;
-}
-// the largest ring that an expert of the launch may take, and the sort before it
-template <int NW, int BUDGET, int RG, int XP, int ELEM, int BLOCK, int MAXQ>
-constexpr size_t lds_bytes()
-{
-    size_t b = sizeof(MoeScratch);
-    const size_t r0 = ring_bytes<NW, BUDGET, RG, XP, ELEM, BLOCK, 0>(), r1 = ring_bytes<NW, BUDGET, RG, XP, ELEM, BLOCK, 1>();
-    const size_t r2 = ring_bytes<NW, BUDGET, RG, XP, ELEM, BLOCK, 2>(), r4 = ring_bytes<NW, BUDGET, RG, XP, ELEM, BLOCK, 4>();
-    b = r0 > b ? r0 : b;
-    if (MAXQ >= 1) b = r1 > b ? r1 : b;
-    if (MAXQ >= 2) b = r2 > b ? r2 : b;
-    if (MAXQ >= 4) b = r4 > b ? r4 : b;
-    return b;
+    constexpr int b[5] = {MoeShape<MoeSlot<RG, 1, XP, ELEM, BLOCK, SUB>, NW, BUDGET>::Bytes,
+                          MoeShape<MoeSlot<RG, 2, XP, ELEM, BLOCK, SUB>, NW, BUDGET>::Bytes,
+                          MoeShape<MoeSlot<RG, 4, XP, ELEM, BLOCK, SUB>, NW, BUDGET>::Bytes,
+                          MoeShape<MoeSlot<RG, 8, XP, ELEM, BLOCK, SUB>, NW, BUDGET>::Bytes,
+                          MoeShape<MoeSlot<RG, 16, XP, ELEM, BLOCK, SUB>, NW, BUDGET>::Bytes};
+    size_t most = sizeof(MoeScratch);
+    for (int i = 0, r = 1; i < 5 && r <= MAXR; ++i, r *= 2) most = (size_t)b[i] > most ? (size_t)b[i] : most;
+    return most;
 }
 
-template <int ELEM, int BLOCK, bool SPLIT, bool POW2, int MAXQ>
+template <int ELEM, int BLOCK, int SUB, bool SPLIT, bool POW2, int MAXR>
 static hipError_t run_moe(const MoeLaunch& p, bool up, hipStream_t s)
 {
     if (up) {
-        constexpr size_t sh = lds_bytes<kMoeUpWaves, kMoeUpBudget, 2, 1, ELEM, BLOCK, MAXQ>();
-        static_assert(sh <= 64 * 1024, "LDS");
+        constexpr size_t sh = ring_bytes<kMoeUpWaves, kMoeUpBudget, 2, 1, ELEM, BLOCK, SUB, MAXR>();
+        static_assert(sh <= kMoeUpBudget, "LDS");
         const int most = p.m * p.top < p.experts ? p.m * p.top : p.experts;
-        hipLaunchKernelGGL((k_moe_up<ELEM, BLOCK, SPLIT, POW2, MAXQ>), dim3((unsigned)(p.ffn / 16), (unsigned)most),
+        if (sh + 16 * 1024 > 64 * 1024) {
+            const hipError_t e = allow_lds(k_moe_up<ELEM, BLOCK, SUB, SPLIT, POW2, MAXR>, sh);
+            if (e != hipSuccess) return e;
+        }
+        hipLaunchKernelGGL((k_moe_up<ELEM, BLOCK, SUB, SPLIT, POW2, MAXR>), dim3((unsigned)(p.ffn / 16), (unsigned)most),
                            dim3(64 * kMoeUpWaves), sh, s, p);
     } else {
-        constexpr size_t sh = lds_bytes<kMoeDownWaves, kMoeDownBudget, 1, 2, ELEM, BLOCK, MAXQ>();
-        static_assert(sh + sizeof(MoeTable) + 4 * (256 + 256 * kMoeDownWaves) <= 160 * 1024, "LDS");
-        const hipError_t e = allow_lds(k_moe_down<ELEM, BLOCK, SPLIT, POW2, MAXQ>, sh);
+        constexpr size_t sh = ring_bytes<kMoeDownWaves, kMoeDownBudget<MAXR>, 1, 2, ELEM, BLOCK, SUB, MAXR>();
+        static_assert(sh <= kMoeDownBudget<MAXR>, "LDS");
+        const hipError_t e = allow_lds(k_moe_down<ELEM, BLOCK, SUB, SPLIT, POW2, MAXR>, sh);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((k_moe_down<ELEM, BLOCK, SPLIT, POW2, MAXQ>), dim3((unsigned)(p.hidden / 16)),
+        hipLaunchKernelGGL((k_moe_down<ELEM, BLOCK, SUB, SPLIT, POW2, MAXR>), dim3((unsigned)(p.hidden / 16)),
                            dim3(64 * kMoeDownWaves), sh, s, p);
     }
     return hipGetLastError();
 }
 
-template <int ELEM, int BLOCK, bool SPLIT, bool POW2>
+template <int ELEM, int BLOCK, int SUB, bool SPLIT, bool POW2>
 static hipError_t run_moe_tokens(const MoeLaunch& p, bool up, hipStream_t s)
 {
-    if (p.m == 1) return run_moe<ELEM, BLOCK, SPLIT, POW2, 0>(p, up, s);
-    if (p.m <= 4) return run_moe<ELEM, BLOCK, SPLIT, POW2, 1>(p, up, s);
-    if (p.m <= 8) return run_moe<ELEM, BLOCK, SPLIT, POW2, 2>(p, up, s);
-    return run_moe<ELEM, BLOCK, SPLIT, POW2, 4>(p, up, s);
+    if (p.m == 1) return run_moe<ELEM, BLOCK, SUB, SPLIT, POW2, 1>(p, up, s);
+    if (p.m <= 4) return run_moe<ELEM, BLOCK, SUB, SPLIT, POW2, 4>(p, up, s);
+    return run_moe<ELEM, BLOCK, SUB, SPLIT, POW2, 16>(p, up, s);
+}
+
+// Chunks of two runs for the 4-bit grids: a load's rows are whole 128-byte
+// lines then (streaming alone, 37 experts of 4096 x 1536: 64 -> 54 us for gate
+// and up, 38 -> 32 for down; K that is an odd multiple of 128 takes one run.
+template <int ELEM, int BLOCK, bool SPLIT, bool POW2>
+static hipError_t run_moe_chunk(const MoeLaunch& p, bool up, hipStream_t s)
+{
+    if constexpr (ELEM <= 1)
+        if ((up ? p.hidden : p.ffn) % 256 == 0) return run_moe_tokens<ELEM, BLOCK, 2, SPLIT, POW2>(p, up, s);
+    return run_moe_tokens<ELEM, BLOCK, 1, SPLIT, POW2>(p, up, s);
 }
 
 template <int ELEM, int BLOCK>
 static hipError_t run_moe_scales(const MoeLaunch& p, bool up, hipStream_t s)
 {
     const MoeWeights& w = up ? p.up : p.down;
-    if (!wo_exact_in_bf16(ELEM, w.fmt)) return run_moe_tokens<ELEM, BLOCK, true, false>(p, up, s);
+    if (!wo_exact_in_bf16(ELEM, w.fmt)) return run_moe_chunk<ELEM, BLOCK, true, false>(p, up, s);
     if constexpr (ELEM == 0)
-        if (w.fmt.is_e8m0) return run_moe_tokens<ELEM, BLOCK, false, true>(p, up, s);
-    return run_moe_tokens<ELEM, BLOCK, false, false>(p, up, s);
+        if (w.fmt.is_e8m0) return run_moe_chunk<ELEM, BLOCK, false, true>(p, up, s);
+    return run_moe_chunk<ELEM, BLOCK, false, false>(p, up, s);
 }
 
 template <int ELEM>
@@ -559,12 +689,13 @@ hipError_t launch_moe(const MoeLaunch& p, hipStream_t s)
 
 // ---------------------------------------------------------------------------
 // The router's choice: a wave for each row, its experts' scores spread over
-// the lanes (at most 16 each), `top` rounds of the wave's largest.  Scores
-// are compared and divided in binary64: the order of two near scores plus
-// their biases is the binary64 formula's, where binary32's exponential would
-// turn neighbours round.
+// the lanes, NL each.  Up to 256 experts every lane counts how many keys are
+// above its own, from readlanes, which ranks them all at once (128 experts, top
+// 8: 3.9 us; eight rounds of the wave's largest, 6 cross-lane steps of three
+// values each, 5.7); more take the rounds.  Scores are compared and divided in
+// binary64: the order of two near scores plus their biases is the binary64
+// formula's, where binary32's exponential would turn neighbours round.
 // ---------------------------------------------------------------------------
-constexpr int kRouteLane = kMoeMaxRouted / 64;
 constexpr int kRouteWaves = 4;
 
 __device__ __forceinline__ uint64_t order_key(double v)
@@ -574,91 +705,135 @@ __device__ __forceinline__ uint64_t order_key(double v)
     return (u >> 63) ? ~u : u | 0x8000000000000000ull;
 }
 
+template <int NL>
 __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteLaunch p)
 {
     const int lane = threadIdx.x & 63;
     const int64_t row = (int64_t)blockIdx.x * kRouteWaves + (threadIdx.x >> 6);
     if (row >= p.rows) return;
     const int E = p.experts;
-    double score[kRouteLane];
-    uint64_t key[kRouteLane];             // 0: no candidate
-    double top = -INFINITY;
+    float z[NL];
+    double score[NL];
+    uint64_t key[NL];                     // 0: no candidate
+    float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kRouteLane; ++i) {
+    for (int i = 0; i < NL; ++i) {
         const int e = 64 * i + lane;
-        score[i] = -INFINITY;
-        if (64 * i < E && e < E) {
-            const float z = p.bf16 ? bf16_lo(((const uint16_t*)p.logits)[row * p.ld + e]) : ((const float*)p.logits)[row * p.ld + e];
-            score[i] = z;
-            top = fmax(top, (double)z);
-        }
-    }
-    if (!p.sigmoid) {
-#pragma unroll
-        for (int o = 32; o; o >>= 1) top = fmax(top, __shfl_xor(top, o));
+        z[i] = -INFINITY;
+        if (e < E) z[i] = p.bf16 ? bf16_lo(((const uint16_t*)p.logits)[row * p.ld + e]) : ((const float*)p.logits)[row * p.ld + e];
+        top = fmaxf(top, z[i]);
     }
     double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < kRouteLane; ++i) {
-        key[i] = 0;
-        if (64 * i >= E) continue;
-        const int e = 64 * i + lane;
-        const double z = score[i];
-        const bool in = e < E && z != -INFINITY;             // a masked expert is never chosen
-        // the largest logit's own score is 1 (also where it is infinite)
-        score[i] = !in ? 0.0 : p.sigmoid ? 1.0 / (1.0 + exp(-z)) : z == top ? 1.0 : exp(z - top);
-        sum += score[i];
-    }
     if (!p.sigmoid) {
 #pragma unroll
+        for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    }
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        const double v = z[i];
+        // a masked expert is never chosen; the largest logit's own score is 1 (also where it is infinite)
+        score[i] = z[i] == -INFINITY ? 0.0 : p.sigmoid ? 1.0 / (1.0 + exp(-v)) : z[i] == top ? 1.0 : exp(v - (double)top);
+        sum += score[i];
+    }
+    if (!p.sigmoid && (p.bias || !p.renormalize)) {        // else it cancels
+#pragma unroll
         for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) score[i] /= sum;
     }
 #pragma unroll
-    for (int i = 0; i < kRouteLane; ++i) {
-        if (64 * i >= E) continue;
+    for (int i = 0; i < NL; ++i) {
         const int e = 64 * i + lane;
-        if (e >= E) continue;
-        const float z = p.bf16 ? bf16_lo(((const uint16_t*)p.logits)[row * p.ld + e]) : ((const float*)p.logits)[row * p.ld + e];
-        if (!p.sigmoid) score[i] /= sum;
-        if (z == -INFINITY) continue;
+        key[i] = 0;
         // without a bias the scores' order is the logits', ties and underflow aside
-        key[i] = order_key(p.bias ? score[i] + (double)p.bias[e] : (double)z);
+        if (z[i] != -INFINITY) key[i] = order_key(p.bias ? score[i] + (double)p.bias[e < E ? e : 0] : (double)z[i]);
     }
-    // `top` rounds: the wave's largest key, of equal ones the lower expert
-    double mine = 0.0, total = 0.0;
-    int id = -1;
-    for (int k = 0; k < p.top; ++k) {
-        uint64_t best = 0;
-        int at = 0;
-        double s = 0.0;
+    int32_t* const ids = p.ids + row * p.top;
+    float* const weights = p.weights + row * p.top;
+    double total = 0.0;
+    int rank[NL], found = 0;
 #pragma unroll
-        for (int i = 0; i < kRouteLane; ++i)
-            if (key[i] > best) { best = key[i]; at = i; s = score[i]; }
-        int e = best ? 64 * at + lane : kNoExpert;
+    for (int i = 0; i < NL; ++i) {
+        rank[i] = kNoExpert;
+        found += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[i] != 0));
+    }
+    found = found < p.top ? found : p.top;
+    if constexpr (NL <= 4) {
 #pragma unroll
-        for (int o = 32; o; o >>= 1) {
-            const uint64_t b = ((uint64_t)(uint32_t)__shfl_xor((int)(best >> 32), o) << 32) | (uint32_t)__shfl_xor((int)best, o);
-            const int oe = __shfl_xor(e, o);
-            const double os = __shfl_xor(s, o);
-            if (b > best || (b == best && oe < e)) { best = b; e = oe; s = os; }
+        for (int i = 0; i < NL; ++i) rank[i] = 0;
+        auto count = [&](auto above) {
+#pragma unroll
+            for (int o = 0; o < NL; ++o) {
+                const uint32_t hi = (uint32_t)(key[o] >> 32), lo = (uint32_t)key[o];
+#pragma unroll 16
+                for (int j = 0; j < 64; ++j) {             // lanes past the experts hold no key
+                    const uint64_t k = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, j) << 32) |
+                                       (uint32_t)__builtin_amdgcn_readlane((int)lo, j);
+#pragma unroll
+                    for (int i = 0; i < NL; ++i) rank[i] += above(k, i, 64 * o + j);
+                }
+            }
+        };
+        count([&](uint64_t k, int i, int) { return k > key[i]; });
+        // without equal keys the ranks of n are 0 .. n - 1
+        int all = 0, sum_of = 0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            all += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[i] != 0));
+            sum_of += key[i] != 0 ? rank[i] : 0;
         }
-        if (best == 0) break;                                  // nothing left to choose
-        total += s;
-        if (lane == k) { id = e; mine = s; }
 #pragma unroll
-        for (int i = 0; i < kRouteLane; ++i)
-            if (64 * i + lane == e) key[i] = 0;
+        for (int o = 32; o; o >>= 1) sum_of += __shfl_xor(sum_of, o);
+        if (sum_of != all * (all - 1) / 2)                 // equal ones: the lower expert first
+            count([&](uint64_t k, int i, int e) { return k == key[i] && e < 64 * i + lane; });
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            if (key[i] == 0) rank[i] = kNoExpert;
+            if (rank[i] < p.top) total += score[i];
+        }
+#pragma unroll
+        for (int o = 32; o; o >>= 1) total += __shfl_xor(total, o);
+    } else {
+        for (int k = 0; k < found; ++k) {
+            uint64_t best = 0;
+            int e = kNoExpert;
+            double s = 0.0;
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                if (key[i] > best) { best = key[i]; e = 64 * i + lane; s = score[i]; }
+#pragma unroll
+            for (int o = 32; o; o >>= 1) {
+                const uint64_t b = ((uint64_t)(uint32_t)__shfl_xor((int)(best >> 32), o) << 32) | (uint32_t)__shfl_xor((int)best, o);
+                const int oe = __shfl_xor(e, o);
+                const double os = __shfl_xor(s, o);
+                if (b > best || (b == best && oe < e)) { best = b; e = oe; s = os; }
+            }
+            total += s;
+#pragma unroll
+            for (int i = 0; i < NL; ++i)
+                if (64 * i + lane == e) { rank[i] = k; key[i] = 0; }
+        }
     }
-    if (lane >= p.top) return;
-    double w = mine;
-    if (p.renormalize) w = total == 0.0 ? 0.0 : mine / total;
-    p.ids[row * p.top + lane] = id;
-    p.weights[row * p.top + lane] = id < 0 ? 0.0f : (float)(w * (double)p.scale);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+        if (rank[i] >= p.top) continue;
+        const double w = !p.renormalize ? score[i] : total == 0.0 ? 0.0 : score[i] / total;
+        ids[rank[i]] = 64 * i + lane;
+        weights[rank[i]] = (float)(w * (double)p.scale);
+    }
+    if (lane >= found && lane < p.top) {
+        ids[lane] = -1;
+        weights[lane] = 0.0f;
+    }
 }
 
 hipError_t launch_moe_route(const RouteLaunch& p, hipStream_t s)
 {
-    hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((p.rows + kRouteWaves - 1) / kRouteWaves)), dim3(64 * kRouteWaves), 0, s, p);
+    const dim3 grid((unsigned)((p.rows + kRouteWaves - 1) / kRouteWaves)), threads(64 * kRouteWaves);
+    if (p.experts <= 64) hipLaunchKernelGGL((k_moe_route<1>), grid, threads, 0, s, p);
+    else if (p.experts <= 128) hipLaunchKernelGGL((k_moe_route<2>), grid, threads, 0, s, p);
+    else if (p.experts <= 256) hipLaunchKernelGGL((k_moe_route<4>), grid, threads, 0, s, p);
+    else hipLaunchKernelGGL((k_moe_route<kMoeMaxRouted / 64>), grid, threads, 0, s, p);
     return hipGetLastError();
 }
 
