@@ -140,7 +140,7 @@ def lib():
         "fp4_moe_route": (i32, [vp, i32, i64, i64, i64, i32, i32, vp, i32, f32, vp, vp, vp]),
         "fp4_moe_workspace": (i64, [i64, i32, i64]),
         "fp4_moe": (i32, [vp, i64, i64, vp, vp, vp, i32, i32, vp, i64, vp, i64, vp, i64, vp]),
-        "fp4_distill_workspace": (i64, [i64, i64]),
+        "fp4_distill_workspace": (i64, [i64, i64, i32]),
         "fp4_distill_loss": (i32, [vp, i32, i64, i64, i64, vp, vp, i32, f32, i32, vp, vp, vp, i64, vp]),
         "fp4_distill_loss_backward": (i32, [vp, i32, i64, i64, i64, vp, vp, i32, f32, i32, vp, vp, vp, i64, vp]),
     }
@@ -232,8 +232,7 @@ class QTensor:
         qb = self.rows * (self.cols * ELEMENT_BITS[self.element] // 8)
         if not (self.q.is_contiguous() and self.scales.is_contiguous() and self.tensor_scale.is_contiguous()):
             raise ValueError("QTensor buffers must be contiguous")
-        if self.q.numel() * self.q.element_size() < qb or \
-                self.scales.numel() * self.scales.element_size() < self.rows * (self.cols // self.block) or \
+        if self.q.nbytes < qb or self.scales.nbytes < self.rows * (self.cols // self.block) or \
                 self.tensor_scale.numel() < 2:
             raise ValueError(f"QTensor buffers are smaller than a [{self.rows}, {self.cols}] tensor on the "
                              f"{self.element} grid needs")
@@ -849,8 +848,26 @@ def _epilogue(what: str, m: int, n: int, bias, act, mul, residual) -> list:
     return args
 
 
+def _bf16_empty(rows: int, cols: int, dev: torch.device, *like) -> torch.Tensor:
+    """A bf16 [rows, cols]: making one like a tensor at hand takes half the time."""
+    for t in like:
+        if t is not None:
+            return _empty_as(t)
+    return torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+
+
 def _given(*tensors) -> list:
     return [t for t in tensors if t is not None]
+
+
+def _one_device(what: str, *tensors: torch.Tensor) -> torch.device:
+    """_on_device for calls whose launches take a few microseconds: one look at each tensor."""
+    try:
+        index = tensors[0].get_device()
+        same = index >= 0 and all([t.get_device() == index for t in tensors])
+    except AttributeError:
+        same = False
+    return tensors[0].device if same else _on_device(what, *tensors)
 
 
 def fp4_gemm_epilogue(a: QTensor, b: QTensor, bias: torch.Tensor | None = None, act: str = "none",
@@ -864,12 +881,12 @@ def fp4_gemm_epilogue(a: QTensor, b: QTensor, bias: torch.Tensor | None = None, 
     m, n = a.rows, b.rows
     args = _epilogue(what, m, n, bias, act, mul, residual)
     ld = None if out is None else _bf16_rows(what, "out", out, m, n)
-    dev = _on_device(what, a.q, a.scales, a.tensor_scale, b.q, b.scales, b.tensor_scale, *_given(bias, mul, residual, out))
+    dev = _one_device(what, a.q, a.scales, a.tensor_scale, b.q, b.scales, b.tensor_scale, *_given(bias, mul, residual, out))
     ta, tb, L = a.packed(), b.packed(), lib()
     with _allocating(stream, dev):
         if out is None:
-            out, ld = torch.empty((m, n), dtype=torch.bfloat16, device=dev), max(n, 1)
-        pre = torch.empty((m, n), dtype=torch.bfloat16, device=dev) if save_pre else None
+            out, ld = _bf16_empty(m, n, dev, mul, residual), max(n, 1)
+        pre = _bf16_empty(m, n, dev, out) if save_pre else None
         if m == 0 or n == 0:
             return out, pre
         ws = _space(L.fp4_gemm_epilogue_workspace(ta, tb), dev, what)
@@ -889,11 +906,11 @@ def fp4_wo_gemm_epilogue(x: torch.Tensor, w: QTensor, bias: torch.Tensor | None 
     ldx = _bf16_rows(what, "x", x, m, w.cols)
     args = _EPILOGUE_ARGS.pack(*_epilogue(what, m, n, bias, act, mul, residual), 0, 0)
     ld = max(n, 1) if out is None else _bf16_rows(what, "out", out, m, n)
-    dev = _on_device(what, x, w.q, w.scales, w.tensor_scale, *_given(bias, mul, residual, out))
+    dev = _one_device(what, x, w.q, w.scales, w.tensor_scale, *_given(bias, mul, residual, out))
     tw = w.packed()
     with _allocating(stream, dev):
         if out is None:
-            out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+            out = _bf16_empty(m, n, dev, mul, residual)
         st = lib().fp4_wo_gemm_epilogue(x.data_ptr(), ldx, m, tw, args, out.data_ptr(), ld, _stream(stream, dev))
     _check(st, what)
     return out
@@ -923,7 +940,7 @@ def fp4_epilogue_backward(dy: torch.Tensor, pre: torch.Tensor | None, act: str =
         raise ValueError(f"{what}: pre is needed with an activation or mul")
     ld_pre = _bf16_rows(what, "pre", pre, m, n) if reads else 0
     ld_mul = 0 if mul is None else _bf16_rows(what, "mul", mul, m, n)
-    dev = _on_device(what, dy, *_given(pre if reads else None, mul))
+    dev = _one_device(what, dy, *_given(pre if reads else None, mul))
     if n == 0:
         return EpilogueGrads(_empty_as(dy), torch.empty(0, dtype=torch.float32, device=dev) if bias else None,
                              None if mul is None else _empty_as(mul))
@@ -954,10 +971,10 @@ def fp4_moe_route(logits: torch.Tensor, top: int, score: str = "softmax", bias: 
     n, e = logits.shape
     if bias is not None and not _is_vector(bias, e, torch.float32):
         raise ValueError(f"{what}: bias must be float32 [{e}]")
-    dev = _on_device(what, logits, *(() if bias is None else (bias,)))
+    dev = _one_device(what, logits, *(() if bias is None else (bias,)))
     with _allocating(stream, dev):
         ids = torch.empty((n, max(top, 0)), dtype=torch.int32, device=dev)
-        weights = torch.empty((n, max(top, 0)), dtype=torch.float32, device=dev)
+        weights = torch.empty_like(ids, dtype=torch.float32)
         st = lib().fp4_moe_route(logits.data_ptr(), DTYPE[logits.dtype], _ld(logits), n, e, top, sc, _ptr(bias),
                                  int(renormalize), scale, ids.data_ptr(), weights.data_ptr(), _stream(stream, dev))
     _check(st, what)
@@ -1009,11 +1026,11 @@ def fp4_moe(x: torch.Tensor, bank: MoeBank, ids: torch.Tensor, weights: torch.Te
         raise ValueError(f"{what}: ids must be int32 and weights float32, both dense [{m}, top]")
     ld_res = 0 if residual is None else _bf16_rows(what, "residual", residual, m, h)
     ld = h if out is None else _bf16_rows(what, "out", out, m, h)
-    dev = _on_device(what, x, ids, weights, *bank.tensors(), *_given(residual, out))
+    dev = _one_device(what, x, ids, weights, *bank.tensors(), *_given(residual, out))
     top, L = ids.shape[1], lib()
     with _allocating(stream, dev):
         if out is None:
-            out = torch.empty((m, h), dtype=torch.bfloat16, device=dev)
+            out = _empty_as(x)
         ws = _space(L.fp4_moe_workspace(m, top, f), dev, what)
         st = L.fp4_moe(x.data_ptr(), ldx, m, tb, ids.data_ptr(), weights.data_ptr(), top, a, _ptr(residual), ld_res,
                        out.data_ptr(), ld, _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream, dev))
@@ -1048,11 +1065,11 @@ def fp4_distill_loss(logits: torch.Tensor, top_ids: torch.Tensor, top_logprobs: 
     divides the listed probabilities by their sum."""
     what = "fp4_distill_loss"
     r = _distill(what, logits, top_ids, top_logprobs, rest)
-    dev = _on_device(what, logits, top_ids, top_logprobs)
+    dev = _one_device(what, logits, top_ids, top_logprobs)
     n, v = logits.shape
     L = lib()
     with _allocating(stream, dev):
-        ws = _space(L.fp4_distill_workspace(n, v), dev, what)
+        ws = _space(L.fp4_distill_workspace(n, v, DTYPE[logits.dtype]), dev, what)
         loss = torch.empty(n, dtype=torch.float32, device=dev)
         stats = torch.empty((n, 7), dtype=torch.float32, device=dev)
         st = L.fp4_distill_loss(logits.data_ptr(), DTYPE[logits.dtype], _ld(logits), n, v, top_ids.data_ptr(),
@@ -1075,7 +1092,7 @@ def fp4_distill_loss_backward(logits: torch.Tensor, top_ids: torch.Tensor, top_l
         raise ValueError(f"{what}: grad_loss must be float32 [{n}]")
     if tuple(saved.stats.shape) != (n, 7) or saved.stats.dtype != torch.float32 or not saved.stats.is_contiguous():
         raise ValueError(f"{what}: saved is not the result of a forward call on these logits")
-    dev = _on_device(what, logits, top_ids, top_logprobs, saved.stats, grad_loss, *(() if out is None else (out,)))
+    dev = _one_device(what, logits, top_ids, top_logprobs, saved.stats, grad_loss, *(() if out is None else (out,)))
     with _allocating(stream, dev):
         if out is None:
             out = _empty_as(logits)

@@ -132,7 +132,8 @@ int64_t fp4_epilogue_workspace(int64_t rows, int64_t cols)
 {
     if (rows < 0 || cols < 1) return FP4_ERR_SHAPE;
     if (cols > kMaxGradCols || rows > kMaxElems / cols) return FP4_ERR_UNSUPPORTED;
-    return up16(4 * epilogue_groups(rows, cols) * cols);
+    const int64_t groups = epilogue_groups(rows, cols);
+    return groups == 1 ? 0 : up16(4 * groups * cols);
 }
 
 fp4_status fp4_epilogue_backward(const uint16_t* dy, int64_t ld_dy, const uint16_t* pre, int64_t ld_pre,
@@ -213,6 +214,7 @@ fp4_status fp4_moe(const uint16_t* x, int64_t ldx, int64_t m, const fp4_moe_bank
     if (m < 1 || m > kMoeMaxTokens || top > kMoeMaxTop || bank->experts > kMaxExperts) return FP4_ERR_UNSUPPORTED;
     const int64_t hidden = bank->gate_up.cols, ffn = bank->down.cols, experts = bank->experts;
     if (top < 1 || experts < 1 || hidden < 1 || ffn < 1) return FP4_ERR_SHAPE;
+    if (hidden > kMaxElems || ffn > kMaxElems) return FP4_ERR_UNSUPPORTED;     // the products below stay far from 63 bits
     if ((st = check_experts(&bank->gate_up, bank->up_scale, experts, 2 * ffn, &p.up)) != FP4_OK) return st;
     if ((st = check_experts(&bank->down, bank->down_scale, experts, hidden, &p.down)) != FP4_OK) return st;
     if (ldx < hidden || ldy < hidden || (residual && ld_residual < hidden)) return FP4_ERR_SHAPE;
@@ -233,11 +235,12 @@ fp4_status fp4_moe(const uint16_t* x, int64_t ldx, int64_t m, const fp4_moe_bank
 }
 
 // ---------------------------------------------------------------------------
-int64_t fp4_distill_workspace(int64_t rows, int64_t vocab)
+int64_t fp4_distill_workspace(int64_t rows, int64_t vocab, int32_t dtype)
 {
+    if (!dtype_ok(dtype)) return FP4_ERR_INVALID_ARG;
     if (rows < 0 || vocab < 1) return FP4_ERR_SHAPE;
     if (rows >= kMaxLineRows || vocab > kMaxDistillVocab) return FP4_ERR_UNSUPPORTED;
-    const int64_t pieces = distill_pieces(rows, vocab);
+    const int64_t pieces = distill_pieces(rows, vocab, esize(dtype));
     return pieces == 1 ? 0 : up16(8 * rows * pieces);
 }
 
@@ -249,7 +252,7 @@ fp4_status fp4_distill_loss(const void* logits, int32_t dtype, int64_t ld, int64
     if (st != FP4_OK) return st;
     if (rows && (!loss || !stats)) return FP4_ERR_INVALID_ARG;
     if (!aligned(loss, 4) || !aligned(stats, 4)) return FP4_ERR_ALIGN;
-    if ((st = check_space(workspace, workspace_bytes, fp4_distill_workspace(rows, vocab))) != FP4_OK) return st;
+    if ((st = check_space(workspace, workspace_bytes, fp4_distill_workspace(rows, vocab, dtype))) != FP4_OK) return st;
     if (rows == 0) return FP4_OK;
     DistillLaunch p{};
     p.logits = logits; p.bf16 = dtype == FP4_DTYPE_BF16; p.ld = ld; p.rows = rows; p.vocab = vocab;
@@ -257,7 +260,7 @@ fp4_status fp4_distill_loss(const void* logits, int32_t dtype, int64_t ld, int64
     p.inv_temperature = 1.0f / temperature; p.renormalize = rest == FP4_DISTILL_RENORMALIZE;
     p.loss = loss; p.stats = stats;
     p.part = (float*)workspace;
-    return hip_status(launch_distill(p, distill_pieces(rows, vocab), (hipStream_t)stream));
+    return hip_status(launch_distill(p, distill_pieces(rows, vocab, esize(dtype)), (hipStream_t)stream));
 }
 
 fp4_status fp4_distill_loss_backward(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,

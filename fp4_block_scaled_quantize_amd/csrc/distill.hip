@@ -403,11 +403,15 @@ __global__ __launch_bounds__(kDsThreads) void k_distill_backward(DistillGradLaun
 // ---------------------------------------------------------------------------
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Pieces of a row: as many as token log probabilities take, and at most
-// kDsMost elements each, whose bitmap must fit the LDS.
-int64_t distill_pieces(int64_t rows, int64_t vocab)
+// A row is one workgroup's where the rows alone fill the device, and also where
+// it is at most 512 KiB: 16 waves read it at what a CU takes, and the second
+// launch, which joins the pieces, costs more than that (61 rows of 50257,
+// binary32: 7.9 + 5.1 us in nine pieces).  Longer rows are cut as the token log
+// probabilities' are, and a piece has at most kDsMost elements, whose bitmap must
+// fit the LDS.
+int64_t distill_pieces(int64_t rows, int64_t vocab, int64_t esize)
 {
-    const int64_t n = logprob_pieces(rows, vocab), least = cdiv(vocab, kDsMost);
+    const int64_t n = vocab * esize <= 512 * 1024 ? 1 : logprob_pieces(rows, vocab), least = cdiv(vocab, kDsMost);
     return n > least ? n : least;
 }
 
@@ -418,8 +422,9 @@ static hipError_t run_distill(DistillLaunch p, int64_t pieces, hipStream_t s)
     pieces = cdiv(p.vocab, p.piece);
     const dim3 grid((unsigned)p.rows, (unsigned)pieces);
     const size_t sh = (size_t)cdiv(p.piece < p.vocab ? p.piece : p.vocab, 32) * 4;
-    // a short row is one wave's, as in the token log probabilities
-    if (pieces == 1 && p.vocab <= 16384) hipLaunchKernelGGL((k_distill_rows<BF16, 64>), grid, dim3(64), sh, s, p);
+    // a short row of many is one wave's, as in the token log probabilities
+    if (pieces == 1 && p.rows < 512) hipLaunchKernelGGL((k_distill_rows<BF16, 1024>), grid, dim3(1024), sh, s, p);
+    else if (pieces == 1 && p.vocab <= 16384) hipLaunchKernelGGL((k_distill_rows<BF16, 64>), grid, dim3(64), sh, s, p);
     else hipLaunchKernelGGL((k_distill_rows<BF16, 256>), grid, dim3(256), sh, s, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || pieces == 1) return e;

@@ -6,10 +6,16 @@
 //
 // in binary32, each output rounded once.  The activations, with s(x) = 1 /
 // (1 + e^-x) and Phi the normal distribution:
-//   relu max(v, 0); silu v s(v); gelu v Phi(v) = v erfc(-v / sqrt 2) / 2;
+//   relu max(v, 0); silu v s(v); gelu v Phi(v);
 //   gelu_tanh v (1 + tanh u) / 2 = v s(2 u), u = sqrt(2 / pi) (v + 0.044715 v^3)
 // The last two are taken in the forms that keep their small values' bits at
-// far negative v, where 1 + erf and 1 + tanh cancel.
+// far negative v, where 1 + erf and 1 + tanh cancel: Phi there is its tail
+//   Phi(-a) = exp(-a^2 / 2) R(a),  R(a) = exp(a^2 / 2) Phi(-a), a >= 0,
+// and R a polynomial in t = 1 / (1 + 0.35 a) times t, whose coefficients were
+// fitted to R over 0 <= a <= 14.5 for the least relative error (3.2e-8;
+// with its binary32 evaluation 3.7e-7 of the tail).  The library's erfc takes
+// about five times the instructions (a gelu over 8192 x 11008 products of 4096,
+// MXFP4, 362 us; silu 262).
 #pragma once
 
 #include <type_traits>
@@ -31,12 +37,37 @@ __device__ __forceinline__ Logistic logistic(float x)
     return x >= 0.0f || x != x ? Logistic{r, l} : Logistic{l, r};
 }
 
+// {Phi(-|v|), exp(-v^2 / 2)}; nothing of either is left in binary32 past 16
+struct Tail { float phi, e; };
+__device__ __forceinline__ Tail normal_tail(float v)
+{
+    const float a = fminf(fabsf(v), 16.0f);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.35f, a, 1.0f));
+    float r = -0.029157895594835f;
+    r = __builtin_fmaf(r, t, 0.144030973315239f);
+    r = __builtin_fmaf(r, t, -0.255839109420776f);
+    r = __builtin_fmaf(r, t, 0.159319803118706f);
+    r = __builtin_fmaf(r, t, -0.023212423548102f);
+    r = __builtin_fmaf(r, t, 0.105552531778812f);
+    r = __builtin_fmaf(r, t, 0.119821280241013f);
+    r = __builtin_fmaf(r, t, 0.139863520860672f);
+    r = __builtin_fmaf(r, t, 0.139621302485466f);
+    // exp(-a^2 / 2): the square's and the product's roundings put back
+    constexpr float k = -0.72134752044448170368f, klo = (float)(-0.72134752044448170368 - (double)k);
+    const float s = a * a, lo = __builtin_fmaf(a, a, -s), x = s * k;
+    const float left = __builtin_fmaf(s, k, -x) + __builtin_fmaf(lo, k, s * klo);
+    float e = __builtin_amdgcn_exp2f(x);
+    e = __builtin_fmaf(e, left * 0.69314718055994530942f, e);
+    return Tail{e * (t * r), e};
+}
+__device__ __forceinline__ float normal_cdf(float v, const Tail& t) { return v >= 0.0f ? 1.0f - t.phi : t.phi; }
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float v)
 {
     if (ACT == kActRelu) return v < 0.0f ? 0.0f : v;         // NaN stays NaN
     if (ACT == kActSilu) return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-v * kEpiLog2e));
-    if (ACT == kActGelu) return 0.5f * v * erfcf(v * -0.70710678118654752440f);
+    if (ACT == kActGelu) return v * normal_cdf(v, normal_tail(v));
     if (ACT == kActGeluTanh) {
         const float u = kTanhOuter * __builtin_fmaf(kTanhCubic * v * v, v, v);
         return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-u * kEpiLog2e));
@@ -54,9 +85,10 @@ __device__ __forceinline__ float act_slope(float v)
         const Logistic s = logistic(v);
         return __builtin_fmaf(v * s.up, s.down, s.up);
     }
-    if (ACT == kActGelu)
-        return __builtin_fmaf(v * 0.39894228040143267794f, __builtin_amdgcn_exp2f(-0.5f * kEpiLog2e * v * v),
-                              0.5f * erfcf(v * -0.70710678118654752440f));
+    if (ACT == kActGelu) {
+        const Tail t = normal_tail(v);
+        return __builtin_fmaf(v * 0.39894228040143267794f, t.e, normal_cdf(v, t));
+    }
     if (ACT == kActGeluTanh) {
         const float x = v > 30.0f ? 30.0f : v < -30.0f ? -30.0f : v;
         const float q = kTanhCubic * x * x;

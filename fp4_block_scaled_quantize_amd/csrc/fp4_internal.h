@@ -348,7 +348,7 @@ struct DistillLaunch {
     float* part;               // [rows, pieces, 2]
     int64_t piece;
 };
-int64_t distill_pieces(int64_t rows, int64_t vocab);
+int64_t distill_pieces(int64_t rows, int64_t vocab, int64_t esize);
 hipError_t launch_distill(const DistillLaunch& p, int64_t pieces, hipStream_t s);
 
 struct DistillGradLaunch {

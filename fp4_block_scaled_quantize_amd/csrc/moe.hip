@@ -302,7 +302,12 @@ __device__ __forceinline__ bool any_bit(const uint64_t (&m)[kMoePairs / 64], int
     return got != 0;
 }
 
-constexpr int kMoeUpWaves = 4, kMoeUpBudget = 40 * 1024;
+// Rings of 40 KiB, so that three workgroups share a CU (52 KiB, and two: 4096 x
+// 11008, 5 experts met, 55 us against 48); for one token, whose few workgroups
+// do not fill the CUs so often, deeper rings and two.
+constexpr int kMoeUpWaves = 4;
+template <int MAXR>
+constexpr int kMoeUpBudget = (MAXR == 1 ? 68 : 40) * 1024;
 constexpr int kMoeDownWaves = 16;
 
 // ---------------------------------------------------------------------------
@@ -385,7 +390,7 @@ __global__ __launch_bounds__(64 * kMoeUpWaves) void k_moe_up(MoeLaunch p)
     moe_rows<MAXR>(cnt, [&](auto rows) {
         constexpr int XR = decltype(rows)::value;
         using S = MoeSlot<2, XR, 1, ELEM, BLOCK, SUB>;
-        using Shape = MoeShape<S, NW, kMoeUpBudget>;
+        using Shape = MoeShape<S, NW, kMoeUpBudget<MAXR>>;
         constexpr int NA = Shape::Waves;
         const int nch = s.k / S::K, first = nch * wave / NA;
         if (wave < NA)
@@ -507,6 +512,38 @@ __device__ __forceinline__ void moe_table(const MoeLaunch& p, MoeTable& t, MoeSc
     __syncthreads();
 }
 
+// One token's pairs, by the first wave: every expert that it names has one.
+__device__ __forceinline__ void moe_table_one(const MoeLaunch& p, MoeTable& t, int tid, float gres)
+{
+    if (tid < 64) {
+        const bool in = tid < p.top;
+        const int id = in ? p.ids[tid] : -1;
+        float w = in ? p.weights[tid] : 0.0f;
+        bool again = false;
+        float more = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kMoeMaxTop; ++j) {             // lanes past the choices: -1
+            const bool same = __builtin_amdgcn_readlane(id, j) == id;
+            const float wj = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(w), j));
+            again |= same && j < tid;
+            if (same && j > tid) more += wj;
+        }
+        w += more;
+        const bool lead = in && !again && id >= 0 && id < p.experts;
+        const uint64_t all = __builtin_amdgcn_ballot_w64(lead);
+        if (lead) {
+            const int a = __builtin_popcountll(all & ((1ull << tid) - 1));
+            t.expert[a] = id;
+            t.tokens[a] = 1;
+            t.pair[a][0] = (uint8_t)tid;
+            t.tok[tid] = 0;
+            t.w[tid] = w * (p.down.scale ? gres * p.down.scale[id] : gres);
+        }
+        if (tid < kMoeClasses) t.count[tid] = tid == 0 ? __builtin_popcountll(all) : 0;
+    }
+    __syncthreads();
+}
+
 // What the LDS has left for the rings beside the table, the scales and the sums.
 template <int MAXR>
 constexpr int kMoeDownBudget = 160 * 1024 - (int)sizeof(MoeTable) - 4 * 256 - 4 * 16 * MAXR * kMoeDownWaves - 64;
@@ -522,7 +559,8 @@ __global__ __launch_bounds__(64 * kMoeDownWaves) void k_moe_down(MoeLaunch p)
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const float g = p.down.g[0], pw = split_pow2(g), gres = g / pw;
     const ScaleFmt fw = device_fmt(p.down.fmt);
-    moe_table(p, t, *reinterpret_cast<MoeScratch*>(lds), tid, gres);
+    if (MAXR == 1) moe_table_one(p, t, tid, gres);
+    else moe_table(p, t, *reinterpret_cast<MoeScratch*>(lds), tid, gres);
     for (int c = tid; c < 256; c += 64 * NW) sdec[c] = scale_decode_any((uint32_t)c, fw) * pw;
     for (int i = lane; i < 16 * MAXR; i += 64) (&tot[wave][0][0])[i] = 0.0f;
     __syncthreads();
@@ -613,8 +651,8 @@ template <int ELEM, int BLOCK, int SUB, bool SPLIT, bool POW2, int MAXR>
 static hipError_t run_moe(const MoeLaunch& p, bool up, hipStream_t s)
 {
     if (up) {
-        constexpr size_t sh = ring_bytes<kMoeUpWaves, kMoeUpBudget, 2, 1, ELEM, BLOCK, SUB, MAXR>();
-        static_assert(sh <= kMoeUpBudget, "LDS");
+        constexpr size_t sh = ring_bytes<kMoeUpWaves, kMoeUpBudget<MAXR>, 2, 1, ELEM, BLOCK, SUB, MAXR>();
+        static_assert(sh <= kMoeUpBudget<MAXR>, "LDS");
         const int most = p.m * p.top < p.experts ? p.m * p.top : p.experts;
         if (sh + 16 * 1024 > 64 * 1024) {
             const hipError_t e = allow_lds(k_moe_up<ELEM, BLOCK, SUB, SPLIT, POW2, MAXR>, sh);
@@ -688,13 +726,14 @@ hipError_t launch_moe(const MoeLaunch& p, hipStream_t s)
 }
 
 // ---------------------------------------------------------------------------
-// The router's choice: a wave for each row, its experts' scores spread over
-// the lanes, NL each.  Up to 256 experts every lane counts how many keys are
-// above its own, from readlanes, which ranks them all at once (128 experts, top
-// 8: 3.9 us; eight rounds of the wave's largest, 6 cross-lane steps of three
-// values each, 5.7); more take the rounds.  Scores are compared and divided in
-// binary64: the order of two near scores plus their biases is the binary64
-// formula's, where binary32's exponential would turn neighbours round.
+// The router's choice: a workgroup for each row, whose four waves all hold its
+// experts' scores, NL a lane.  Up to 256 experts each wave counts, for every key,
+// how many of a quarter of the keys are above it, from readlanes, and the counts
+// add up to the keys' ranks (128 experts, top 8: 4.3 us; one wave with all keys
+// 6.0; rounds of the wave's largest, six cross-lane steps of three values each,
+// 7.4).  More experts take the rounds, by the first wave.  Scores are compared
+// and divided in binary64: the order of two near scores plus their biases is the
+// binary64 formula's, where binary32's exponential would turn neighbours round.
 // ---------------------------------------------------------------------------
 constexpr int kRouteWaves = 4;
 
@@ -708,9 +747,11 @@ __device__ __forceinline__ uint64_t order_key(double v)
 template <int NL>
 __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteLaunch p)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * kRouteWaves + (threadIdx.x >> 6);
-    if (row >= p.rows) return;
+    constexpr bool RANK = NL <= 4;
+    __shared__ int32_t part[RANK ? kRouteWaves : 1][RANK ? 64 * NL : 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t row = blockIdx.x;
+    if (!RANK && wave) return;
     const int E = p.experts;
     float z[NL];
     double score[NL];
@@ -758,15 +799,17 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteLaunch p)
         found += __builtin_popcountll(__builtin_amdgcn_ballot_w64(key[i] != 0));
     }
     found = found < p.top ? found : p.top;
-    if constexpr (NL <= 4) {
+    if constexpr (RANK) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) rank[i] = 0;
+        // the wave's quarter of every lane's keys; lanes past the experts hold none
         auto count = [&](auto above) {
 #pragma unroll
             for (int o = 0; o < NL; ++o) {
                 const uint32_t hi = (uint32_t)(key[o] >> 32), lo = (uint32_t)key[o];
-#pragma unroll 16
-                for (int j = 0; j < 64; ++j) {             // lanes past the experts hold no key
+#pragma unroll
+                for (int u = 0; u < 64 / kRouteWaves; ++u) {
+                    const int j = 64 / kRouteWaves * wave + u;
                     const uint64_t k = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, j) << 32) |
                                        (uint32_t)__builtin_amdgcn_readlane((int)lo, j);
 #pragma unroll
@@ -774,7 +817,19 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteLaunch p)
                 }
             }
         };
+        auto join = [&] {
+#pragma unroll
+            for (int i = 0; i < NL; ++i) part[wave][64 * i + lane] = rank[i];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                rank[i] = 0;
+#pragma unroll
+                for (int w = 0; w < kRouteWaves; ++w) rank[i] += part[w][64 * i + lane];
+            }
+        };
         count([&](uint64_t k, int i, int) { return k > key[i]; });
+        join();
         // without equal keys the ranks of n are 0 .. n - 1
         int all = 0, sum_of = 0;
 #pragma unroll
@@ -784,8 +839,14 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteLaunch p)
         }
 #pragma unroll
         for (int o = 32; o; o >>= 1) sum_of += __shfl_xor(sum_of, o);
-        if (sum_of != all * (all - 1) / 2)                 // equal ones: the lower expert first
-            count([&](uint64_t k, int i, int e) { return k == key[i] && e < 64 * i + lane; });
+        if (sum_of != all * (all - 1) / 2) {               // equal ones: the lower expert first; the same in every wave
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NL; ++i) rank[i] = 0;
+            count([&](uint64_t k, int i, int e) { return k > key[i] || (k == key[i] && e < 64 * i + lane); });
+            join();
+        }
+        if (wave) return;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             if (key[i] == 0) rank[i] = kNoExpert;
@@ -829,7 +890,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_moe_route(RouteLaunch p)
 
 hipError_t launch_moe_route(const RouteLaunch& p, hipStream_t s)
 {
-    const dim3 grid((unsigned)((p.rows + kRouteWaves - 1) / kRouteWaves)), threads(64 * kRouteWaves);
+    const dim3 grid((unsigned)p.rows), threads(64 * kRouteWaves);
     if (p.experts <= 64) hipLaunchKernelGGL((k_moe_route<1>), grid, threads, 0, s, p);
     else if (p.experts <= 128) hipLaunchKernelGGL((k_moe_route<2>), grid, threads, 0, s, p);
     else if (p.experts <= 256) hipLaunchKernelGGL((k_moe_route<4>), grid, threads, 0, s, p);

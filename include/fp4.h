@@ -704,7 +704,7 @@ typedef enum fp4_distill_rest {
     FP4_DISTILL_RENORMALIZE = 1
 } fp4_distill_rest;
 
-FP4_API int64_t fp4_distill_workspace(int64_t rows, int64_t vocab);
+FP4_API int64_t fp4_distill_workspace(int64_t rows, int64_t vocab, int32_t dtype);
 FP4_API fp4_status fp4_distill_loss(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,
                                     const int32_t* top_ids, const float* top_logprobs, int32_t top, float temperature,
                                     int32_t rest, float* loss, float* stats, void* workspace, int64_t workspace_bytes,

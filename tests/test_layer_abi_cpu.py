@@ -78,8 +78,8 @@ def _back(dy=FAKE, ldy=64, pre=FAKE + 256, ldp=64, mul=FAKE + 512, ldm=64, rows=
     (dict(ldy=63), -3), (dict(ldp=63), -3), (dict(ldm=63), -3), (dict(ldd=63), -3), (dict(ldg=63), -3), (dict(ldy=MANY), -2),
     (dict(dy=FAKE + 1), -4), (dict(pre=FAKE + 1), -4), (dict(mul=FAKE + 1), -4), (dict(dpre=FAKE + 1), -4), (dict(dmul=FAKE + 1), -4),
     (dict(dpre=FAKE, ldd=72), -3), (dict(dpre=FAKE + 256, ldd=72), -3), (dict(dmul=FAKE + 512, ldg=72), -3), (dict(dmul=FAKE, ldg=72), -3),
-    (dict(db=FAKE + 2), -4), (dict(ws=None), -1), (dict(room=255), -1), (dict(ws=FAKE + 8), -4),
-    (dict(mul=None, act=0, dpre=None, ws=None), -1),
+    (dict(db=FAKE + 2), -4), (dict(rows=2000, ws=None), -1), (dict(rows=2000, room=255), -1), (dict(rows=2000, ws=FAKE + 8), -4),
+    (dict(rows=2000, mul=None, act=0, dpre=None, ws=None), -1),
 ])
 def test_epilogue_backward_rejects_before_launch(kw, want):
     assert _back(**kw) == want
@@ -92,7 +92,8 @@ def test_epilogue_backward_with_nothing_to_do():
     assert need(-1, 8) == -3 and need(8, 0) == -3 and need(1, (1 << 24) + 1) == -2
     for m in (0, 1, 31, 1000, 100000):
         for n in (1, 255, 257, 11008):
-            assert 4 * n <= need(m, n) <= 4 * n * max(1, min(2048, (m + 31) // 32)) + 16
+            # few rows are summed by one launch
+            assert need(m, n) == 0 if m <= 1024 else 4 * n <= need(m, n) <= 4 * n * min(2048, (m + 31) // 32) + 16
 
 
 def _moe(m=4, top=2, hidden=256, ffn=128, experts=3, x=FAKE, ldx=256, up=None, down=None, us=FAKE, ds=FAKE, ids=FAKE, w=FAKE, act=2,
@@ -154,8 +155,8 @@ DISTILL = [(dict(dt=2), -1), (dict(temp=0.0), -1), (dict(temp=float("inf")), -1)
 
 
 @pytest.mark.parametrize("kw,want", DISTILL + [(dict(loss=None), -1), (dict(st=None), -1), (dict(loss=FAKE + 2), -4), (dict(st=FAKE + 2), -4),
-                                               (dict(v=20000, ld=20000, ws=None), -1), (dict(v=20000, ld=20000, room=8), -1),
-                                               (dict(v=20000, ld=20000, ws=FAKE + 4), -4)])
+                                               (dict(v=1 << 20, ld=1 << 20, ws=None), -1), (dict(v=1 << 20, ld=1 << 20, room=8), -1),
+                                               (dict(v=1 << 20, ld=1 << 20, ws=FAKE + 4), -4)])
 def test_distill_rejects_before_launch(kw, want):
     assert _distill(**kw) == want
 
@@ -173,9 +174,10 @@ def test_distill_backward_rejects_before_launch(kw, want):
 
 def test_distill_workspace():
     need = fq.lib().fp4_distill_workspace
-    assert need(-1, 5) == -3 and need(1, 0) == -3 and need(1, (1 << 24) + 1) == -2 and need(1 << 22, 8) == -2
-    assert need(0, 128000) == 0 and need(1, 1000) == 0 and need(512, 128000) == 0
-    assert 0 < need(1, 128000) <= 8 * 64 and need(1000, 1 << 24) == 8 * 1000 * 64
+    assert need(-1, 5, 0) == -3 and need(1, 0, 0) == -3 and need(1, (1 << 24) + 1, 0) == -2 and need(1 << 22, 8, 1) == -2 and need(1, 8, 2) == -1
+    # rows of 512 KiB are whole, longer ones are cut unless there are many
+    assert need(0, 128000, 0) == 0 and need(1, 131072, 0) == 0 and need(1, 262144, 1) == 0 and need(512, 200000, 0) == 0
+    assert 0 < need(1, 131073, 0) <= 8 * 64 and 0 < need(1, 262145, 1) <= 8 * 64 and need(1000, 1 << 24, 1) == 8 * 1000 * 64
 
 
 class _NoCalls:
