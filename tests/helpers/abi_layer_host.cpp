@@ -77,7 +77,7 @@ void look(const std::string& name, dim3 g, dim3 b, void** args)
     } else if (is("k_epilogue_backward")) {
         const EpiGradLaunch& p = arg<EpiGradLaunch>(args);
         const int64_t step = arg<int64_t>(args, 1);
-        if ((int64_t)g.x * (b.x == 1024 ? 64 : 256) < p.cols || (int64_t)g.y * step < p.rows) fail("rows and columns");
+        if ((int64_t)g.x * (b.x == 1024 ? 64 : 512) < p.cols || (int64_t)g.y * step < p.rows) fail("rows and columns");
         if (g.y > 1 && p.dbias) uses(p.part, 4 * (int64_t)g.y * p.cols, "partial column sums");
     } else if (is("k_epilogue_join")) {
         uses(arg<const float*>(args, 0), 4 * arg<int64_t>(args, 1) * arg<int64_t>(args, 2), "partial column sums, joined");

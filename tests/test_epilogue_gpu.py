@@ -252,6 +252,12 @@ def test_backward(m, n, act):
             check_backward(d, dy, pre, act, mu, bias)
 
 
+@pytest.mark.parametrize("m,n", [(1024, 513), (1025, 513), (1056, 1031), (45000, 8), (33000, 519), (1200, 11008)])
+def test_backward_of_many_row_ranges(m, n):
+    """Either side of the rows that one launch sums, one range to a thousand."""
+    test_backward(m, n, "gelu_tanh")
+
+
 def test_backward_strided_rows():
     m, n = 70, 200
     t = [torch.randn(m, n + p, device="cuda").to(BF)[:, :n] for p in (8, 3, 16)]
