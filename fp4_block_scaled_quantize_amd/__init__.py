@@ -900,7 +900,7 @@ def fp4_wo_gemm_epilogue(x: torch.Tensor, w: QTensor, bias: torch.Tensor | None 
                          mul: torch.Tensor | None = None, residual: torch.Tensor | None = None,
                          out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """fp4_wo_gemm followed by the epilogue of fp4_gemm_epilogue: residual +
-    mul act(X W^T + bias) for at most 16 rows."""
+    mul act(X W^T + bias) for at most 16 rows.  out may be mul or residual, but not x."""
     what = "fp4_wo_gemm_epilogue"
     m, n = x.shape[0], w.rows
     ldx = _bf16_rows(what, "x", x, m, w.cols)
@@ -973,7 +973,7 @@ def fp4_moe_route(logits: torch.Tensor, top: int, score: str = "softmax", bias: 
         raise ValueError(f"{what}: bias must be float32 [{e}]")
     dev = _one_device(what, logits, *(() if bias is None else (bias,)))
     with _allocating(stream, dev):
-        ids = torch.empty((n, max(top, 0)), dtype=torch.int32, device=dev)
+        ids = torch.empty((n, min(max(top, 0), e)), dtype=torch.int32, device=dev)   # more than the experts are refused
         weights = torch.empty_like(ids, dtype=torch.float32)
         st = lib().fp4_moe_route(logits.data_ptr(), DTYPE[logits.dtype], _ld(logits), n, e, top, sc, _ptr(bias),
                                  int(renormalize), scale, ids.data_ptr(), weights.data_ptr(), _stream(stream, dev))

@@ -125,6 +125,7 @@ fp4_status fp4_wo_gemm_epilogue(const uint16_t* x, int64_t ldx, int64_t m, const
     if (w->rows == 0 || w->cols == 0) return FP4_ERR_SHAPE;
     if ((st = check_epilogue(e, y, ldy, m, w->rows, &p.ep)) != FP4_OK) return st;
     if (e->pre) return FP4_ERR_UNSUPPORTED;              // a serving call: nothing is kept for a backward pass
+    if (y == x) return FP4_ERR_INVALID_ARG;              // every workgroup reads all of x (y may be a residual, x is none here)
     return hip_status(epi::launch_wo_gemm(p, (hipStream_t)stream));
 }
 

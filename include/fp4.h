@@ -593,7 +593,8 @@ FP4_API fp4_status fp4_gemm_epilogue(const fp4_tensor* a, const fp4_tensor* b, c
 /*
  * fp4_wo_gemm_epilogue -- fp4_wo_gemm followed by the epilogue, for serving
  * (pre is UNSUPPORTED).  Requirements and errors as fp4_wo_gemm (neither N nor
- * K may be 0 here).
+ * K may be 0 here).  y may not be x (INVALID_ARG), also where x is the
+ * residual too.
  */
 FP4_API fp4_status fp4_wo_gemm_epilogue(const uint16_t* x, int64_t ldx, int64_t m, const fp4_tensor* w,
                                         const fp4_epilogue* e, uint16_t* y, int64_t ldy, void* stream);

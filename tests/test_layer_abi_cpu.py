@@ -64,6 +64,10 @@ def test_products_epilogues_refuse_what_the_products_refuse():
     assert L.fp4_gemm_epilogue_workspace(ctypes.byref(_q(5, 256)), ctypes.byref(ok)) == 0
     assert L.fp4_gemm_epilogue_workspace(None, ctypes.byref(ok)) == -1 and L.fp4_gemm_epilogue_workspace(ctypes.byref(ok), None) == -1
     assert wo(ok, m=0) == -2 and wo(ok, m=17) == -2 and wo(ok, x=None) == -1 and wo(ok, ldx=260) == -4
+    # x as the output, be it the residual or not
+    square = _q(256, 256)
+    assert wo(square, y=FAKE, ldy=256, e=_epi(mul=None, res=None)) == -1
+    assert wo(square, y=FAKE, ldy=256, e=_epi(mul=None, res=FAKE, ldr=256)) == -1
     assert wo(_q(64, 0)) == -3 and wo(_q(0, 256), ldy=0) == -3 and wo(_q(64, 256, transform=1)) == -2
 
 
