@@ -120,11 +120,12 @@ typedef uint32_t u2_any __attribute__((ext_vector_type(2), aligned(2)));
 template <int W>
 using epi_vec = typename std::conditional<W == 8, u4_any, u2_any>::type;
 
-template <int W>
+template <int W, bool PAST = false>
 __device__ __forceinline__ void bf16_load(const uint16_t* p, int n, float (&o)[W])
 {
     if (W > 1 && n >= W) {
-        const epi_vec<W> v = *reinterpret_cast<const epi_vec<W>*>(p);
+        const epi_vec<W>* const q = reinterpret_cast<const epi_vec<W>*>(p);
+        const epi_vec<W> v = PAST ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) { o[2 * i] = bf16_lo(v[i]); o[2 * i + 1] = bf16_hi(v[i]); }
     } else {
@@ -132,14 +133,16 @@ __device__ __forceinline__ void bf16_load(const uint16_t* p, int n, float (&o)[W
         for (int i = 0; i < W; ++i) o[i] = i < n ? bf16_lo(p[i]) : 0.0f;
     }
 }
-template <int W>
+template <int W, bool PAST = false>
 __device__ __forceinline__ void bf16_store(uint16_t* p, int n, const float (&v)[W])
 {
     if (W > 1 && n >= W) {
         epi_vec<W> o;
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<epi_vec<W>*>(p) = o;
+        epi_vec<W>* const q = reinterpret_cast<epi_vec<W>*>(p);
+        if (PAST) __builtin_nontemporal_store(o, q);
+        else *q = o;
     } else {
 #pragma unroll
         for (int i = 0; i < W; ++i)
@@ -153,18 +156,19 @@ __device__ __forceinline__ float epi_bias(const Epilogue& e, int64_t n)
 }
 
 // W outputs of row m from column n on, of N: `sum` the product, `bias` theirs
-// (zeros without one).
-template <int W>
+// (zeros without one).  PAST: rows that are read or written
+// once, past the caches.
+template <int W, bool PAST = false>
 __device__ __forceinline__ void epi_put(const Epilogue& e, uint16_t* c, int64_t ldc, int64_t m, int64_t n, int64_t N,
                                         const float (&sum)[W], const float (&bias)[W])
 {
     const int have = N - n < W ? (int)(N - n) : W;
     float v[W], mul[W], res[W];
-    if (e.mul) bf16_load<W>(e.mul + m * e.ld_mul + n, have, mul);
-    if (e.res) bf16_load<W>(e.res + m * e.ld_res + n, have, res);
+    if (e.mul) bf16_load<W, PAST>(e.mul + m * e.ld_mul + n, have, mul);
+    if (e.res) bf16_load<W, PAST>(e.res + m * e.ld_res + n, have, res);
 #pragma unroll
     for (int i = 0; i < W; ++i) v[i] = sum[i] + bias[i];
-    if (e.pre) bf16_store<W>(e.pre + m * e.ld_pre + n, have, v);
+    if (e.pre) bf16_store<W, PAST>(e.pre + m * e.ld_pre + n, have, v);
     with_act(e.act, [&](auto act) {
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] = act_value<decltype(act)::value>(v[i]);
@@ -175,7 +179,7 @@ __device__ __forceinline__ void epi_put(const Epilogue& e, uint16_t* c, int64_t 
     if (e.res)
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] += res[i];
-    bf16_store<W>(c + m * ldc + n, have, v);
+    bf16_store<W, PAST>(c + m * ldc + n, have, v);
 }
 
 }  // namespace fp4
