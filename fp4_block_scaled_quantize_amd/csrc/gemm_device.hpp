@@ -23,6 +23,12 @@ __device__ __forceinline__ void dma16(const void* g, uint8_t* lds)
 {
     __builtin_amdgcn_global_load_lds(g, (lds_ptr_t)lds, 16, 0, 0);
 }
+// Past the caches (the instruction's non-temporal bit): for whole lines that
+// are read once.
+__device__ __forceinline__ void dma16_once(const void* g, uint8_t* lds)
+{
+    __builtin_amdgcn_global_load_lds(g, (lds_ptr_t)lds, 16, 0, 2);
+}
 __device__ __forceinline__ void dma4(const void* g, uint8_t* lds)
 {
     __builtin_amdgcn_global_load_lds(g, (lds_ptr_t)lds, 4, 0, 0);

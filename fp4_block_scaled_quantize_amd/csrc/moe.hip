@@ -15,7 +15,14 @@
 // needed and the same inputs give the same bits.
 //
 // Both read every byte of the chosen experts' weights once and nothing else
-// of weight, so they are bound by memory; as in the weight-only product a wave
+// of weight, so they are bound by memory (up + down: 4096 x 1536, NVFP4, 37
+// experts met by 16 tokens, 262 + 131 MB in 66 + 48 us, 4.0 and 2.7 TB/s; 4096 x
+// 11008, MXFP4, 5 met by 3 tokens, 240 + 120 MB in 45 + 29 us, 5.3 and 4.1; one
+// token's 8 experts of 2048 x 768, 14 + 7 MB, 9.0 + 7.6 us, of which the
+// latencies of a launch, the ids and the first chunk are most).  What keeps the
+// down projection of many tokens from the copy's rate is the LDS: a slot holds the
+// rows of h of its expert's tokens beside the weights, so that fewer bytes of
+// weights are under way.  As in the weight-only product a wave
 // streams 128-element chunks with loads straight into its own LDS ring, where
 // their order keeps four lanes on one 64-byte run, and takes the fragments
 // from there.  A wave's chunks are a contiguous part of the workgroup's
@@ -157,9 +164,13 @@ __device__ __forceinline__ void moe_stream(uint8_t* ring, const MoeSide& s, cons
 #pragma unroll
         for (int g = 0; g < RG; ++g)
 #pragma unroll
-            for (int k = 0; k < S::WD; ++k)
-                if (ELEM < 4 || wact[k])
-                    dma16(qe + wsrc[g][k] + (uint32_t)ik * (uint32_t)S::WB, sl + S::W + 16 * S::WP * g + 1024 * k);
+            for (int k = 0; k < S::WD; ++k) {
+                const uint8_t* const from = qe + wsrc[g][k] + (uint32_t)ik * (uint32_t)S::WB;
+                uint8_t* const to = sl + S::W + 16 * S::WP * g + 1024 * k;
+                // whole lines: 4096 x 1536, 37 experts met, 67 + 49 us -> 66 + 48; 4096 x 11008, 5 met, 48 + 31 -> 45 + 29
+                if (S::WB == 128) dma16_once(from, to);
+                else if (ELEM < 4 || wact[k]) dma16(from, to);
+            }
 #pragma unroll
         for (int j = 0; j < S::NSC; ++j)
             if (sact[j]) dma4(se + ssrc[j] + (uint32_t)ik * (uint32_t)S::SCB, sl + S::SC + 256 * j);
