@@ -16,8 +16,8 @@
 //
 // Both read every byte of the chosen experts' weights once and nothing else
 // of weight, so they are bound by memory (up + down: 4096 x 1536, NVFP4, 37
-// experts met by 16 tokens, 262 + 131 MB in 66 + 48 us, 4.0 and 2.7 TB/s; 4096 x
-// 11008, MXFP4, 5 met by 3 tokens, 240 + 120 MB in 45 + 29 us, 5.3 and 4.1; one
+// experts met by 16 tokens, 262 + 131 MB in 62 + 47 us, 4.2 and 2.8 TB/s; 4096 x
+// 11008, MXFP4, 5 met by 3 tokens, 240 + 120 MB in 44 + 29 us, 5.4 and 4.1; one
 // token's 8 experts of 2048 x 768, 14 + 7 MB, 9.0 + 7.6 us, of which the
 // latencies of a launch, the ids and the first chunk are most).  What keeps the
 // down projection of many tokens from the copy's rate is the LDS: a slot holds the
@@ -313,12 +313,14 @@ __device__ __forceinline__ bool any_bit(const uint64_t (&m)[kMoePairs / 64], int
     return got != 0;
 }
 
-// Rings of 40 KiB, so that three workgroups share a CU (52 KiB, and two: 4096 x
-// 11008, 5 experts met, 55 us against 48); for one token, whose few workgroups
-// do not fill the CUs so often, deeper rings and two.
+// Rings of 51 KiB, the most that lets three workgroups share a CU (two of them
+// with larger rings: 4096 x 11008, 5 experts met, 55 us against 48); 40 KiB
+// leave fewer waves two slots (4096 x 1536, 37 met, 65.6 us against 62.4).  For
+// one token, whose few workgroups do not fill the CUs so often, deeper rings
+// and two.
 constexpr int kMoeUpWaves = 4;
 template <int MAXR>
-constexpr int kMoeUpBudget = (MAXR == 1 ? 68 : 40) * 1024;
+constexpr int kMoeUpBudget = (MAXR == 1 ? 68 : 51) * 1024;
 constexpr int kMoeDownWaves = 16;
 
 // ---------------------------------------------------------------------------
@@ -352,7 +354,6 @@ __global__ __launch_bounds__(64 * kMoeUpWaves) void k_moe_up(MoeLaunch p)
     __shared__ float sdec[256];
     __shared__ uint64_t found[2][kMoePairs / 64];
     __shared__ uint8_t pair[kMoeMaxTokens], token[kMoeMaxTokens];
-    __shared__ float part[NW][2][256];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int pairs = p.m * p.top, y = blockIdx.y;
     const bool by_pair = pairs <= p.experts;
@@ -396,24 +397,28 @@ __global__ __launch_bounds__(64 * kMoeUpWaves) void k_moe_up(MoeLaunch p)
     s.row0 = (uint32_t)n0; s.row1 = (uint32_t)(p.ffn + n0);
     s.k = (int32_t)p.hidden;
     s.x = p.x; s.ldx = p.ldx; s.plane = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) part[wave][i >> 2][4 * lane + (i & 3)] = 0.0f;
+    // a wave's sums: 256 of the gate, 256 of the up matrix, where its ring was
+    int stream = 0, ring = 0;
     moe_rows<MAXR>(cnt, [&](auto rows) {
         constexpr int XR = decltype(rows)::value;
         using S = MoeSlot<2, XR, 1, ELEM, BLOCK, SUB>;
         using Shape = MoeShape<S, NW, kMoeUpBudget<MAXR>>;
         constexpr int NA = Shape::Waves;
-        const int nch = s.k / S::K, first = nch * wave / NA;
-        if (wave < NA)
-            moe_stream<Shape::D, 2, XR, 1, ELEM, BLOCK, SUB, SPLIT, POW2>(
-                lds + wave * (Shape::D * S::Bytes), s, sdec, first, nch * (wave + 1) / NA - first, lane,
-                [&](int) { return MoeExpert{e, cnt, token}; }, [&](int, const v4f (&acc)[2]) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        part[wave][0][4 * lane + r] = acc[0][r];
-                        part[wave][1][4 * lane + r] = acc[1][r];
-                    }
-                });
+        static_assert(Shape::D * S::Bytes >= 2048, "a wave's sums");
+        stream = NA;
+        ring = Shape::D * S::Bytes;
+        const int nch = s.k / S::K, first = nch * wave / NA, mine = nch * (wave + 1) / NA - first;
+        if (wave >= NA) return;
+        v4f* const sums = reinterpret_cast<v4f*>(lds + wave * ring);
+        auto put = [&](int, const v4f (&acc)[2]) {
+            sums[lane] = acc[0];
+            sums[64 + lane] = acc[1];
+        };
+        // its chunks end with the wave's last, when all that it loaded has been read
+        if (mine > 0)
+            moe_stream<Shape::D, 2, XR, 1, ELEM, BLOCK, SUB, SPLIT, POW2>(lds + wave * ring, s, sdec, first, mine, lane,
+                                                                          [&](int) { return MoeExpert{e, cnt, token}; }, put);
+        else put(0, {v4f{0.f, 0.f, 0.f, 0.f}, v4f{0.f, 0.f, 0.f, 0.f}});
     });
     __syncthreads();
     const int j = tid >> 4, n = tid & 15;
@@ -421,7 +426,12 @@ __global__ __launch_bounds__(64 * kMoeUpWaves) void k_moe_up(MoeLaunch p)
     const int at = 4 * (16 * (j >> 2) + n) + (j & 3);
     float gate = 0.0f, up = 0.0f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) { gate += part[w][0][at]; up += part[w][1][at]; }
+    for (int w = 0; w < NW; ++w) {
+        if (w >= stream) break;
+        const float* const sums = reinterpret_cast<const float*>(lds + w * ring);
+        gate += sums[at];
+        up += sums[256 + at];
+    }
     put_hidden(p, gate, up, f, pair[j], n0 + n);
 }
 
@@ -665,7 +675,7 @@ static hipError_t run_moe(const MoeLaunch& p, bool up, hipStream_t s)
         constexpr size_t sh = ring_bytes<kMoeUpWaves, kMoeUpBudget<MAXR>, 2, 1, ELEM, BLOCK, SUB, MAXR>();
         static_assert(sh <= kMoeUpBudget<MAXR>, "LDS");
         const int most = p.m * p.top < p.experts ? p.m * p.top : p.experts;
-        if (sh + 16 * 1024 > 64 * 1024) {
+        if (sh + 2 * 1024 > 64 * 1024) {                   // with the scales and the tokens
             const hipError_t e = allow_lds(k_moe_up<ELEM, BLOCK, SUB, SPLIT, POW2, MAXR>, sh);
             if (e != hipSuccess) return e;
         }
