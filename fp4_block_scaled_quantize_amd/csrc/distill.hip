@@ -101,7 +101,8 @@ __device__ __forceinline__ void finish_distill(const DistillLaunch& p, int64_t r
     cross = wave_sum(cross);
     own = wave_sum(own);
     if (lane) return;
-    const bool empty = m == -INFINITY && rest == 0.0f;    // a student's row of masks
+    // a student's row of masks; own is NaN where a listed logit is, which no maximum shows
+    const bool empty = m == -INFINITY && rest == 0.0f && own == 0.0;
     // the others' sum against the whole row's maximum, and its share R of the total
     const double below = mr == -INFINITY ? 0.0 : ((double)mr - (double)m) * k;
     const double total = own + (double)rest * exp2(below), logs = log(total);

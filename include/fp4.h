@@ -695,7 +695,8 @@ FP4_API fp4_status fp4_moe(const uint16_t* x, int64_t ldx, int64_t m, const fp4_
  * for the other tokens, and a student that gives them nothing (all listed, or
  * -inf) has no such term.  A student's -inf at a token with p > 0 makes the
  * loss inf (its gradient stays finite); a row of only -inf has loss inf and
- * gradient 0; a NaN or +inf logit makes its row's loss NaN.
+ * gradient 0; a NaN or +inf logit makes the loss of its row NaN (a row of loss
+ * 0 by its list alone, above, keeps that).
  * stats [rows, 7]: for the backward call.  temperature > 0, and 2 /
  * temperature is finite.  Fewer than 2^22 rows, at most 2^24 tokens.
  * workspace: as above, fp4_distill_workspace bytes.

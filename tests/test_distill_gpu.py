@@ -224,6 +224,20 @@ def test_nan_and_infinity_stay_in_their_rows():
 
 
 @pytest.mark.parametrize("rest", ["bucket", "renormalize"])
+@pytest.mark.parametrize("v", [700, 140001])                 # a row in one piece, and in several
+def test_a_listed_nan_in_a_row_of_masks(v, rest):
+    """A NaN logit that is listed makes the loss NaN also where every other logit is -inf; a row without entries keeps 0."""
+    z = torch.full((4, v), -math.inf, device="cuda")
+    z[0, 5], z[1, 9], z[3, 5] = float("nan"), float("nan"), float("nan")
+    ids = torch.tensor([[5, 7], [5, 7], [5, 7], [-1, -1]], dtype=torch.int32, device="cuda")
+    t = torch.log(torch.tensor([0.5, 0.25], device="cuda")).repeat(4, 1).contiguous()
+    f = fq.fp4_distill_loss(z, ids, t, rest=rest)
+    assert torch.isnan(f.loss[:2]).all() and f.loss[2] == math.inf and f.loss[3] == 0
+    d = fq.fp4_distill_loss_backward(z, ids, t, f, torch.ones(4, device="cuda"), rest=rest)
+    assert torch.isnan(d[:2]).any(1).all() and (d[2:] == 0).all()
+
+
+@pytest.mark.parametrize("rest", ["bucket", "renormalize"])
 @pytest.mark.parametrize("temperature", [1.0, 2.0])
 def test_gradient_against_differences(rest, temperature):
     """Along a direction u with |u| <= 1 and h = 2^-6: central differences of
