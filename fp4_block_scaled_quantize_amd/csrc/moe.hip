@@ -233,8 +233,8 @@ __device__ __forceinline__ void moe_stream(uint8_t* ring, const MoeSide& s, cons
                 for (int tt = 0; tt < 4; ++tt) {
                     const float st = tt < 2 ? s0 : s1;                  // elements 0..15: the first block
                     v4i hi, lo;
-                    if constexpr (WIDE) dq8_any<ELEM, SPLIT>(dw, tt, st, hi, lo);
-                    else if constexpr (SPLIT) dq8_bf16_split<ELEM == 1>((uint32_t)wv[tt], st, hi, lo);
+                    if constexpr (WIDE) dq8_any<ELEM, SPLIT, true>(dw, tt, st, hi, lo);
+                    else if constexpr (SPLIT) dq8_bf16_split<ELEM == 1, true>((uint32_t)wv[tt], st, hi, lo);
                     else hi = dq8_bf16<POW2, ELEM == 1>((uint32_t)wv[tt], st);
 #pragma unroll
                     for (int h = 0; h < XP; ++h) {

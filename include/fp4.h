@@ -382,7 +382,8 @@ FP4_API fp4_status fp4_set_gemm_small_outputs(int64_t outputs, int64_t* previous
  * transform on w (UNSUPPORTED otherwise).  Every element grid: E2M1, INT4
  * and the 8- and 6-bit ones (quant_prune_distill/486 "Метод": the MX
  * family's 8- and 6-bit members); each product e(w_nk) s_w enters the bf16
- * matrix instruction exactly, as one bf16 value or as the sum of two.
+ * matrix instruction exactly, as one bf16 value or as the sum of two (an
+ * infinity in x meets both, and where the second is zero that leaves NaN).
  */
 FP4_API fp4_status fp4_wo_gemm(const uint16_t* x, int64_t ldx, int64_t m, const fp4_tensor* w, uint16_t* y,
                        int64_t ldy, void* stream);
@@ -659,7 +660,8 @@ typedef struct fp4_moe_bank {
  *   y_i = bf16_RNE(residual_i + sum_k w_ik D_e (act(G_e x_i) (U_e x_i))),
  *   e = ids_ik
  * with bf16 x, ids (int32) and weights (binary32) [m, top] dense, top 1 .. 16.
- * Weights enter the matrix instruction exactly as in fp4_wo_gemm, sums are
+ * Weights enter the matrix instruction exactly, as in fp4_wo_gemm but so that
+ * an infinity times a weight other than zero is one on every grid; sums are
  * binary32, and what act gives reaches the down projection with 16 bits (an
  * infinity there stays one).  An id outside 0 .. experts - 1 (-1 by
  * convention) is no expert; an id that a token names twice has both weights.

@@ -166,6 +166,38 @@ def test_an_infinity_stays_one():
     assert not torch.isfinite(y).any()
 
 
+def positive_bank(seed, block, scale, element, sign):
+    """One expert whose codes are all of one sign in each matrix, none of them zero: gate and up positive, down `sign`."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def make(rows, s):
+        w = s * (torch.rand(rows, 256, generator=g, device="cuda") * 0.5 + 0.5)
+        q = fq.fp4_quantize(w.to(BF), block, scale, amax="none" if scale == "e8m0" else "current", element=element)
+        assert (s * fq.fp4_dequantize(q) > 0).all()
+        return q
+    return fq.MoeBank(make(512, 1.0), make(256, sign), 1)
+
+
+# in the last six a weight enters as two terms, of which the second may be zero
+@pytest.mark.parametrize("block,scale,element", [
+    (16, "e4m3", "e2m1"), (32, "e8m0", "e2m1"), (32, "e8m0", "fp8_e4m3"), (32, "e8m0", "int8"), (32, "e8m0", "fp6_e3m2"),
+    (16, "e1m6", "e2m1"), (16, "e2m5", "int4"), (16, "ue5m3", "int8"), (16, "e4m3", "int8"), (32, "e4m3", "int6"),
+    (16, "e1m6", "fp8_e4m3")])
+@pytest.mark.parametrize("m", [1, 3, 16])
+def test_an_infinity_keeps_its_sign(m, block, scale, element):
+    """Weights of one sign: an infinity that act gives, or that x holds, reaches y as one and never as a NaN."""
+    ids, w = torch.zeros(m, 1, dtype=torch.int32, device="cuda"), torch.ones(m, 1, device="cuda")
+    for sign in (1.0, -1.0):
+        bank = positive_bank(28, block, scale, element, sign)
+        x = torch.full((m, 256), 3e38, device="cuda").to(BF)     # finite: the products overflow
+        y = fq.fp4_moe(x, bank, ids, w)
+        assert (y == sign * math.inf).all()
+        x = torch.rand(m, 256, device="cuda", generator=torch.Generator(device="cuda").manual_seed(29)).to(BF)
+        x[0, 77] = math.inf
+        y = fq.fp4_moe(x, bank, ids, w)
+        assert (y[0] == sign * math.inf).all() and torch.isfinite(y[1:]).all()
+
+
 def test_strided_rows_and_in_place():
     bank = bank_of(5, 256, 256, 21)
     wide = tokens(7, 264, 22)
