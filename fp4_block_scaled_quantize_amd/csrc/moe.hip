@@ -7,7 +7,7 @@
 //
 // Two launches.  k_moe_up: a workgroup for 16 columns of one expert's gate and
 // up matrices, the tokens that chose it as the rows of the product; it writes
-// h = act(gate) up as two bf16 terms (16 bits of h: one bf16 would round what
+// h = act(gate) up as two bf16 terms (17 bits of h: one bf16 would round what
 // the down projection sums).  k_moe_down: a workgroup for 16 outputs, all
 // experts one after another: a wave folds each expert's sums into its tokens'
 // outputs with the router's weight in binary32, and the waves' sums join in
@@ -337,11 +337,14 @@ __device__ __forceinline__ void put_hidden(const MoeLaunch& p, float gate, float
     float h = gate * f;
     with_act(p.act, [&](auto act) { h = act_value<decltype(act)::value>(h); });
     h *= up * f;
-    // h as the sum of two bf16: its first eight bits, and what they leave, rounded
-    const uint32_t hi = f_bits(h) & 0xFFFF0000u;
+    // h as the sum of two bf16, both to nearest, 17 bits (a third term would cost
+    // the down projection's rings half as much again).  A finite h past bf16's
+    // largest value is cut instead: it must not become an infinity.
+    uint32_t hi = (uint32_t)f32_to_bf16_rne(h) << 16;
+    if ((hi & 0x7FFFFFFFu) == 0x7F800000u) hi = f_bits(h) & 0xFFFF0000u;
     const float left = h - bits_f(hi);
     const int64_t to = (int64_t)pair * p.ffn + n;
-    p.h[to] = (uint16_t)(hi >> 16) | (h != h ? 0x40u : 0u);
+    p.h[to] = (uint16_t)(hi >> 16);
     p.h[to + (int64_t)p.m * p.top * p.ffn] = left == left ? (uint16_t)f32_to_bf16_rne(left) : (uint16_t)0;
 }
 

@@ -662,7 +662,7 @@ typedef struct fp4_moe_bank {
  * with bf16 x, ids (int32) and weights (binary32) [m, top] dense, top 1 .. 16.
  * Weights enter the matrix instruction exactly, as in fp4_wo_gemm but so that
  * an infinity times a weight other than zero is one on every grid; sums are
- * binary32, and what act gives reaches the down projection with 16 bits (an
+ * binary32, and what act gives reaches the down projection with 17 bits (an
  * infinity there stays one).  An id outside 0 .. experts - 1 (-1 by
  * convention) is no expert; an id that a token names twice has both weights.
  * A token without experts gets residual (null: zero).  Nothing of one token

@@ -198,6 +198,50 @@ def test_an_infinity_keeps_its_sign(m, block, scale, element):
         assert (y[0] == sign * math.inf).all() and torch.isfinite(y[1:]).all()
 
 
+def picking_bank(scale):
+    """Two experts whose down projection is the identity: the first gives scale^2 x[0] x[64] everywhere, the second x[127]^2."""
+    gate, up = torch.zeros(2, 128, 128, device="cuda"), torch.zeros(2, 128, 128, device="cuda")
+    gate[0, :, 0], up[0, :, 64], gate[1, :, 127], up[1, :, 127] = 1.0, 1.0, 1.0, 1.0
+    one = [fq.fp4_quantize(w.to(BF), 32, "e8m0", amax="none") for w in (
+        torch.cat([gate, up], 1).view(512, 128), torch.eye(128, device="cuda").repeat(2, 1))]
+    return fq.MoeBank(*one, 2, torch.tensor([scale, 1.0], device="cuda"))
+
+
+def test_the_hidden_value_has_seventeen_bits():
+    """The first expert's hidden value h, less h64 by the second's router weight: what is left is the rounding of h to
+    its two terms.  Both to nearest: the first is off by at most 2^-8 of h's binade, so that the second's last place is
+    2^-16 of it, and half of that, 2^-17, is the error at most.  Before it the two scales, act's product and h64 in
+    binary32, 4 2^-24 of h; after it y's rounding, 2^-8 of what is left."""
+    g = torch.Generator(device="cuda").manual_seed(30)
+    ids = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda").repeat(16, 1)
+    worst = 0.0
+    for _ in range(40):
+        scale = float(torch.rand(1, generator=g, device="cuda") + 1.0)
+        x = torch.zeros(16, 128, device="cuda")
+        x[:, 0], x[:, 64] = torch.rand(2, 16, generator=g, device="cuda") + 0.5
+        x[:, 127] = 1.0
+        x = x.to(BF)
+        h = x[:, 0].double() * x[:, 64].double() * float(torch.tensor(scale)) ** 2
+        w = torch.stack([torch.ones(16, device="cuda"), -h.float()], 1).contiguous()
+        y = fq.fp4_moe(x, picking_bank(scale), ids, w, act="none").double()
+        binade = torch.exp2(torch.floor(torch.log2(h)))
+        off = (y.abs() * (1 - 2.0 ** -8) - 2.0 ** -22 * h[:, None]) / binade[:, None]
+        worst = max(worst, off.max().item())
+    assert worst <= 2.0 ** -17
+
+
+def test_a_hidden_value_past_bf16_is_finite():
+    """binary32 reaches 2^-8 further than bf16: a hidden value there is no infinity."""
+    x = torch.zeros(1, 128, device="cuda")
+    x[0, 0], x[0, 64], x[0, 127] = torch.finfo(BF).max, 1.0, 1.0
+    scale = 1.0015
+    h = torch.finfo(BF).max * float(torch.tensor(scale)) ** 2
+    assert torch.finfo(BF).max < h < torch.finfo(torch.float32).max
+    ids, w = torch.tensor([[0]], dtype=torch.int32, device="cuda"), torch.tensor([[0.5]], device="cuda")
+    y = fq.fp4_moe(x.to(BF), picking_bank(scale), ids, w, act="none").double()
+    assert ((y - 0.5 * h).abs() <= (2.0 ** -8 + 2.0 ** -15) * 0.5 * h).all()
+
+
 def test_strided_rows_and_in_place():
     bank = bank_of(5, 256, 256, 21)
     wide = tokens(7, 264, 22)
