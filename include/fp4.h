@@ -558,7 +558,8 @@ FP4_API fp4_status fp4_residual_norm_backward(const fp4_norm* args, const float*
  * s(x) = 1 / (1 + e^-x) and Phi the normal distribution, act(v) is
  *   none v; relu max(v, 0); silu v s(v); gelu v Phi(v);
  *   gelu_tanh v s(2 u), u = sqrt(2 / pi) (v + 0.044715 v^3)
- * so that a gated layer is two products: the up projection's output is the
+ * (an exponential below 2^-126 counts as zero, which an act of about -1e-36 and
+ * smaller then is) so that a gated layer is two products: the up projection's output is the
  * gate projection's mul.  bias: [n] in bias_dtype (f32 or bf16); mul, residual
  * and pre: bf16 [m, n], element aligned, row strides >= n; each may be null.
  * y may be mul or residual (same row stride), pre none of them. */

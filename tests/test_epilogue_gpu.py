@@ -296,6 +296,22 @@ def test_backward_against_differences(act):
     assert ((d - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -16).all()
 
 
+def test_gelu_slope_in_binary32():
+    """At every bf16 number up to 13, as the sum of a single row, which nothing rounds to bf16: Phi(v) + v phi(v) with
+    the normal tail within 2^-21 and exp(-v^2 / 2) within 2^-22 of itself, three roundings on the way to v phi(v) (a
+    constant and two products), one of 1 - tail and one of the sum."""
+    bits = torch.arange(0x2000, 0x4151, dtype=torch.int32)   # 2^-63 .. 13
+    v = torch.cat([bits, bits + 0x8000 - 0x10000]).to(torch.int16).view(BF).cuda()[None]
+    d = fq.fp4_epilogue_backward(torch.ones_like(v), v, act="gelu", bias=True).dbias.double().cpu()
+    x = v[0].double().cpu()
+    assert x.max() == 13.0 and x.min() == -13.0
+    tail = 0.5 * torch.special.erfc(x.abs() / math.sqrt(2.0))
+    vphi = x * torch.exp(-0.5 * x * x) / math.sqrt(2.0 * math.pi)
+    want = torch.where(x < 0, tail, 1.0 - tail) + vphi
+    tol = 2.0 ** -21 * tail + (2.0 ** -22 + 3 * 2.0 ** -24) * vphi.abs() + 2.0 ** -24 * (want.abs() + (x >= 0))
+    assert ((d - want).abs() <= tol).all(), ((d - want).abs() / tol).max()
+
+
 def test_backward_bits_repeat():
     m, n = 3000, 500
     pre, dy, mul = ((torch.randn(m, n, device="cuda")).to(BF) for _ in range(3))
