@@ -409,11 +409,16 @@ __global__ __launch_bounds__(kDsThreads) void k_distill_backward(DistillGradLaun
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // A row is one workgroup's where the rows alone fill the device, and also where
-// it is at most 512 KiB: 16 waves read it at what a CU takes, and the second
-// launch, which joins the pieces, costs more than that (61 rows of 50257,
-// binary32: 7.9 + 5.1 us in nine pieces).  Longer rows are cut as the token log
-// probabilities' are, and a piece has at most kDsMost elements, whose bitmap must
-// fit the LDS.
+// it is at most 512 KiB, in 16 waves.  For rows by the tens that is about what
+// pieces and the launch that joins them take, for a few long ones more (one
+// workgroup a row against pieces, us a call in a graph):
+//             32000 f32    50257 f32    128256 f32   128256 bf16
+//   1 row     9.4   8.6    10.8   8.6   15.2   8.8   13.9   8.8
+//   8         9.6   8.9    11.3   9.7   15.5   8.9   14.2   8.9
+//   61        10.3  10.6   12.1  12.6   16.2  14.9   15.1  13.3
+//   256       12.9  14.6   17.2  19.1   29.8  31.2   18.7  19.7
+// Longer rows are cut as the token log probabilities' are, and a piece has at
+// most kDsMost elements, whose bitmap must fit the LDS.
 int64_t distill_pieces(int64_t rows, int64_t vocab, int64_t esize)
 {
     const int64_t n = vocab * esize <= 512 * 1024 ? 1 : logprob_pieces(rows, vocab), least = cdiv(vocab, kDsMost);

@@ -131,7 +131,14 @@ hipError_t launch_epilogue_join(const GemmEpiLaunch& p, hipStream_t s)
 // multiplier 191 us (4.7 TB/s), 8192 x 11008 without one 116, 8000 x 5003 118,
 // 4096 x 4096 39, against 215, 131, 135 and 41 with 2048 workgroups of 256
 // columns and 256 threads (1024 of 1024 columns: 210, 127, 131, 41; stores
-// past the caches changed none by more than 2 us).
+// past the caches changed none by more than 2 us).  One launch against ranges
+// and their join, silu with a multiplier and sums, us a call in a graph:
+//              x 256        x 1027       x 4096       x 11008
+//   130 rows   5.4   7.8    8.0  13.5    5.8   8.3    8.2  11.4
+//   256        6.5   8.7    8.3  16.0    7.0   9.4    9.2  12.7
+//   512        9.8   8.9    14.2 16.1    12.5 12.6    14.5 17.0
+//   1024       17.1  9.1    27.2 16.3    20.7 13.9    29.6 27.9
+// so that the bound is late for the last of these.
 constexpr int64_t kEgFewRows = 1024, kEgGroups = 1400;
 constexpr int kEgCols = 512, kEgFewCols = 64;
 int64_t epilogue_groups(int64_t rows, int64_t cols)

@@ -237,6 +237,9 @@ __device__ __forceinline__ int mx_swz(int r)
 // 270 without any of the three), with a residual too 398 against 428, 4096^3
 // 59 against 61; the multiplier's producer before it, 577 against 611, but
 // 4096^3, whose 32 MiB the caches would have kept, 102 against 98.
+// Beside the main loop's registers the epilogue's fields and the range's pointers
+// do not all fit: k_gemm_nv keeps 8 bytes a lane in scratch (28 for MXFP8 at block
+// 32, 60 in the bf16 form), k_gemm_dq 16; the plain kernels none.
 constexpr int kCTileRow = 4 * kTile + 16;           // bytes per LDS row of the image
 constexpr int kCTileBytes = kTile / 2 * kCTileRow;
 
@@ -2372,7 +2375,8 @@ hipError_t launch_wo_gemm(const WoArgs& p, hipStream_t s)
 #if FP4_EPILOGUE_FORM
 // Microseconds that a 256 x 256 tile takes for 128 elements of K, and the
 // elements that a K range must be a multiple of (what a kernel's scale loads
-// cover at once).
+// cover at once).  The f16 path's is that of tiles on a third of the CUs (80 of
+// 1111 x 4096 x 11008, 222 us); with 240 workgroups it is 3.8.
 struct TileCost { double us; int64_t step; };
 static TileCost tile_cost(const GemmLaunch& p)
 {
@@ -2385,7 +2389,12 @@ static TileCost tile_cost(const GemmLaunch& p)
 // workgroups run in rounds of 256, each as long as a range, and the partial
 // sums are written and read once more at about 4 TB/s, in a launch of its own
 // (1111 x 4096 x 11008, NVFP4: three ranges 111 us and 12.5 to join them; whole
-// products, 80 tiles, 222).
+// products, 80 tiles, 222).  Products that k_gemm_small takes (by their outputs,
+// a bound from before there were ranges) are left to it; tiles in ranges overtake
+// it with rows and K (N = 4096, us, small kernel against ranges: NVFP4 K = 4096
+// 128 rows 25.5 35.6, 256 37.5 44.9, 512 68.8 51.1; K = 11008 45.1 43.6, 70.6 51.7, 144.2
+// 70.8; UE5M3 29.8 44.3, 61.5 51.9, 83.8 65.3; 61.5 56.4, 151.4 68.5, 203.5 92.6; MXFP8
+// 29.0 36.7, 49.4 43.9, 93.6 55.7; 56.7 48.9, 97.3 59.4, 191.8 82.2).
 int64_t gemm_split(GemmEpiLaunch* p)
 {
     const int64_t tiles = ((p->n + kTile - 1) / kTile) * ((p->m + kTile - 1) / kTile);

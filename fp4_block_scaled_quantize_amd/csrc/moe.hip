@@ -21,8 +21,15 @@
 // token's 8 experts of 2048 x 768, 14 + 7 MB, 9.0 + 7.6 us, of which the
 // latencies of a launch, the ids and the first chunk are most).  What keeps the
 // down projection of many tokens from the copy's rate is the LDS: a slot holds the
-// rows of h of its expert's tokens beside the weights, so that fewer bytes of
-// weights are under way.  As in the weight-only product a wave
+// rows of h of its expert's tokens beside the weights, each wave its own, so that
+// fewer bytes of weights are under way the more tokens an expert has (E2M1, block
+// 16: 64 KiB a CU at 2, 40, 24 and 12 at 4, 8 and 16).  16 tokens, the whole layer,
+// 4096 x 11008, NVFP4: top 2 of 8 experts 609 MB in 157 us (3.9 TB/s), of 4 304 MB
+// in 105 (2.9), of 2, all tokens on both, 152 MB in 76 (2.0).  Nor do hidden / 16
+// workgroups fit the CUs but at multiples of 4096: top 6 of 64, 47 met, 4096 x 1536
+// 4.3 TB/s, 7168 x 2048 4.5, 5120 x 1536 3.6, 2048 x 1408 2.6.
+//
+// As in the weight-only product a wave
 // streams 128-element chunks with loads straight into its own LDS ring, where
 // their order keeps four lanes on one 64-byte run, and takes the fragments
 // from there.  A wave's chunks are a contiguous part of the workgroup's
@@ -30,8 +37,10 @@
 // number of experts, and crosses few expert borders.
 //
 // A workgroup sorts the (token, choice) pairs by expert itself, from the ids:
-// at most 256, one a thread.  Columns of the product are the tokens of one
-// expert, so nothing of one token reaches another's outputs (NaN included).
+// at most 256, one a thread.  Rows of the product are the tokens of one expert,
+// a row of a matrix instruction's result depends on its own row of them alone,
+// and the rows past the tokens, which repeat the last, are never folded: nothing
+// of one token reaches another's outputs (NaN included).
 #include "epilogue_device.hpp"
 #include "fp4_device.hpp"
 #include "fp4_internal.h"
@@ -314,7 +323,8 @@ __device__ __forceinline__ bool any_bit(const uint64_t (&m)[kMoePairs / 64], int
 }
 
 // Rings of 51 KiB, the most that lets three workgroups share a CU (two of them
-// with larger rings: 4096 x 11008, 5 experts met, 55 us against 48); 40 KiB
+// with larger rings: 4096 x 11008, 5 experts met, 55 us against 48, when the
+// weights still went through the caches; now 44); 40 KiB
 // leave fewer waves two slots (4096 x 1536, 37 met, 65.6 us against 62.4).  For
 // one token, whose few workgroups do not fill the CUs so often, deeper rings
 // and two.
