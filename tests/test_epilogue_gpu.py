@@ -296,6 +296,42 @@ def test_backward_against_differences(act):
     assert ((d - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -16).all()
 
 
+@pytest.mark.parametrize("m,n", [(70, 203), (1500, 519)])    # one launch, and ranges of rows
+@pytest.mark.parametrize("to", [("dy", "pre"), ("pre", "mul"), ("mul", "dy"), ("dy", "mul")])
+def test_backward_in_place(m, n, to):
+    """dpre and dmul in the place of two of the inputs, padded rows: the bits of the call into rows of their own."""
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    t = {k: torch.randn(m, n + 5, generator=g, device="cuda").to(BF) for k in ("dy", "pre", "mul")}
+    behind = {k: v[:, n:].clone() for k, v in t.items()}
+    want = fq.fp4_epilogue_backward(t["dy"][:, :n], t["pre"][:, :n], act="gelu_tanh", mul=t["mul"][:, :n], bias=True)
+    lib, ld, dbias = fq.lib(), n + 5, torch.empty(n, device="cuda")
+    ws = torch.empty(max(16, lib.fp4_epilogue_workspace(m, n)), dtype=torch.uint8, device="cuda")
+    args = [x for k in ("dy", "pre", "mul") for x in (t[k].data_ptr(), ld)]
+    st = lib.fp4_epilogue_backward(*args, m, n, fq.ACT["gelu_tanh"], t[to[0]].data_ptr(), ld, t[to[1]].data_ptr(), ld,
+                                   dbias.data_ptr(), ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert torch.equal(t[to[0]][:, :n], want.dpre) and torch.equal(t[to[1]][:, :n], want.dmul) and torch.equal(dbias, want.dbias)
+    assert all(torch.equal(t[k][:, n:], behind[k]) for k in t)
+
+
+@pytest.mark.parametrize("place", ["mul", "residual"])
+@pytest.mark.parametrize("block,scale,k", [(32, "e8m0", 4096), (16, "e4m3", 1408)])
+def test_product_epilogue_in_k_ranges_in_place(block, scale, k, place):
+    m, n = 260, 301
+    a, b = quantized(m, k, 71, block, scale, "e2m1", 1.0), quantized(n, k, 72, block, scale, "e2m1", 0.1)
+    bias, mul, res = tensors(m, n + 3, 73, torch.float32, True, True)
+    bias, mul, res = bias[:n], mul[:, :n], res[:, :n]
+    was = fq.set_gemm_small_outputs(0)
+    try:
+        assert fq.lib().fp4_gemm_epilogue_workspace(a.packed(), b.packed()) > 0
+        want, pre = fq.fp4_gemm_epilogue(a, b, bias=bias, act="gelu", mul=mul, residual=res, save_pre=True)
+        to = mul if place == "mul" else res
+        y, p = fq.fp4_gemm_epilogue(a, b, bias=bias, act="gelu", mul=mul, residual=res, save_pre=True, out=to)
+        assert y.data_ptr() == to.data_ptr() and torch.equal(y, want) and torch.equal(p, pre)
+    finally:
+        fq.set_gemm_small_outputs(was)
+
+
 def test_gelu_slope_in_binary32():
     """At every bf16 number up to 13, as the sum of a single row, which nothing rounds to bf16: Phi(v) + v phi(v) with
     the normal tail within 2^-21 and exp(-v^2 / 2) within 2^-22 of itself, three roundings on the way to v phi(v) (a

@@ -124,6 +124,17 @@ def test_all_tokens_on_one_expert_and_none():
     assert torch.equal(fq.fp4_moe(x, bank, none, torch.ones(16, 16, device="cuda")), torch.zeros_like(x))
 
 
+@pytest.mark.parametrize("m,experts,top", [(16, 16, 16), (16, 17, 16), (13, 16, 15), (4, 16, 16), (1, 16, 16), (9, 3, 3)])
+def test_every_token_on_nearly_every_expert(m, experts, top):
+    """Many tokens on each of many experts, in another order for each token."""
+    bank = bank_of(experts, 256, 256, 31)
+    x = tokens(m, 256, 32)
+    g = torch.Generator(device="cuda").manual_seed(33)
+    ids = torch.stack([torch.randperm(experts, generator=g, device="cuda")[:top] for _ in range(m)]).to(torch.int32).contiguous()
+    w = torch.rand(m, top, generator=g, device="cuda")
+    check(fq.fp4_moe(x, bank, ids, w), x, bank, ids, w)
+
+
 def test_the_same_expert_twice():
     bank = bank_of(4, 256, 256, 14)
     x = tokens(3, 256, 15)
